@@ -248,6 +248,174 @@ mfsdp_status mfsdp_owner_step_static(mfsdp_plan_t plan, const mfsdp_step_args* a
 /* Free a plan.  NULL is accepted. */
 mfsdp_status mfsdp_plan_destroy(mfsdp_plan_t plan);
 
+/* ---- Gradients of the owner buffer, between the backward pass and the step ----
+ *
+ * The global L2 norm of every gradient in the buffer, the norm of each
+ * tensor, and clipping to a largest norm:
+ *
+ *   sumsq = sum over entries and elements of g^2;  norm = sqrt(sumsq);
+ *   scale = min(1, max_norm / (norm + eps));       g <- scale * g.
+ *
+ * The owner holds whole tensors, so each of these is local to it; the
+ * global norm over several owners needs one 16-byte record from each
+ * (mfsdp_grad_total).  The clipped gradient is either written
+ * (mfsdp_grad_clip) or formed as the step reads it (mfsdp_owner_step_scaled,
+ * which moves no byte more than mfsdp_owner_step).  The scale stays on the
+ * device throughout: nothing here synchronises, and every call below can be
+ * captured into a graph once its descriptors are resident.
+ *
+ * Squares and sums are fp64 in a fixed order: results are bitwise the same
+ * from run to run, and no finite gradient overflows or vanishes in them.
+ * Non-finite gradients propagate by the formulas: a NaN makes norm and scale
+ * NaN; an Inf makes norm Inf and scale 0 (so the Inf itself becomes NaN).
+ * Bytes of the buffers that belong to no entry are neither read into a
+ * result nor written. */
+
+/* What mfsdp_grad_norm and mfsdp_grad_total write (device memory, 16-byte
+ * aligned; its scale field is what mfsdp_grad_clip and
+ * mfsdp_owner_step_scaled take). */
+typedef struct mfsdp_grad_stats {
+    double sumsq;             /* sum of squares */
+    float norm;               /* sqrt(sumsq), formed in fp64 and rounded once */
+    float scale;              /* min(1, max_norm/(norm + eps)), formed in fp64 and rounded once */
+} mfsdp_grad_stats;
+
+/* Device workspace of mfsdp_grad_norm and mfsdp_grad_clip on this plan's
+ * table (descriptors and partial sums; separate from the step's).  It may
+ * serve any number of calls, one at a time. */
+mfsdp_status mfsdp_plan_grad_workspace_bytes(mfsdp_plan_t plan, uint64_t* bytes);
+
+typedef struct mfsdp_grad_norm_args {
+    const void* grads;        /* device, read only; the plan's offsets; 16-byte aligned */
+    void* workspace;          /* device, mfsdp_plan_grad_workspace_bytes, 256-byte aligned; library
+                                 scratch: the caller must not write it between calls */
+    uint64_t workspace_bytes;
+    double max_norm;          /* > 0; INFINITY: scale is 1 whatever the norm */
+    double eps;               /* >= 0, finite */
+    mfsdp_grad_stats* stats;  /* device, written */
+    float* entry_norms;       /* NULL, or device fp32 [mfsdp_plan_num_entries]: the L2 norm of each
+                                 entry's gradient (0 for an empty entry), formed in fp64 and rounded once */
+    void* stream;             /* hipStream_t; NULL = the null stream */
+    uint32_t flags;           /* MFSDP_STEP_DESCRIPTORS_RESIDENT: an earlier mfsdp_grad_norm or
+                                 mfsdp_grad_clip of this plan already filled this workspace; skip the
+                                 upload.  Other bits must be 0. */
+} mfsdp_grad_norm_args;
+
+/* Enqueue the norm pass.  An empty table gives norm 0 and scale 1.
+ * Errors: INVALID_ARGUMENT (null pointer, misaligned buffer, max_norm or eps
+ * out of range, unknown flag), WORKSPACE_TOO_SMALL, UNSUPPORTED (a table of
+ * more than 2^31 - 1 work chunks), HIP. */
+mfsdp_status mfsdp_grad_norm(mfsdp_plan_t plan, const mfsdp_grad_norm_args* args);
+
+/* Join the records of several owners: stats->sumsq = the sum of parts[0..count)
+ * in that order (so every owner that holds the same records computes the same
+ * bits), and norm and scale from it.  parts: device, 16-byte aligned, each as
+ * mfsdp_grad_norm wrote it; only sumsq is read.  stats may be one of parts.
+ * Errors: INVALID_ARGUMENT (null or misaligned pointer, count outside
+ * 1..65536, max_norm or eps out of range), HIP. */
+mfsdp_status mfsdp_grad_total(const mfsdp_grad_stats* parts, int64_t count, double max_norm, double eps,
+                              mfsdp_grad_stats* stats, void* stream);
+
+typedef struct mfsdp_grad_clip_args {
+    const void* grads;        /* device, the plan's offsets; 16-byte aligned */
+    void* out;                /* device, the same offsets; grads itself (in place), or a buffer that
+                                 does not overlap it; 16-byte aligned */
+    const float* scale;       /* device, one value, 4-byte aligned */
+    void* workspace;          /* as in mfsdp_grad_norm_args */
+    uint64_t workspace_bytes;
+    void* stream;
+    uint32_t flags;           /* as in mfsdp_grad_norm_args */
+} mfsdp_grad_clip_args;
+
+/* Enqueue out <- scale * grads over every entry: the fp32 product rounded
+ * once to the entry's type.  A scale of exactly 1 leaves every bit: in place
+ * nothing is read or written then, else the entries are copied.
+ * Errors: INVALID_ARGUMENT (null pointer, misaligned buffer, buffers that
+ * overlap in part, unknown flag), WORKSPACE_TOO_SMALL, UNSUPPORTED, HIP. */
+mfsdp_status mfsdp_grad_clip(mfsdp_plan_t plan, const mfsdp_grad_clip_args* args);
+
+/* mfsdp_owner_step with every gradient multiplied by *grad_scale (device,
+ * fp32, 4-byte aligned) as it is read: g' = scale * g in fp32, unrounded to
+ * the storage type, takes the place of g in the Muon momentum and in AdamW.
+ * For fp32 gradients the result is bitwise that of mfsdp_grad_clip followed
+ * by mfsdp_owner_step; a scale of 1 gives bitwise mfsdp_owner_step.
+ * Errors: those of mfsdp_owner_step, plus INVALID_ARGUMENT (NULL or
+ * misaligned grad_scale). */
+mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* args, const float* grad_scale);
+
+/* ---- An embedding table of the owner buffer ----
+ *
+ * An embedding is a 2D tensor that trains with AdamW (role
+ * MFSDP_ROLE_ADAMW), held whole by its owner like any other entry: rows =
+ * vocabulary, cols = width.  These two calls read it where it lies in the
+ * owner's params and form its gradient where the step reads it:
+ *
+ *   lookup:  out[i][:] = scale * W[id_i - first_id][:];
+ *   grad:    G[v][:] (+)= scale * sum over i with id_i - first_id = v of dout[i][:].
+ *
+ * An id outside first_id .. first_id + rows - 1 has a zero row in the
+ * lookup and no part in the gradient: a vocabulary cut into several entries
+ * is looked up in each with its own first_id and the results added, and a
+ * negative id marks padding.  Sums are fp32, formed in an order that depends
+ * on the ids and sizes alone (bitwise the same from run to run, no atomics on
+ * values), multiplied by scale in fp32, and rounded once to the entry's
+ * type. */
+typedef enum mfsdp_id_type {
+    MFSDP_I32 = 0,
+    MFSDP_I64 = 1
+} mfsdp_id_type;
+
+typedef struct mfsdp_embed_lookup_args {
+    const void* params;       /* device, the owner's params buffer; 16-byte aligned */
+    const void* ids;          /* device, n_ids of id_type, aligned to their size */
+    int64_t n_ids;            /* 0 .. 2^30; 0: nothing is done */
+    int32_t id_type;          /* mfsdp_id_type */
+    int32_t out_type;         /* mfsdp_dtype of out */
+    int64_t first_id;         /* id of the table's row 0, 0 .. 2^62 */
+    void* out;                /* device, n_ids rows of cols elements, aligned to the element size */
+    int64_t out_stride;       /* elements from one row of out to the next, >= cols; 0 = cols */
+    float scale;
+    void* stream;
+} mfsdp_embed_lookup_args;
+
+/* Enqueue the lookup in entry `entry` of the plan (any role).  Elements of
+ * out between two rows are not touched.
+ * Errors: INVALID_ARGUMENT (null pointer, entry out of range, n_ids,
+ * first_id or out_stride out of range, misaligned buffer), UNSUPPORTED
+ * (id_type, out_type), HIP. */
+mfsdp_status mfsdp_embed_lookup(mfsdp_plan_t plan, int64_t entry, const mfsdp_embed_lookup_args* args);
+
+/* Device workspace of mfsdp_embed_grad for up to n_ids ids (it grows with
+ * n_ids; 0 ids need 0 bytes).  Errors: INVALID_ARGUMENT. */
+mfsdp_status mfsdp_plan_embed_workspace_bytes(mfsdp_plan_t plan, int64_t entry, int64_t n_ids, uint64_t* bytes);
+
+typedef struct mfsdp_embed_grad_args {
+    void* grads;              /* device, the owner's grads buffer; 16-byte aligned */
+    const void* ids;          /* as in mfsdp_embed_lookup_args */
+    int64_t n_ids;            /* 0 .. 2^30 */
+    int32_t id_type;
+    int32_t dout_type;        /* mfsdp_dtype of dout */
+    int64_t first_id;
+    const void* dout;         /* device, n_ids rows of cols elements, aligned to the element size; may be
+                                 NULL when n_ids is 0 */
+    int64_t dout_stride;      /* elements from one row of dout to the next, >= cols; 0 = cols */
+    float scale;
+    int32_t accumulate;       /* 0: every row of the entry's gradient is written, zeros where no id
+                                 points; 1: the sums are added to what is there, and rows without an id
+                                 are not touched */
+    void* workspace;          /* device, mfsdp_plan_embed_workspace_bytes, 256-byte aligned; written
+                                 before it is read, so it needs no clearing and may be shared by calls
+                                 that do not overlap; NULL where 0 bytes are needed */
+    uint64_t workspace_bytes;
+    void* stream;
+} mfsdp_embed_grad_args;
+
+/* Enqueue the gradient of entry `entry`.
+ * Errors: INVALID_ARGUMENT (null pointer, entry out of range, n_ids,
+ * first_id, dout_stride or accumulate out of range, misaligned buffer),
+ * UNSUPPORTED (id_type, dout_type), WORKSPACE_TOO_SMALL, HIP. */
+mfsdp_status mfsdp_embed_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_embed_grad_args* args);
+
 /* ---- Owner planner (host only) ----
  *
  * "MatrixFSDP" (arXiv 2607.05895), Abstract: a balance-aware owner planner

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libmfsdp.so")
 F32, BF16 = 0, 1
 ROLE_AUTO, ROLE_MUON, ROLE_ADAMW = 0, 1, 2
 STEP_DESCRIPTORS_RESIDENT = 1
+I32, I64 = 0, 1  # mfsdp_id_type
 STATIC_WORKSPACE_BYTES = 64 << 20  # MFSDP_STATIC_WORKSPACE_BYTES
 
 STATUS = {
@@ -89,10 +90,46 @@ class TensorPlace(ctypes.Structure):
                 ("cost", ctypes.c_double), ("mem_bytes", ctypes.c_uint64)]
 
 
+class GradStats(ctypes.Structure):
+    """mfsdp_grad_stats (16 bytes of device memory); SCALE_OFFSET is where its
+    scale lies, the address that grad_clip and step_scaled take."""
+    _fields_ = [("sumsq", ctypes.c_double), ("norm", ctypes.c_float), ("scale", ctypes.c_float)]
+    SCALE_OFFSET = 12
+
+
+class GradNormArgs(ctypes.Structure):
+    _fields_ = [("grads", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
+                ("max_norm", ctypes.c_double), ("eps", ctypes.c_double), ("stats", ctypes.c_void_p),
+                ("entry_norms", ctypes.c_void_p), ("stream", ctypes.c_void_p), ("flags", ctypes.c_uint32)]
+
+
+class GradClipArgs(ctypes.Structure):
+    _fields_ = [("grads", ctypes.c_void_p), ("out", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p),
+                ("flags", ctypes.c_uint32)]
+
+
+class EmbedLookupArgs(ctypes.Structure):
+    _fields_ = [("params", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("n_ids", ctypes.c_int64),
+                ("id_type", ctypes.c_int32), ("out_type", ctypes.c_int32), ("first_id", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("stream", ctypes.c_void_p)]
+
+
+class EmbedGradArgs(ctypes.Structure):
+    _fields_ = [("grads", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("n_ids", ctypes.c_int64),
+                ("id_type", ctypes.c_int32), ("dout_type", ctypes.c_int32), ("first_id", ctypes.c_int64),
+                ("dout", ctypes.c_void_p), ("dout_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("accumulate", ctypes.c_int32), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64),
+                ("stream", ctypes.c_void_p)]
+
+
 EXPORTS = (
     "mfsdp_plan_create", "mfsdp_plan_state_bytes", "mfsdp_plan_workspace_bytes", "mfsdp_plan_ns_out_elems",
     "mfsdp_plan_num_events", "mfsdp_plan_num_entries", "mfsdp_plan_entry_info", "mfsdp_plan_regions",
-    "mfsdp_owner_step", "mfsdp_owner_step_static", "mfsdp_plan_destroy",
+    "mfsdp_owner_step", "mfsdp_owner_step_static", "mfsdp_owner_step_scaled", "mfsdp_plan_destroy",
+    "mfsdp_plan_grad_workspace_bytes", "mfsdp_grad_norm", "mfsdp_grad_total", "mfsdp_grad_clip",
+    "mfsdp_plan_embed_workspace_bytes", "mfsdp_embed_lookup", "mfsdp_embed_grad",
     "mfsdp_owner_partition", "mfsdp_owner_gather", "mfsdp_owner_scatter", "mfsdp_status_string",
     "mfsdp_last_error_message", "mfsdp_probe_mfma_bf16", "mfsdp_probe_hbm",
 )
@@ -121,6 +158,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mfsdp_plan_regions.argtypes = [P, ctypes.POINTER(Region), ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
     lib.mfsdp_owner_step.argtypes = [P, ctypes.POINTER(StepArgs)]
     lib.mfsdp_owner_step_static.argtypes = [P, ctypes.POINTER(StepArgs)]
+    lib.mfsdp_owner_step_scaled.argtypes = [P, ctypes.POINTER(StepArgs), P]
+    lib.mfsdp_plan_grad_workspace_bytes.argtypes = [P, u64p]
+    lib.mfsdp_grad_norm.argtypes = [P, ctypes.POINTER(GradNormArgs)]
+    lib.mfsdp_grad_total.argtypes = [P, ctypes.c_int64, ctypes.c_double, ctypes.c_double, P, P]
+    lib.mfsdp_grad_clip.argtypes = [P, ctypes.POINTER(GradClipArgs)]
+    lib.mfsdp_plan_embed_workspace_bytes.argtypes = [P, ctypes.c_int64, ctypes.c_int64, u64p]
+    lib.mfsdp_embed_lookup.argtypes = [P, ctypes.c_int64, ctypes.POINTER(EmbedLookupArgs)]
+    lib.mfsdp_embed_grad.argtypes = [P, ctypes.c_int64, ctypes.POINTER(EmbedGradArgs)]
     lib.mfsdp_plan_destroy.argtypes = [P]
     lib.mfsdp_owner_partition.argtypes = [ctypes.POINTER(Tensor), ctypes.c_int64, ctypes.POINTER(PartitionParams),
                                           ctypes.POINTER(TensorPlace), ctypes.POINTER(ctypes.c_double), u64p, u64p]
@@ -256,6 +301,57 @@ class OwnerPlan:
                         ctypes.cast(ev, ctypes.POINTER(ctypes.c_void_p)) if ev is not None else None, len(events))
         _check(self._lib.mfsdp_owner_step_static(self._h, ctypes.byref(args)))
 
+    def step_scaled(self, params: int, grads: int, state: int, workspace: int, workspace_bytes: int, step: int,
+                    grad_scale: int, stream: int = 0, ns_out: int = 0, flags: int = 0,
+                    events: Sequence[int] = ()) -> None:
+        """mfsdp_owner_step_scaled: the step with every gradient times the
+        device float at grad_scale (a mfsdp_grad_stats' scale field)."""
+        ev = (ctypes.c_void_p * len(events))(*events) if events else None
+        args = StepArgs(params, grads, state, workspace, workspace_bytes, step, stream or None, ns_out or None, flags,
+                        ctypes.cast(ev, ctypes.POINTER(ctypes.c_void_p)) if ev is not None else None, len(events))
+        _check(self._lib.mfsdp_owner_step_scaled(self._h, ctypes.byref(args), grad_scale))
+
+    @property
+    def grad_workspace_bytes(self) -> int:
+        return self._u64(self._lib.mfsdp_plan_grad_workspace_bytes)
+
+    def grad_norm(self, grads: int, workspace: int, workspace_bytes: int, stats: int, max_norm: float = float("inf"),
+                  eps: float = 1e-6, entry_norms: int = 0, stream: int = 0, flags: int = 0) -> None:
+        """mfsdp_grad_norm: norm and clipping scale of the whole buffer into
+        the GradStats at `stats`, and each entry's norm into entry_norms."""
+        args = GradNormArgs(grads, workspace, workspace_bytes, max_norm, eps, stats, entry_norms, stream, flags)
+        _check(self._lib.mfsdp_grad_norm(self._h, ctypes.byref(args)))
+
+    def grad_clip(self, grads: int, out: int, scale: int, workspace: int, workspace_bytes: int, stream: int = 0,
+                  flags: int = 0) -> None:
+        """mfsdp_grad_clip: out <- (device float at scale) * grads; out may be
+        grads."""
+        args = GradClipArgs(grads, out, scale, workspace, workspace_bytes, stream, flags)
+        _check(self._lib.mfsdp_grad_clip(self._h, ctypes.byref(args)))
+
+    def embed_lookup(self, entry: int, params: int, ids: int, n_ids: int, out: int, id_type: int = I64,
+                     out_type: int = BF16, first_id: int = 0, out_stride: int = 0, scale: float = 1.0,
+                     stream: int = 0) -> None:
+        """mfsdp_embed_lookup: out[i] = scale * row (ids[i] - first_id) of the
+        entry in params, zeros for an id outside."""
+        args = EmbedLookupArgs(params, ids, n_ids, id_type, out_type, first_id, out, out_stride, scale, stream)
+        _check(self._lib.mfsdp_embed_lookup(self._h, entry, ctypes.byref(args)))
+
+    def embed_workspace_bytes(self, entry: int, n_ids: int) -> int:
+        v = ctypes.c_uint64()
+        _check(self._lib.mfsdp_plan_embed_workspace_bytes(self._h, entry, n_ids, ctypes.byref(v)))
+        return v.value
+
+    def embed_grad(self, entry: int, grads: int, ids: int, n_ids: int, dout: int, workspace: int = 0,
+                   workspace_bytes: int = 0, id_type: int = I64, dout_type: int = BF16, first_id: int = 0,
+                   dout_stride: int = 0, scale: float = 1.0, accumulate: bool = False, stream: int = 0) -> None:
+        """mfsdp_embed_grad: the entry's gradient in grads from the output
+        gradients dout of a lookup of ids (written, or added with
+        accumulate)."""
+        args = EmbedGradArgs(grads, ids, n_ids, id_type, dout_type, first_id, dout, dout_stride, scale,
+                             1 if accumulate else 0, workspace, workspace_bytes, stream)
+        _check(self._lib.mfsdp_embed_grad(self._h, entry, ctypes.byref(args)))
+
     def _ptrs(self, addrs):
         if addrs is None:
             return None
@@ -286,6 +382,13 @@ class OwnerPlan:
             self.close()
         except Exception:
             pass
+
+
+def grad_total(parts: int, count: int, stats: int, max_norm: float = float("inf"), eps: float = 1e-6,
+               stream: int = 0) -> None:
+    """mfsdp_grad_total: the norm and scale over `count` owners' GradStats
+    (device array at parts), summed in order, into the GradStats at stats."""
+    _check(load().mfsdp_grad_total(parts, count, max_norm, eps, stats, stream or None))
 
 
 @dataclass(frozen=True)

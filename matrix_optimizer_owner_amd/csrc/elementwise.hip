@@ -12,6 +12,7 @@
 //    no Newton-Schulz iterations.
 //  * k_adamw: AdamW for the tensors that are not matrices (Abstract).
 #include <cmath>
+#include <type_traits>
 
 #include "device_util.h"
 #include "kernels.h"
@@ -29,6 +30,7 @@ struct MomentumArgs {
     float* partials;
     float beta;
     int nesterov;
+    const float* gscale;  // SCALED kernels: the factor of every gradient
 };
 
 // Eight consecutive elements (fp32, or bf16 bits in uint16_t) of the
@@ -84,10 +86,14 @@ template <> struct Vec8<float> {
 // for a wide one (the thread owns the whole 8 x 8 block, so the transpose
 // costs nothing).  Padding elements get u = 0.  T is the Newton-Schulz
 // storage type, MT the momentum's (fp32, or bf16 rounded to nearest-even on
-// store; the update and u use the unrounded fp32 value).
-template <typename T, typename MT>
+// store; the update and u use the unrounded fp32 value).  SCALED: *gscale * g
+// takes the place of g, one fp32 product as the gradient is unpacked; a
+// kernel of its own, so the unscaled one stays as it was, bit for bit.
+template <typename T, typename MT, bool SCALED>
 __global__ __launch_bounds__(256) void k_momentum(MomentumArgs a) {
     __shared__ float red[4];
+    float gs = 1.f;
+    if constexpr (SCALED) gs = *a.gscale;
     const int blk = blockIdx.x;
     const int mi = upper_index(a.k1_begin, a.n_mat, blk);
     const MatDesc d = a.mats[mi];
@@ -142,6 +148,10 @@ __global__ __launch_bounds__(256) void k_momentum(MomentumArgs a) {
                 gv[0] = gf[i][0].x; gv[1] = gf[i][0].y; gv[2] = gf[i][0].z; gv[3] = gf[i][0].w;
                 gv[4] = gf[i][1].x; gv[5] = gf[i][1].y; gv[6] = gf[i][1].z; gv[7] = gf[i][1].w;
             }
+            if constexpr (SCALED) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) gv[k] *= gs;
+            }
             float mv[8];
             Raw8<MT>::get(mf[i], mv);
 #pragma unroll
@@ -162,7 +172,8 @@ __global__ __launch_bounds__(256) void k_momentum(MomentumArgs a) {
                 u[i][k] = 0.f;
                 if (r < R && c0 + k < C) {
                     const int64_t idx = int64_t(r) * C + c0 + k;
-                    const float gk = load_elem(g, d.dtype, idx);
+                    float gk = load_elem(g, d.dtype, idx);
+                    if constexpr (SCALED) gk *= gs;
                     const float mk = __builtin_fmaf(a.beta, load_elem(mom, mdt, idx), gk);
                     store_elem(mom, mdt, idx, mk);
                     u[i][k] = a.nesterov ? __builtin_fmaf(a.beta, mk, gk) : mk;
@@ -258,6 +269,7 @@ struct AdamArgs {
     float b1, b2, omb1, omb2;  // betas and 1 - betas
     float inv_bc1, inv_bc2;    // 1/(1 - beta^t)
     float lr, lrwd, eps;
+    const float* gscale;       // SCALED kernel: the factor of every gradient
 };
 
 // Eight consecutive parameter / gradient elements (fp32, or bf16 rounded to
@@ -288,9 +300,12 @@ __device__ __forceinline__ void adamw_elem(const AdamArgs& a, float gv, float& w
 // each thread owns 8 consecutive elements, read and written as 16-byte
 // vectors (tensor offsets are 16-byte aligned, the moments 256-byte
 // aligned, chunk starts a multiple of 2048 elements), the tensor's last
-// partial group element by element.
+// partial group element by element.  SCALED as in k_momentum.
+template <bool SCALED>
 __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
     static_assert(kTailChunk == 256 * 8, "eight elements per thread");
+    float gs = 1.f;
+    if constexpr (SCALED) gs = *a.gscale;
     const int chunk = blockIdx.x;
     const int ti = upper_index(a.tail_begin, a.n_tail, chunk);
     const TailDesc t = a.tails[ti];
@@ -308,14 +323,19 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
         load8(reinterpret_cast<const uint8_t*>(m1), kF32, i0, mv);
         load8(reinterpret_cast<const uint8_t*>(m2), kF32, i0, vv);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) adamw_elem(a, gv[k], wv[k], mv[k], vv[k]);
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (SCALED) gv[k] *= gs;
+            adamw_elem(a, gv[k], wv[k], mv[k], vv[k]);
+        }
         store8(reinterpret_cast<uint8_t*>(m1), kF32, i0, mv);
         store8(reinterpret_cast<uint8_t*>(m2), kF32, i0, vv);
         store8(w, t.dtype, i0, wv);
     } else {
         for (int64_t i = i0; i < end; ++i) {
             float wv = load_elem(w, t.dtype, i), m = m1[i], v = m2[i];
-            adamw_elem(a, load_elem(g, t.dtype, i), wv, m, v);
+            float gv = load_elem(g, t.dtype, i);
+            if constexpr (SCALED) gv *= gs;
+            adamw_elem(a, gv, wv, m, v);
             m1[i] = m;
             m2[i] = v;
             store_elem(w, t.dtype, i, wv);
@@ -337,18 +357,27 @@ hipError_t launch_momentum(int ns_precision, const WorkspaceMap& map, const mfsd
     a.partials = reinterpret_cast<float*>(b.ws + map.off_partials);
     a.beta = hp.momentum;
     a.nesterov = hp.nesterov;
+    a.gscale = b.grad_scale;
     const bool mbf = hp.momentum_dtype == kBF16;
-    if (ns_precision == 1) {
-        if (mbf)
-            k_momentum<float, uint16_t><<<dim3(map.n_k1_blocks), dim3(256), 0, stream>>>(a);
-        else
-            k_momentum<float, float><<<dim3(map.n_k1_blocks), dim3(256), 0, stream>>>(a);
-    } else {
-        if (mbf)
-            k_momentum<uint16_t, uint16_t><<<dim3(map.n_k1_blocks), dim3(256), 0, stream>>>(a);
-        else
-            k_momentum<uint16_t, float><<<dim3(map.n_k1_blocks), dim3(256), 0, stream>>>(a);
-    }
+    const dim3 grid(map.n_k1_blocks), block(256);
+    auto launch = [&](auto scaled) {
+        constexpr bool S = decltype(scaled)::value;
+        if (ns_precision == 1) {
+            if (mbf)
+                k_momentum<float, uint16_t, S><<<grid, block, 0, stream>>>(a);
+            else
+                k_momentum<float, float, S><<<grid, block, 0, stream>>>(a);
+        } else {
+            if (mbf)
+                k_momentum<uint16_t, uint16_t, S><<<grid, block, 0, stream>>>(a);
+            else
+                k_momentum<uint16_t, float, S><<<grid, block, 0, stream>>>(a);
+        }
+    };
+    if (a.gscale)
+        launch(std::true_type{});
+    else
+        launch(std::false_type{});
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_norm_finalize<<<dim3(map.n_mat), dim3(256), 0, stream>>>(
@@ -393,7 +422,11 @@ hipError_t launch_adamw(const WorkspaceMap& map, const mfsdp_hparams& hp, int64_
     a.lr = hp.adam_lr;
     a.lrwd = float(double(hp.adam_lr) * double(hp.adam_weight_decay));
     a.eps = hp.adam_eps;
-    k_adamw<<<dim3(map.n_tail_chunks), dim3(256), 0, stream>>>(a);
+    a.gscale = b.grad_scale;
+    if (a.gscale)
+        k_adamw<true><<<dim3(map.n_tail_chunks), dim3(256), 0, stream>>>(a);
+    else
+        k_adamw<false><<<dim3(map.n_tail_chunks), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
 }
 

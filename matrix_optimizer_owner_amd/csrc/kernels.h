@@ -14,6 +14,7 @@ struct StepBuffers {
     uint8_t* state;
     uint8_t* ws;
     float* ns_out;
+    const float* grad_scale;  // NULL, or a device factor of every gradient
 };
 
 // Momentum / Nesterov / cast / orient, with Frobenius partial sums, then the

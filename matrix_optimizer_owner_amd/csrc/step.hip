@@ -43,7 +43,9 @@ mfsdp_status check_args(mfsdp_plan_t plan, const mfsdp_step_args* args) {
 }
 
 // The launch sequence of one step over workspace `ws` (checked by the caller).
-mfsdp_status enqueue_step(mfsdp_plan_t plan, const mfsdp_step_args* args, uint8_t* ws, bool upload) {
+// grad_scale: NULL, or the device factor of every gradient.
+mfsdp_status enqueue_step(mfsdp_plan_t plan, const mfsdp_step_args* args, uint8_t* ws, bool upload,
+                          const float* grad_scale) {
     const WorkspaceMap& map = plan->map;
     hipStream_t stream = static_cast<hipStream_t>(args->stream);
     StepBuffers b;
@@ -52,6 +54,7 @@ mfsdp_status enqueue_step(mfsdp_plan_t plan, const mfsdp_step_args* args, uint8_
     b.state = static_cast<uint8_t*>(args->state);
     b.ws = ws;
     b.ns_out = args->ns_out;
+    b.grad_scale = grad_scale;
 
     hipError_t e;
     auto mark = [&](uint32_t k) -> hipError_t {
@@ -106,11 +109,8 @@ std::mutex g_static_mu;
 void* g_static_ptr[kMaxDevices] = {};           // device address of `scratch` per device
 uint64_t g_static_last_plan[kMaxDevices] = {};  // plan whose descriptors the array holds (0: none)
 
-}  // namespace
-
-extern "C" mfsdp_status mfsdp_owner_step(mfsdp_plan_t plan, const mfsdp_step_args* args) {
-    clear_error();
-    if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
+// The step on the caller's workspace, for both entry points.
+mfsdp_status step_on_caller_workspace(mfsdp_plan_t plan, const mfsdp_step_args* args, const float* grad_scale) {
     const WorkspaceMap& map = plan->map;
     if (map.n_mat == 0 && map.n_tail == 0) return MFSDP_OK;  // nothing but empty shards
     if (mfsdp_status st = check_args(plan, args); st != MFSDP_OK) return st;
@@ -122,7 +122,24 @@ extern "C" mfsdp_status mfsdp_owner_step(mfsdp_plan_t plan, const mfsdp_step_arg
                     "workspace has " + std::to_string(args->workspace_bytes) + " bytes, plan needs " +
                         std::to_string(map.total_bytes));
     return enqueue_step(plan, args, static_cast<uint8_t*>(args->workspace),
-                        !(args->flags & MFSDP_STEP_DESCRIPTORS_RESIDENT));
+                        !(args->flags & MFSDP_STEP_DESCRIPTORS_RESIDENT), grad_scale);
+}
+
+}  // namespace
+
+extern "C" mfsdp_status mfsdp_owner_step(mfsdp_plan_t plan, const mfsdp_step_args* args) {
+    clear_error();
+    if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
+    return step_on_caller_workspace(plan, args, nullptr);
+}
+
+extern "C" mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* args,
+                                                const float* grad_scale) {
+    clear_error();
+    if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
+    if (!grad_scale || reinterpret_cast<uintptr_t>(grad_scale) % 4 != 0)
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "grad_scale is NULL or not 4-byte aligned");
+    return step_on_caller_workspace(plan, args, grad_scale);
 }
 
 extern "C" mfsdp_status mfsdp_owner_step_static(mfsdp_plan_t plan, const mfsdp_step_args* args) {
@@ -158,5 +175,5 @@ extern "C" mfsdp_status mfsdp_owner_step_static(mfsdp_plan_t plan, const mfsdp_s
         upload = !((args->flags & MFSDP_STEP_DESCRIPTORS_RESIDENT) && g_static_last_plan[dev] == plan->id);
         g_static_last_plan[dev] = plan->id;
     }
-    return enqueue_step(plan, args, ws, upload);
+    return enqueue_step(plan, args, ws, upload, nullptr);
 }
