@@ -2,8 +2,12 @@
 // lowering (grad_plan.cpp) and the kernels (grad.hip).
 //
 // Workspace map (byte offsets, 256-byte aligned):
-//   [desc]      GradChunk[n_chunks], int32 entry_begin[n_entries + 1]
-//   [partials]  double[n_chunks]: sum of g^2 of one chunk
+//   [desc]      GradRun[n_chunks] (clipping), GradRun[n_pieces] and int32
+//               block_begin[n_blocks + 1], entry_begin[n_entries + 1] and
+//               large[n_large] (norm), and the norm's counters of finished
+//               blocks (0 between calls): kNormGroups + 1 uint32 at a pitch of
+//               kNormCounterPitch
+//   [partials]  double[n_pieces]: sum of g^2 of one piece
 #pragma once
 #include <stdint.h>
 
@@ -11,26 +15,47 @@
 
 namespace mfsdp {
 
-// A run of one entry's elements, the work of one block.  Its first byte is
-// 16-byte aligned: entry offsets are, and a chunk starts a multiple of the
-// chunk length (a power of two of at least 1024 elements) into its entry.
-struct GradChunk {
+// A run of one entry's elements.  Its first byte is 16-byte aligned: entry
+// offsets are, and a run starts a multiple of kGradSlice into its entry.
+struct GradRun {
     uint64_t off;      // bytes into params / grads
-    uint32_t numel;    // 1 .. chunk length
+    uint64_t numel;    // at least 1
     int32_t dtype;
+    int32_t pad_;
 };
-static_assert(sizeof(GradChunk) == 16, "GradChunk layout");
+static_assert(sizeof(GradRun) == 24, "GradRun layout");
 
 struct GradTables {
     std::vector<uint8_t> blob;  // [desc], uploaded by one copy
-    uint64_t off_entry_begin = 0, off_partials = 0, total_bytes = 0;
-    int32_t n_chunks = 0, n_entries = 0;
+    uint64_t off_pieces = 0, off_block_begin = 0, off_entry_begin = 0, off_large = 0, off_counters = 0,
+             off_partials = 0;
+    uint64_t total_bytes = 0;
+    int32_t n_entries = 0;
+    // Clipping: chunk c is 2^slice_shift slices of kGradSlice bytes (its last
+    // ones may be empty), one slice a block.
+    int32_t n_chunks = 0, slice_shift = 0;
+    // The norm: block b sums pieces block_begin[b] .. block_begin[b+1]-1, which
+    // cut the table into n_blocks shares of the same cost (a piece ends where
+    // its share or its entry does).  Entry e is pieces entry_begin[e] ..
+    // entry_begin[e+1]-1; `large` are the entries of more than kNormFew.
+    int32_t n_pieces = 0, n_blocks = 0, n_large = 0;
 };
 
-// Chunk lengths: the smallest power of two from kGradChunkMin to
-// kGradChunkMax that cuts the table into at most kGradChunks chunks.
-constexpr int64_t kGradChunkMin = 4096;
-constexpr int64_t kGradChunkMax = int64_t(1) << 24;
+constexpr int64_t kGradSlice = 8192;
+// A chunk is the smallest power of two of bytes that cuts the table into at
+// most kGradChunks chunks: short enough not to leave many empty slices
+// behind small tensors, few enough for a short list.
 constexpr int64_t kGradChunks = 16384;
+constexpr int64_t kGradChunkMax = int64_t(1) << 30;
+// The norm's shares.  Cost counts slices, and kNormPieceCost more for each
+// piece (about what its descriptor, its sum and its drained loads take), so
+// that many small tensors spread over more blocks.  One share for every
+// kNormShareMin of cost, at most kNormBlocks.
+constexpr int64_t kNormPieceCost = 2;
+constexpr int64_t kNormShareMin = 4;
+constexpr int64_t kNormBlocks = 1024;
+constexpr int kNormFew = 8;
+constexpr uint32_t kNormGroups = 32;
+constexpr uint32_t kNormCounterPitch = 64;  // 256 bytes: no two share a cache line
 
 }  // namespace mfsdp
