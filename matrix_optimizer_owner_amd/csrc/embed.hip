@@ -3,6 +3,7 @@
 //
 //   lookup:  out[i] = scale * W[id_i - first];
 //   grad:    G[v] (+)= scale * sum over i with id_i - first = v of dout[i].
+#include <algorithm>
 #include <string>
 
 #include "device_util.h"
@@ -11,76 +12,626 @@
 namespace mfsdp {
 namespace {
 
-constexpr int kEmbedThreads = 256;
+// ---- ids and elements ----
 
-// Row of position i, or -1 for an id outside the table.  The difference is
+// Row of position i, or `rows` for an id outside the table.  The difference is
 // taken modulo 2^64: first is at most 2^62, so no id outside wraps into it.
-__device__ __forceinline__ int64_t row_of(const void* ids, int id_type, int64_t i, int64_t first, int64_t rows) {
+__device__ __forceinline__ int row_of(const void* ids, int id_type, int64_t i, int64_t first, int rows) {
     const int64_t id = id_type == MFSDP_I64 ? static_cast<const int64_t*>(ids)[i] : static_cast<const int32_t*>(ids)[i];
     const uint64_t r = uint64_t(id) - uint64_t(first);
-    return r < uint64_t(rows) ? int64_t(r) : -1;
+    return r < uint64_t(rows) ? int(r) : rows;
 }
+
+// A 16-byte word at any element address: rows of an odd width start anywhere,
+// and global accesses of this width need no alignment here.
+typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(2)));
+
+// N consecutive elements of type DT as the words they are stored in.
+template <int DT, int N> struct Raw {
+    static constexpr int kWords = N * (DT == kBF16 ? 2 : 4) / 16;
+    static constexpr int kSize = DT == kBF16 ? 2 : 4;
+    u32x4_t w[kWords];
+    // the first `width` of N elements at p (elements); nothing behind them is read
+    template <bool STREAM> __device__ __forceinline__ void load(const void* p, int width) {
+        if (width == N) {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                const word_t* q = static_cast<const word_t*>(p) + k;
+                w[k] = STREAM ? __builtin_nontemporal_load(q) : *q;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                uint32_t v = 0;
+                if (k < width) v = DT == kBF16 ? uint32_t(static_cast<const uint16_t*>(p)[k]) : static_cast<const uint32_t*>(p)[k];
+                if (DT == kBF16)
+                    w[k / 8][k / 2 % 4] = k % 2 ? w[k / 8][k / 2 % 4] | v << 16 : v;
+                else
+                    w[k / 4][k % 4] = v;
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int k) const {
+        if (DT == kBF16) {
+            const uint32_t x = w[k / 8][k / 2 % 4];
+            return __uint_as_float(k % 2 ? x & 0xffff0000u : x << 16);
+        }
+        return __uint_as_float(w[k / 4][k % 4]);
+    }
+};
+
+// N floats rounded once and stored as `width` elements of type DT.
+template <int DT, int N, bool STREAM> __device__ __forceinline__ void store(void* p, int width, const float (&v)[N]) {
+    if (width == N) {
+        constexpr int kWords = Raw<DT, N>::kWords;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            u32x4_t w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = DT == kBF16 ? pack_bf16x2(v[(k * 8 + 2 * e) % N], v[(k * 8 + 2 * e + 1) % N])
+                                   : __float_as_uint(v[(k * 4 + e) % N]);
+            word_t* q = static_cast<word_t*>(p) + k;
+            if (STREAM)
+                __builtin_nontemporal_store(w, q);
+            else
+                *q = w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < width) store_elem(p, DT, k, v[k]);
+    }
+}
+
+// ---- lookup ----
+
+constexpr int kLookupThreads = 256;
+constexpr int64_t kBlocksMax = (int64_t(1) << 23) - 1;  // a launch holds fewer than 2^32 threads
 
 struct LookupArgs {
-    const void* table;
+    const uint8_t* table;
     const void* ids;
-    void* out;
-    int64_t rows, cols, first, out_stride;
-    int table_type, id_type, out_type;
+    uint8_t* out;
+    int64_t n, first, out_stride;
+    int rows, cols;
+    int id_type;
+    int group_shift;  // 2^group_shift lanes a row; grid.y such groups side by side
     float scale;
 };
 
-__global__ __launch_bounds__(kEmbedThreads) void k_embed_lookup(LookupArgs a) {
-    const int64_t i = blockIdx.x;
-    const int64_t r = row_of(a.ids, a.id_type, i, a.first, a.rows);
-    for (int64_t c = threadIdx.x; c < a.cols; c += kEmbedThreads) {
-        const float v = r < 0 ? 0.f : a.scale * load_elem(a.table, a.table_type, r * a.cols + c);
-        store_elem(a.out, a.out_type, i * a.out_stride + c, v);
+// HBM-bound: each id's row is read and written once.  One word of the
+// narrower type a thread and no loop, the shape that copies fastest here
+// (grad.hip); 2^group_shift lanes share a position, so narrow rows fill the
+// wave too.  first_block: the launch's first block.
+template <int TD, int OD>
+__global__ __launch_bounds__(kLookupThreads) void k_embed_lookup(LookupArgs a, int64_t first_block) {
+    constexpr int N = TD == kF32 && OD == kF32 ? 4 : 8;
+    const int64_t i = (first_block + blockIdx.x) * (kLookupThreads >> a.group_shift) + (threadIdx.x >> a.group_shift);
+    const int lane = int(threadIdx.x) & ((1 << a.group_shift) - 1);
+    const int c = ((int(blockIdx.y) << a.group_shift) + lane) * N;
+    if (i >= a.n || c >= a.cols) return;
+    const int r = row_of(a.ids, a.id_type, i, a.first, a.rows);
+    const int width = a.cols - c < N ? a.cols - c : N;
+    float v[N];
+    if (r < a.rows) {
+        Raw<TD, N> x;
+        x.template load<false>(a.table + (int64_t(r) * a.cols + c) * Raw<TD, N>::kSize, width);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = a.scale * x.get(k);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = 0.f;
+    }
+    store<OD, N, false>(a.out + (i * a.out_stride + c) * Raw<OD, N>::kSize, width, v);
+}
+
+// ---- gradient ----
+//
+// grad[v] (+)= scale * sum of dout[i] over the positions i of row v: fp32 sums
+// in the order of the positions, cut at places that depend on the ids and
+// sizes alone.  HBM-bound: dout is read once and every row written once.
+
+struct GradArgs {
+    uint8_t* grad;
+    const void* ids;
+    const uint8_t* dout;
+    int64_t first, dout_stride;
+    int rows, cols, n;
+    int id_type;
+    int group_shift, slabs;  // 2^group_shift lanes a row, `slabs` of them side by side
+    float scale;
+};
+
+constexpr int kPer = 8;  // columns of a lane
+
+template <int GD, bool ACC>
+__device__ __forceinline__ void write_row(const GradArgs& a, int row, int c, int width, const float (&sum)[kPer]) {
+    uint8_t* p = a.grad + (int64_t(row) * a.cols + c) * Raw<GD, kPer>::kSize;
+    float v[kPer];
+    if constexpr (ACC) {
+        Raw<GD, kPer> old;
+        old.template load<false>(p, width);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = __builtin_fmaf(a.scale, sum[k], old.get(k));
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[k] = a.scale * sum[k];
+    }
+    store<GD, kPer, false>(p, width, v);
+}
+
+// The sum of dout rows list[0..count), columns c .. c + width, kUnroll loads in flight.
+template <int OD>
+__device__ __forceinline__ void sum_rows(const GradArgs& a, const int* list, int count, int c, int width, float (&acc)[kPer]) {
+    constexpr int kUnroll = 8;
+    for (int q = 0; q < count; q += kUnroll) {
+        Raw<OD, kPer> x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (q + u < count)
+                x[u].template load<true>(a.dout + (int64_t(list[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (q + u < count)
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc[k] += x[u].get(k);
     }
 }
 
-struct GradArgs {
-    void* grad;
-    const void* ids;
-    const void* dout;
-    int64_t rows, cols, first, dout_stride;
-    int n, grad_type, id_type, dout_type, accumulate;
-    float scale;
+// Every thread's acc of a block of THREADS, added over its groups in their
+// order; valid in group 0.
+template <int THREADS> __device__ __forceinline__ void add_groups(float* red, int group_shift, float (&acc)[kPer]) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) red[k * THREADS + threadIdx.x] = acc[k];
+    __syncthreads();
+    if ((threadIdx.x >> group_shift) != 0) return;
+    for (int g = 1; g < (THREADS >> group_shift); ++g)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] += red[k * THREADS + (g << group_shift) + threadIdx.x];
+}
+
+// Zeros over the whole table's gradient: one word a thread, the shape that
+// writes fastest here (6.9 TB/s; 5.9 with 128 KB a block).
+constexpr int kZeroThreads = 256;
+__global__ __launch_bounds__(kZeroThreads) void k_embed_zero(uint8_t* grad, int64_t bytes, int64_t first_block) {
+    const int64_t at = ((first_block + blockIdx.x) * kZeroThreads + threadIdx.x) * 16;
+    if (at + 16 <= bytes)
+        *reinterpret_cast<u32x4_t*>(grad + at) = u32x4_t{0u, 0u, 0u, 0u};
+    else
+        for (int64_t b = at; b < bytes; b += 2) *reinterpret_cast<uint16_t*>(grad + b) = 0;
+}
+
+// Few ids: the block of position i looks through all of them, ends if an
+// earlier one has the same row, and else sums that row's positions in order.
+// No sort and no workspace; the work grows with n^2, so only up to kFewIds.
+constexpr int kFewThreads = 256, kFewWaves = kFewThreads / 64, kFewRounds = 8;
+constexpr int kFewIds = kFewThreads * kFewRounds;
+
+template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) void k_embed_few(GradArgs a) {
+    __shared__ int list[kFewIds];
+    __shared__ int wave_first[kFewWaves], wave_n[kFewWaves];
+    __shared__ float red[kFewThreads * kPer];
+    const int i = int(blockIdx.x), slab = int(blockIdx.y);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = row_of(a.ids, a.id_type, i, a.first, a.rows);
+    if (row == a.rows) return;
+    // wave w has the positions from w * rounds * 64 on, in order
+    const int rounds = (a.n + kFewThreads - 1) / kFewThreads;
+    uint64_t hits[kFewRounds];
+    int found = 0, first = INT32_MAX;
+#pragma unroll
+    for (int k = 0; k < kFewRounds; ++k) {
+        const int p = (wave * rounds + k) * 64 + lane;
+        hits[k] = __ballot(k < rounds && p < a.n && row_of(a.ids, a.id_type, k < rounds && p < a.n ? p : 0, a.first, a.rows) == row);
+        if (hits[k] && first == INT32_MAX) first = p - lane + __builtin_ctzll(hits[k]);
+        found += __popcll(hits[k]);
+    }
+    if (lane == 0) {
+        wave_first[wave] = first;
+        wave_n[wave] = found;
+    }
+    __syncthreads();
+    int at = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+        if (wave_first[w] < i) return;  // an earlier position's block has this row
+        at += w < wave ? wave_n[w] : 0;
+        total += wave_n[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kFewRounds; ++k) {
+        if (hits[k] >> lane & 1) list[at + __popcll(hits[k] & ((uint64_t(1) << lane) - 1))] = (wave * rounds + k) * 64 + lane;
+        at += __popcll(hits[k]);
+    }
+    __syncthreads();
+    const int g = threadIdx.x >> a.group_shift, groups = kFewThreads >> a.group_shift;
+    const int c = ((slab << a.group_shift) + (int(threadIdx.x) & ((1 << a.group_shift) - 1))) * kPer;
+    const int width = a.cols - c < kPer ? a.cols - c : kPer;
+    float acc[kPer] = {};
+    if (total <= 8) {  // one group has them all in flight at once
+        if (g == 0 && width > 0) {
+            sum_rows<OD>(a, list, total, c, width, acc);
+            write_row<GD, ACC>(a, row, c, width, acc);
+        }
+        return;
+    }
+    const int share = (total + groups - 1) / groups, lo = g * share;
+    if (width > 0 && lo < total) sum_rows<OD>(a, list + lo, total - lo < share ? total - lo : share, c, width, acc);
+    add_groups<kFewThreads>(red, a.group_shift, acc);
+    if (g == 0 && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
+}
+
+// ---- many ids: sort positions by row, then sum runs of the sorted order ----
+//
+// The sort is a stable radix sort of (row, position) in two passes over about
+// half of the row's bits each: per pass one launch counts each tile's digits
+// and one ranks and scatters.  Ids outside the table sort last, as row `rows`.
+
+constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
+
+struct SortArgs {
+    const void* ids;          // first pass; else keys_in and pos_in
+    int64_t first;
+    int rows, n, id_type;
+    int tile, n_tiles;        // positions of a block, a multiple of kSortThreads
+    int shift, bits;          // the pass's digit
+    const int *keys_in, *pos_in;
+    int* hist;                // [n_tiles][2^bits]
+    int *keys_out, *pos_out;
+    uint8_t* flags;           // [rows]: whether a position has the row; NULL when nothing is zero-filled
 };
 
-// One block per table row: it finds the row's positions in order, and sums.
-__global__ __launch_bounds__(kEmbedThreads) void k_embed_grad(GradArgs a) {
-    __shared__ int list[kEmbedThreads];
-    __shared__ int wave_n[kEmbedThreads / 64];
-    const int64_t v = blockIdx.x;
+template <bool FIRST> __device__ __forceinline__ int sort_key(const SortArgs& a, int p) {
+    return FIRST ? row_of(a.ids, a.id_type, p, a.first, a.rows) : a.keys_in[p];
+}
+
+template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a) {
+    extern __shared__ int count[];
+    const int bins = 1 << a.bits;
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) count[d] = 0;
+    if (FIRST && a.flags) {
+        // words of four flags (the region is padded to 256 bytes)
+        for (int w = blockIdx.x * kSortThreads + threadIdx.x; w < (a.rows + 3) / 4; w += gridDim.x * kSortThreads)
+            reinterpret_cast<uint32_t*>(a.flags)[w] = 0;
+    }
+    __syncthreads();
+    const int lo = blockIdx.x * a.tile, hi = a.n - lo < a.tile ? a.n : lo + a.tile;
+    for (int p = lo + threadIdx.x; p < hi; p += kSortThreads) atomicAdd(&count[sort_key<FIRST>(a, p) >> a.shift & (bins - 1)], 1);
+    __syncthreads();
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) a.hist[int64_t(blockIdx.x) * bins + d] = count[d];
+}
+
+// Exclusive sum of v over the block; `sum` receives the total.
+__device__ __forceinline__ int block_scan(int v, int* red, int& sum) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t c0 = 0; c0 < a.cols; c0 += kEmbedThreads) {
-        const int64_t c = c0 + threadIdx.x;
-        float acc = 0.f;
-        bool any = false;
-        for (int base = 0; base < a.n; base += kEmbedThreads) {
-            const int i = base + int(threadIdx.x);
-            const bool hit = i < a.n && row_of(a.ids, a.id_type, i, a.first, a.rows) == v;
-            const uint64_t m = __ballot(hit);
-            if (lane == 0) wave_n[wave] = __popcll(m);
-            __syncthreads();
-            int at = __popcll(m & ((uint64_t(1) << lane) - 1)), total = 0;
-            for (int w = 0; w < kEmbedThreads / 64; ++w) {
-                if (w < wave) at += wave_n[w];
-                total += wave_n[w];
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int y = __shfl_up(x, off, 64);
+        if (lane >= off) x += y;
+    }
+    if (lane == 63) red[wave] = x;
+    __syncthreads();
+    int before = 0;
+    sum = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) before += red[w];
+        sum += red[w];
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
+// One tile of a pass.  Wave w of the block has a contiguous eighth of the
+// tile; a key's place is the number of smaller digits, then of equal digits
+// in earlier tiles, earlier waves, earlier rounds and lower lanes: stable.
+template <bool FIRST> __device__ __forceinline__ void sort_scatter(const SortArgs& a, int tile, int* cnt) {
+    __shared__ int red[kSortWaves];
+    const int bins = 1 << a.bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int d = threadIdx.x; d < kSortWaves * bins; d += kSortThreads) cnt[d] = 0;
+    __syncthreads();
+    const int part = a.tile / kSortWaves, lo = tile * a.tile + wave * part;
+    int* mine = cnt + wave * bins;
+    for (int r = 0; r < part; r += 64) {
+        const int p = lo + r + lane;
+        if (p < a.n) atomicAdd(&mine[sort_key<FIRST>(a, p) >> a.shift & (bins - 1)], 1);
+    }
+    __syncthreads();
+    int carry = 0;
+    for (int d0 = 0; d0 < bins; d0 += kSortThreads) {
+        const int d = d0 + int(threadIdx.x);
+        int before = 0, total = 0;
+        if (d < bins) {
+            constexpr int kUnroll = 16;
+            for (int t0 = 0; t0 < a.n_tiles; t0 += kUnroll) {
+                int h[kUnroll];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) h[u] = t0 + u < a.n_tiles ? a.hist[int64_t(t0 + u) * bins + d] : 0;
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    total += h[u];
+                    before += t0 + u < tile ? h[u] : 0;
+                }
             }
-            if (hit) list[at] = i;
-            __syncthreads();
-            any = any || total > 0;
-            if (c < a.cols)
-                for (int k = 0; k < total; ++k) acc += load_elem(a.dout, a.dout_type, int64_t(list[k]) * a.dout_stride + c);
-            __syncthreads();
         }
-        if (c < a.cols && (any || !a.accumulate)) {
-            const float old = a.accumulate ? load_elem(a.grad, a.grad_type, v * a.cols + c) : 0.f;
-            store_elem(a.grad, a.grad_type, v * a.cols + c, __builtin_fmaf(a.scale, acc, old));
+        int sum;
+        int at = carry + block_scan(total, red, sum) + before;
+        carry += sum;
+        if (d < bins)
+            for (int w = 0; w < kSortWaves; ++w) {
+                const int c = cnt[w * bins + d];
+                cnt[w * bins + d] = at;
+                at += c;
+            }
+    }
+    __syncthreads();
+    volatile int* place = mine;
+    for (int r = 0; r < part; r += 64) {
+        const int p = lo + r + lane;
+        const bool live = p < a.n;
+        const int key = live ? sort_key<FIRST>(a, p) : 0;
+        const int digit = key >> a.shift & (bins - 1);
+        uint64_t same = __ballot(live);
+        for (int b = 0; b < a.bits; ++b) {
+            const uint64_t m = __ballot(digit >> b & 1);
+            same &= digit >> b & 1 ? m : ~m;
+        }
+        if (live) {
+            const int at = place[digit], rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+            __builtin_amdgcn_wave_barrier();  // every lane has read its place before the first of them moves it on
+            if (rank == 0) place[digit] = at + __popcll(same);
+            a.keys_out[at + rank] = key;
+            a.pos_out[at + rank] = FIRST ? p : a.pos_in[p];
+            if (FIRST && a.flags && key < a.rows) a.flags[key] = 1;  // the same value by every writer
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_first(SortArgs a) {
+    extern __shared__ int cnt[];
+    sort_scatter<true>(a, blockIdx.x, cnt);
+}
+
+// Zeros in the rows that no position has.  A block has `rows` whole rows of
+// at most 512 words, or a piece of 512 words of one longer row; a word that
+// two rows share is the first one's.
+struct FillArgs {
+    uint8_t* grad;
+    const uint8_t* flags;
+    int rows, cols, type;
+    int span;                // rows of a block
+    int pieces;              // blocks of a row, when span is 1
+    uint32_t inv_cols;       // ceil(2^32 / cols)
+    int64_t n_blocks;
+};
+
+__device__ __forceinline__ void fill_zeros(const FillArgs& a, int64_t block) {
+    const int per = a.type == kBF16 ? 8 : 4, es = 16 / per;
+    const int g = a.pieces == 1 ? int(block) : int(block / a.pieces), piece = int(block - int64_t(g) * a.pieces);
+    const int r0 = g * a.span, r1 = a.rows - r0 < a.span ? a.rows : r0 + a.span;
+    const int64_t total = int64_t(a.rows) * a.cols, begin = int64_t(r0) * a.cols, end = int64_t(r1) * a.cols;
+    const int64_t w = (begin + per - 1) / per + int64_t(piece) * kSortThreads + threadIdx.x;
+    const int64_t e = w * per;
+    if (e >= end) return;
+    const uint32_t x = uint32_t(e - begin);  // below the span's elements
+    if (a.cols >= per && e + per <= total) {
+        const int ra = r0 + int(a.span == 1 ? 0u : __umulhi(x, a.inv_cols));
+        const int rb = ra + (x + per - 1 - uint32_t(ra - r0) * uint32_t(a.cols) >= uint32_t(a.cols) ? 1 : 0);
+        const uint8_t fa = a.flags[ra], fb = a.flags[rb];
+        if (!fa && !fb) {
+            *reinterpret_cast<u32x4_t*>(a.grad + e * es) = u32x4_t{0u, 0u, 0u, 0u};
+            return;
+        }
+        if (fa && fb) return;
+    }
+    for (int64_t k = e; k < e + per && k < total; ++k)
+        if (!a.flags[k / a.cols]) store_elem(a.grad, a.type, k, 0.f);
+}
+
+// The second pass, and beside it the zeros: the sort keeps a few of the CUs
+// for some microseconds, the zeros all of HBM for the rest.
+__global__ __launch_bounds__(kSortThreads) void k_sort_last(SortArgs a, FillArgs f) {
+    extern __shared__ int cnt[];
+    if (int(blockIdx.x) < a.n_tiles)
+        sort_scatter<false>(a, blockIdx.x, cnt);
+    else
+        for (int64_t b = int64_t(blockIdx.x) - a.n_tiles; b < f.n_blocks; b += int64_t(gridDim.x) - a.n_tiles) fill_zeros(f, b);
+}
+
+// Sums over the sorted order.  Work is cut into chunks of `chunk` sorted
+// positions, so a batch of one id over and over is spread like any other.  A
+// run of equal rows that crosses chunk borders belongs whole to the chunk it
+// starts in if it has at most kRunMax positions; a longer one is summed in a
+// piece for each chunk (slot 1 of the chunk it starts in, slot 0 of the
+// others), and k_embed_join adds the pieces in order.  kRunMax: without it
+// every border costs two rows of fp32 pieces, written and read.
+constexpr int kSumThreads = 256, kRunMax = 64;
+
+struct SumArgs {
+    GradArgs g;
+    const int *keys, *pos;
+    float* parts;            // [n_chunks][2][width]
+    int width;               // columns rounded up to kPer
+    int chunk, n_chunks;
+};
+
+// First index in the sorted K[lo..hi) with K[index] >= key, or hi.
+__device__ __forceinline__ int lower_bound(const int* K, int lo, int hi, int key) {
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (K[mid] < key) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+}
+
+template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) void k_embed_sum(SumArgs s) {
+    extern __shared__ int lds[];
+    const GradArgs& a = s.g;
+    const int C = s.chunk, G = 1 << a.group_shift, win = C + 2 * kRunMax;
+    const int lane = int(threadIdx.x) & (G - 1), grp = threadIdx.x >> a.group_shift;
+    const uint32_t item = blockIdx.x * uint32_t(kSumThreads >> a.group_shift) + grp;
+    const int chunk = int(item / uint32_t(a.slabs)), slab = int(item % uint32_t(a.slabs));
+    // the group's chunk of keys with kRunMax more on both sides, and its positions with kRunMax more
+    int* K = lds + grp * (win + C + kRunMax);
+    int* P = K + win;
+    const int base = chunk * C;
+    if (chunk < s.n_chunks) {
+        for (int j = lane; j < win; j += G) {
+            const int p = base - kRunMax + j;
+            K[j] = p < 0 ? -1 : p < a.n ? s.keys[p] : INT32_MAX;
+        }
+        for (int j = lane; j < C + kRunMax; j += G) P[j] = base + j < a.n ? s.pos[base + j] : 0;
+    }
+    __syncthreads();
+    const int c = ((slab << a.group_shift) + lane) * kPer;
+    const int width = a.cols - c < kPer ? a.cols - c : kPer;
+    if (chunk >= s.n_chunks || width <= 0) return;
+    int q0 = 0, q1 = a.n - base < C ? a.n - base : C;
+    const int kf = K[kRunMax], kt = K[kRunMax + q1 - 1];
+    if (kf >= a.rows) return;
+    bool head = false, tail = false;  // a piece of a long run at the chunk's start, at its end
+    if (K[kRunMax - 1] == kf) {
+        const int start = lower_bound(K, 0, kRunMax, kf);
+        head = start == 0 || K[start + kRunMax] == kf;
+        if (!head) q0 = lower_bound(K, kRunMax, win, kf + 1) - kRunMax;
+    }
+    if (kt >= a.rows) {
+        q1 = lower_bound(K, kRunMax, kRunMax + q1, a.rows) - kRunMax;
+    } else if (K[kRunMax + q1] == kt) {
+        const int start = lower_bound(K, 0, kRunMax + q1, kt);
+        tail = start == 0 || K[start + kRunMax] == kt;
+        // a short run that started before the chunk has moved q0 past the chunk's end already
+        if (!tail && q0 < q1) q1 = lower_bound(K, kRunMax + q1, win, kt + 1) - kRunMax;
+    }
+    constexpr int kUnroll = 8;
+    float acc[kPer] = {};
+    for (int q = q0; q < q1; q += kUnroll) {
+        Raw<OD, kPer> x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (q + u < q1)
+                x[u].template load<true>(a.dout + (int64_t(P[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (q + u >= q1) break;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] += x[u].get(k);
+            const int key = K[kRunMax + q + u];
+            if (q + u + 1 < q1 && K[kRunMax + q + u + 1] == key) continue;
+            if ((head && key == kf) || (tail && key == kt)) {
+                float* o = s.parts + (int64_t(chunk) * 2 + (head && key == kf ? 0 : 1)) * s.width + c;
+                reinterpret_cast<f32x4_t*>(o)[0] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+                reinterpret_cast<f32x4_t*>(o)[1] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
+            } else {
+                write_row<GD, ACC>(a, key, c, width, acc);
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
         }
     }
+}
+
+// The long runs: the block of the chunk where one starts adds its pieces in
+// order (each group a stretch of them, then the groups); the others end at once.
+constexpr int kJoinThreads = 512;
+
+template <int GD, bool ACC> __global__ __launch_bounds__(kJoinThreads) void k_embed_join(SumArgs s, uint32_t first_item) {
+    __shared__ float red[kJoinThreads * kPer];
+    __shared__ int start_at, more;
+    const GradArgs& a = s.g;
+    const uint32_t item = first_item + blockIdx.x;
+    const int chunk = int(item / uint32_t(a.slabs)), slab = int(item % uint32_t(a.slabs));
+    const int base = chunk * s.chunk, next = base + s.chunk;
+    if (next >= a.n) return;
+    const int key = s.keys[next - 1];
+    if (key >= a.rows || s.keys[next] != key || (base > 0 && s.keys[base - 1] == key)) return;
+    const int t = int(threadIdx.x);
+    if (t < s.chunk && s.keys[base + t] == key && (t == 0 || s.keys[base + t - 1] != key)) start_at = base + t;
+    if (t == 0) more = 0;
+    __syncthreads();
+    const int64_t past = int64_t(start_at) + kRunMax;
+    if (past >= a.n || s.keys[past] != key) return;  // short: its chunk has written it
+    // how many chunks behind this one the run reaches
+    for (int j = chunk + 1 + t; j < s.n_chunks && s.keys[int64_t(j) * s.chunk] == key; j += kJoinThreads) atomicAdd(&more, 1);
+    __syncthreads();
+    const int pieces = 1 + more, groups = kJoinThreads >> a.group_shift, g = t >> a.group_shift;
+    const int c = ((slab << a.group_shift) + (t & ((1 << a.group_shift) - 1))) * kPer;
+    const int width = a.cols - c < kPer ? a.cols - c : kPer;
+    const int share = (pieces + groups - 1) / groups, lo = g * share, hi = lo + share < pieces ? lo + share : pieces;
+    float acc[kPer] = {};
+    if (width > 0) {
+#pragma unroll 4
+        for (int j = lo; j < hi; ++j) {
+            const float* o = s.parts + (int64_t(chunk + j) * 2 + (j == 0 ? 1 : 0)) * s.width + c;
+            const f32x4_t x = reinterpret_cast<const f32x4_t*>(o)[0], y = reinterpret_cast<const f32x4_t*>(o)[1];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k] += x[k];
+                acc[4 + k] += y[k];
+            }
+        }
+    }
+    add_groups<kJoinThreads>(red, a.group_shift, acc);
+    if (g == 0 && width > 0) write_row<GD, ACC>(a, key, c, width, acc);
+}
+
+// ---- host side ----
+
+// Lanes of a group, 8 to `most` (as a shift): the most lanes that leave at
+// most an eighth more of them idle than the best choice does.
+int pick_group(int words, int most_shift) {
+    auto padded = [&](int s) { return ((words + (1 << s) - 1) >> s) << s; };
+    int best = 1 << 30;
+    for (int s = 3; s <= most_shift; ++s) best = std::min(best, padded(s));
+    for (int s = most_shift; s > 3; --s)
+        if (padded(s) <= best + best / 8) return s;
+    return 3;
+}
+
+// How a gradient of n ids is cut, and where its workspace regions lie.
+struct GradShape {
+    bool few;
+    int group_shift, slabs, width;
+    int bits[2], tile, n_tiles, chunk, n_chunks;
+    uint64_t keys[2], pos[2], hist, flags, parts, total;
+};
+
+GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
+    GradShape s = {};
+    const int words = int((e.cols + kPer - 1) / kPer);
+    s.group_shift = pick_group(std::max(words, 1), 6);
+    s.slabs = std::max(1, (words + (1 << s.group_shift) - 1) >> s.group_shift);
+    s.width = words * kPer;
+    s.few = n <= kFewIds || e.rows == 0 || e.cols == 0;
+    if (s.few) return s;
+    int bits = 2;  // of the largest key, `rows`
+    while ((int64_t(1) << bits) <= e.rows) ++bits;
+    s.bits[0] = (bits + 1) / 2;
+    s.bits[1] = bits - s.bits[0];
+    // at least 4096 positions a tile, at most 64 tiles
+    s.tile = int(std::max<int64_t>(4096, (n + 64 * kSortThreads - 1) / (64 * kSortThreads) * kSortThreads));
+    s.n_tiles = int((n + s.tile - 1) / s.tile);
+    // the longest chunk that still makes 4096 waves (16 a CU)
+    s.chunk = s.group_shift < 5 ? 64 : 256;
+    while (s.chunk > 16 && ((n / s.chunk * s.slabs) << s.group_shift) / 64 < 4096) s.chunk /= 2;
+    s.n_chunks = int((n + s.chunk - 1) / s.chunk);
+    uint64_t off = 0;
+    auto region = [&](uint64_t bytes) {
+        const uint64_t at = off;
+        off = align_up(off + bytes, kAlign);
+        return at;
+    };
+    for (int k = 0; k < 2; ++k) {
+        s.keys[k] = region(uint64_t(n) * 4);
+        s.pos[k] = region(uint64_t(n) * 4);
+    }
+    s.hist = region((uint64_t(s.n_tiles) * 4) << std::max(s.bits[0], s.bits[1]));
+    s.flags = region(uint64_t(e.rows));
+    s.parts = region(uint64_t(s.n_chunks) * 2 * uint64_t(s.width) * 4);
+    s.total = off;
+    return s;
 }
 
 mfsdp_status hip_fail(hipError_t e, const char* what) {
@@ -121,6 +672,102 @@ mfsdp_status check(mfsdp_plan_t plan, int64_t entry, const void* buffer, const v
 
 using namespace mfsdp;
 
+namespace mfsdp {
+namespace {
+
+template <int TD, int OD> hipError_t launch_lookup(LookupArgs a, hipStream_t stream) {
+    constexpr int N = TD == kF32 && OD == kF32 ? 4 : 8;
+    const int words = (a.cols + N - 1) / N;
+    a.group_shift = pick_group(words, 8);
+    const uint32_t slabs = uint32_t((words + (1 << a.group_shift) - 1) >> a.group_shift);
+    const int64_t rows = kLookupThreads >> a.group_shift, blocks = (a.n + rows - 1) / rows;
+    for (int64_t first = 0; first < blocks; first += kBlocksMax)
+        k_embed_lookup<TD, OD>
+            <<<dim3(uint32_t(std::min(blocks - first, kBlocksMax)), slabs), dim3(kLookupThreads), 0, stream>>>(a, first);
+    return hipGetLastError();
+}
+
+hipError_t zero_table(uint8_t* grad, int64_t bytes, hipStream_t stream) {
+    const int64_t blocks = (bytes + kZeroThreads * 16 - 1) / (kZeroThreads * 16);
+    for (int64_t first = 0; first < blocks; first += kBlocksMax)
+        k_embed_zero<<<dim3(uint32_t(std::min(blocks - first, kBlocksMax))), dim3(kZeroThreads), 0, stream>>>(grad, bytes, first);
+    return hipGetLastError();
+}
+
+template <int OD, int GD, bool ACC> hipError_t launch_few(const GradArgs& a, hipStream_t stream) {
+    if (!ACC)
+        if (hipError_t e = zero_table(a.grad, int64_t(a.rows) * a.cols * Raw<GD, kPer>::kSize, stream); e != hipSuccess) return e;
+    if (a.n > 0) k_embed_few<OD, GD, ACC><<<dim3(uint32_t(a.n), uint32_t(a.slabs)), dim3(kFewThreads), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int OD, int GD, bool ACC>
+hipError_t launch_sorted(const GradArgs& a, const GradShape& s, uint8_t* ws, hipStream_t stream) {
+    auto ints = [&](uint64_t off) { return reinterpret_cast<int*>(ws + off); };
+    SortArgs t = {};
+    t.ids = a.ids;
+    t.first = a.first;
+    t.rows = a.rows;
+    t.n = a.n;
+    t.id_type = a.id_type;
+    t.tile = s.tile;
+    t.n_tiles = s.n_tiles;
+    t.hist = ints(s.hist);
+    t.flags = ACC ? nullptr : ws + s.flags;
+    t.shift = 0;
+    t.bits = s.bits[0];
+    t.keys_out = ints(s.keys[0]);
+    t.pos_out = ints(s.pos[0]);
+    const size_t lds0 = size_t(4) << s.bits[0], lds1 = size_t(4) << s.bits[1];
+    k_sort_count<true><<<dim3(s.n_tiles), dim3(kSortThreads), lds0, stream>>>(t);
+    k_sort_first<<<dim3(s.n_tiles), dim3(kSortThreads), lds0 * kSortWaves, stream>>>(t);
+    t.shift = s.bits[0];
+    t.bits = s.bits[1];
+    t.keys_in = t.keys_out;
+    t.pos_in = t.pos_out;
+    t.keys_out = ints(s.keys[1]);
+    t.pos_out = ints(s.pos[1]);
+    k_sort_count<false><<<dim3(s.n_tiles), dim3(kSortThreads), lds1, stream>>>(t);
+    FillArgs f = {};
+    if (!ACC) {
+        const int per = 16 / Raw<GD, kPer>::kSize, block = kSortThreads * per;
+        f.grad = a.grad;
+        f.flags = t.flags;
+        f.rows = a.rows;
+        f.cols = a.cols;
+        f.type = GD;
+        f.span = std::max(1, block / a.cols);
+        f.pieces = f.span > 1 ? 1 : (a.cols + block - 1) / block;
+        f.inv_cols = uint32_t((uint64_t(1) << 32) / uint32_t(a.cols) + 1);
+        f.n_blocks = int64_t((a.rows + f.span - 1) / f.span) * f.pieces;
+    }
+    const int64_t fill = std::min<int64_t>(f.n_blocks, (int64_t(1) << 22));
+    k_sort_last<<<dim3(uint32_t(s.n_tiles + fill)), dim3(kSortThreads), lds1 * kSortWaves, stream>>>(t, f);
+    SumArgs u = {};
+    u.g = a;
+    u.keys = t.keys_out;
+    u.pos = t.pos_out;
+    u.parts = reinterpret_cast<float*>(ws + s.parts);
+    u.width = s.width;
+    u.chunk = s.chunk;
+    u.n_chunks = s.n_chunks;
+    const int groups = kSumThreads >> a.group_shift;
+    const int64_t items = int64_t(s.n_chunks) * a.slabs;
+    const size_t lds = size_t(groups) * size_t(2 * s.chunk + 3 * kRunMax) * 4;
+    k_embed_sum<OD, GD, ACC><<<dim3(uint32_t((items + groups - 1) / groups)), dim3(kSumThreads), lds, stream>>>(u);
+    for (int64_t first = 0; first < items; first += kBlocksMax)
+        k_embed_join<GD, ACC><<<dim3(uint32_t(std::min(items - first, kBlocksMax))), dim3(kJoinThreads), 0, stream>>>(u, uint32_t(first));
+    return hipGetLastError();
+}
+
+template <int OD, int GD, bool ACC>
+hipError_t launch_grad(const GradArgs& a, const GradShape& s, uint8_t* ws, hipStream_t stream) {
+    return s.few ? launch_few<OD, GD, ACC>(a, stream) : launch_sorted<OD, GD, ACC>(a, s, ws, stream);
+}
+
+}  // namespace
+}  // namespace mfsdp
+
 extern "C" mfsdp_status mfsdp_embed_lookup(mfsdp_plan_t plan, int64_t entry, const mfsdp_embed_lookup_args* args) {
     clear_error();
     if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
@@ -131,10 +778,22 @@ extern "C" mfsdp_status mfsdp_embed_lookup(mfsdp_plan_t plan, int64_t entry, con
         return st;
     const mfsdp_entry& e = plan->entries[size_t(entry)];
     if (args->n_ids == 0 || e.cols == 0) return MFSDP_OK;
-    LookupArgs a{static_cast<const uint8_t*>(args->params) + e.offset, args->ids, args->out, e.rows, e.cols,
-                 args->first_id, stride, e.dtype, args->id_type, args->out_type, args->scale};
-    k_embed_lookup<<<dim3(uint32_t(args->n_ids)), dim3(kEmbedThreads), 0, static_cast<hipStream_t>(args->stream)>>>(a);
-    if (hipError_t err = hipGetLastError(); err != hipSuccess) return hip_fail(err, "lookup launch");
+    LookupArgs a = {};
+    a.table = static_cast<const uint8_t*>(args->params) + e.offset;
+    a.ids = args->ids;
+    a.out = static_cast<uint8_t*>(args->out);
+    a.n = args->n_ids;
+    a.first = args->first_id;
+    a.out_stride = stride;
+    a.rows = int(e.rows);
+    a.cols = int(e.cols);
+    a.id_type = args->id_type;
+    a.scale = args->scale;
+    hipStream_t stream = static_cast<hipStream_t>(args->stream);
+    const bool tb = e.dtype == kBF16, ob = args->out_type == kBF16;
+    const hipError_t err = tb ? (ob ? launch_lookup<kBF16, kBF16>(a, stream) : launch_lookup<kBF16, kF32>(a, stream))
+                              : (ob ? launch_lookup<kF32, kBF16>(a, stream) : launch_lookup<kF32, kF32>(a, stream));
+    if (err != hipSuccess) return hip_fail(err, "lookup launch");
     return MFSDP_OK;
 }
 
@@ -145,7 +804,7 @@ extern "C" mfsdp_status mfsdp_plan_embed_workspace_bytes(mfsdp_plan_t plan, int6
     if (entry < 0 || entry >= int64_t(plan->entries.size()))
         return fail(MFSDP_ERR_INVALID_ARGUMENT, "entry index out of range");
     if (n_ids < 0 || n_ids > kMaxIds) return fail(MFSDP_ERR_INVALID_ARGUMENT, "n_ids must be in 0..2^30");
-    *bytes = 0;
+    *bytes = grad_shape(plan->entries[size_t(entry)], n_ids).total;
     return MFSDP_OK;
 }
 
@@ -161,9 +820,42 @@ extern "C" mfsdp_status mfsdp_embed_grad(mfsdp_plan_t plan, int64_t entry, const
         return fail(MFSDP_ERR_INVALID_ARGUMENT, "accumulate must be 0 or 1");
     const mfsdp_entry& e = plan->entries[size_t(entry)];
     if (e.rows == 0 || e.cols == 0 || (args->n_ids == 0 && args->accumulate)) return MFSDP_OK;
-    GradArgs a{static_cast<uint8_t*>(args->grads) + e.offset, args->ids, args->dout, e.rows, e.cols, args->first_id,
-               stride, int(args->n_ids), e.dtype, args->id_type, args->dout_type, args->accumulate, args->scale};
-    k_embed_grad<<<dim3(uint32_t(e.rows)), dim3(kEmbedThreads), 0, static_cast<hipStream_t>(args->stream)>>>(a);
-    if (hipError_t err = hipGetLastError(); err != hipSuccess) return hip_fail(err, "embedding gradient launch");
+    const GradShape s = grad_shape(e, args->n_ids);
+    if (s.total > 0) {
+        if (!args->workspace || misaligned(args->workspace, kAlign))
+            return fail(MFSDP_ERR_INVALID_ARGUMENT, "workspace is NULL or not 256-byte aligned");
+        if (args->workspace_bytes < s.total)
+            return fail(MFSDP_ERR_WORKSPACE_TOO_SMALL, "workspace has " + std::to_string(args->workspace_bytes) +
+                                                           " bytes, " + std::to_string(args->n_ids) + " ids need " +
+                                                           std::to_string(s.total));
+    }
+    GradArgs a = {};
+    a.grad = static_cast<uint8_t*>(args->grads) + e.offset;
+    a.ids = args->ids;
+    a.dout = static_cast<const uint8_t*>(args->dout);
+    a.first = args->first_id;
+    a.dout_stride = stride;
+    a.rows = int(e.rows);
+    a.cols = int(e.cols);
+    a.n = int(args->n_ids);
+    a.id_type = args->id_type;
+    a.group_shift = s.group_shift;
+    a.slabs = s.slabs;
+    a.scale = args->scale;
+    uint8_t* ws = static_cast<uint8_t*>(args->workspace);
+    hipStream_t stream = static_cast<hipStream_t>(args->stream);
+    const int which = (args->dout_type == kBF16 ? 4 : 0) + (e.dtype == kBF16 ? 2 : 0) + args->accumulate;
+    hipError_t err = hipSuccess;
+    switch (which) {
+        case 0: err = launch_grad<kF32, kF32, false>(a, s, ws, stream); break;
+        case 1: err = launch_grad<kF32, kF32, true>(a, s, ws, stream); break;
+        case 2: err = launch_grad<kF32, kBF16, false>(a, s, ws, stream); break;
+        case 3: err = launch_grad<kF32, kBF16, true>(a, s, ws, stream); break;
+        case 4: err = launch_grad<kBF16, kF32, false>(a, s, ws, stream); break;
+        case 5: err = launch_grad<kBF16, kF32, true>(a, s, ws, stream); break;
+        case 6: err = launch_grad<kBF16, kBF16, false>(a, s, ws, stream); break;
+        case 7: err = launch_grad<kBF16, kBF16, true>(a, s, ws, stream); break;
+    }
+    if (err != hipSuccess) return hip_fail(err, "embedding gradient launch");
     return MFSDP_OK;
 }
