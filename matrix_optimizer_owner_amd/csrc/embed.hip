@@ -194,12 +194,15 @@ template <int THREADS> __device__ __forceinline__ void add_groups(float* red, in
 // Zeros over the whole table's gradient: one word a thread, the shape that
 // writes fastest here (6.9 TB/s; 5.9 with 128 KB a block).
 constexpr int kZeroThreads = 256;
-__global__ __launch_bounds__(kZeroThreads) void k_embed_zero(uint8_t* grad, int64_t bytes, int64_t first_block) {
-    const int64_t at = ((first_block + blockIdx.x) * kZeroThreads + threadIdx.x) * 16;
+__device__ __forceinline__ void fill_zeros(uint8_t* grad, int64_t bytes, int64_t word) {
+    const int64_t at = word * 16;
     if (at + 16 <= bytes)
         *reinterpret_cast<u32x4_t*>(grad + at) = u32x4_t{0u, 0u, 0u, 0u};
     else
         for (int64_t b = at; b < bytes; b += 2) *reinterpret_cast<uint16_t*>(grad + b) = 0;
+}
+__global__ __launch_bounds__(kZeroThreads) void k_embed_zero(uint8_t* grad, int64_t bytes, int64_t first_block) {
+    fill_zeros(grad, bytes, (first_block + blockIdx.x) * kZeroThreads + threadIdx.x);
 }
 
 // Few ids: the block of position i looks through all of them, ends if an
@@ -208,11 +211,10 @@ __global__ __launch_bounds__(kZeroThreads) void k_embed_zero(uint8_t* grad, int6
 constexpr int kFewThreads = 256, kFewWaves = kFewThreads / 64, kFewRounds = 8;
 constexpr int kFewIds = kFewThreads * kFewRounds;
 
-template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) void k_embed_few(GradArgs a) {
+template <int OD, int GD, bool ACC> __device__ __forceinline__ void few_ids(const GradArgs& a, int i, int slab) {
     __shared__ int list[kFewIds];
     __shared__ int wave_first[kFewWaves], wave_n[kFewWaves];
     __shared__ float red[kFewThreads * kPer];
-    const int i = int(blockIdx.x), slab = int(blockIdx.y);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = row_of(a.ids, a.id_type, i, a.first, a.rows);
     if (row == a.rows) return;
@@ -262,13 +264,73 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) vo
     if (g == 0 && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
 }
 
+template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) void k_embed_few(GradArgs a) {
+    few_ids<OD, GD, ACC>(a, int(blockIdx.x), int(blockIdx.y));
+}
+
+// The same with the zeros of the other rows beside it: a block has `span`
+// whole rows of at most kFewThreads words, or a piece of kFewThreads words of
+// one longer row, and looks through the ids for its rows first.  A word that
+// two rows share is the first one's.  One launch instead of two saves 3 us on
+// a small table; a large one clears faster without the ids (kFewBytes).
+constexpr int kFewSpanIds = 512, kFewSpanRows = 1024;
+constexpr int64_t kFewBytes = int64_t(32) << 20;
+
+struct SpanArgs {
+    int span, pieces;        // rows of a block, or blocks of a row
+    int few_blocks;          // the launch's first ones
+};
+
+template <int GD> __device__ __forceinline__ void fill_span(const GradArgs& a, const SpanArgs& s, int block) {
+    constexpr int kElems = GD == kBF16 ? 8 : 4, kSize = 16 / kElems;
+    __shared__ uint8_t hit[kFewSpanRows + 4];
+    const int g = block / s.pieces, piece = block - g * s.pieces, r0 = g * s.span;
+    const int r1 = a.rows - r0 < s.span ? a.rows : r0 + s.span;
+    for (int r = threadIdx.x; r <= s.span; r += kFewThreads) hit[r] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kFewSpanIds / kFewThreads; ++k) {
+        const int p = k * kFewThreads + int(threadIdx.x);
+        if (p < a.n) {
+            const int r = row_of(a.ids, a.id_type, p, a.first, a.rows);
+            if (r >= r0 && r <= r1 && r < a.rows) hit[r - r0] = 1;
+        }
+    }
+    __syncthreads();
+    const int64_t total = int64_t(a.rows) * a.cols, begin = int64_t(r0) * a.cols, end = int64_t(r1) * a.cols;
+    const int64_t e = ((begin + kElems - 1) / kElems + int64_t(piece) * kFewThreads + threadIdx.x) * kElems;
+    if (e >= end) return;
+    uint32_t x = uint32_t(e - begin), r = x / uint32_t(a.cols), c = x - r * uint32_t(a.cols);
+    if (c + kElems <= uint32_t(a.cols)) {  // a word of one row
+        if (!hit[r]) *reinterpret_cast<u32x4_t*>(a.grad + e * kSize) = u32x4_t{0u, 0u, 0u, 0u};
+        return;
+    }
+    // a word over a row's end reaches into one more row (rows are at least a word wide here), at most into r1,
+    // whose ids were looked for too
+    for (int k = 0; k < kElems && e + k < total; ++k) {
+        if (!hit[r]) store_elem(a.grad, GD, e + k, 0.f);
+        if (++c == uint32_t(a.cols)) {
+            c = 0;
+            ++r;
+        }
+    }
+}
+
+template <int OD, int GD> __global__ __launch_bounds__(kFewThreads) void k_embed_few_fill(GradArgs a, SpanArgs s) {
+    const int b = int(blockIdx.x);
+    if (b < s.few_blocks)
+        few_ids<OD, GD, false>(a, b / a.slabs, b % a.slabs);
+    else
+        fill_span<GD>(a, s, b - s.few_blocks);
+}
+
 // ---- many ids: sort positions by row, then sum runs of the sorted order ----
 //
 // The sort is a stable radix sort of (row, position) in two passes over about
 // half of the row's bits each: per pass one launch counts each tile's digits
 // and one ranks and scatters.  Ids outside the table sort last, as row `rows`.
 
-constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64;
+constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64, kSortUnroll = 4;
 
 struct SortArgs {
     const void* ids;          // first pass; else keys_in and pos_in
@@ -279,27 +341,56 @@ struct SortArgs {
     const int *keys_in, *pos_in;
     int* hist;                // [n_tiles][2^bits]
     int *keys_out, *pos_out;
-    uint8_t* flags;           // [rows]: whether a position has the row; NULL when nothing is zero-filled
+    int* n_runs;              // cleared by the first launch
+};
+
+// Zeros beside the sort: the table's gradient is cleared by blocks that the
+// sort's four launches carry behind their own, a quarter each, so that the
+// sort, which keeps a few CUs for some microseconds a launch, takes no time
+// of its own.  One word a thread, the shape that writes fastest here.  (Clearing
+// only the rows without an id, by a flag a row, saves their bytes but waits
+// for the flag first: 4.1 TB/s instead of 6.9.)
+struct FillArgs {
+    uint8_t* grad;
+    int64_t bytes;
+    int64_t first_block;     // of kSortThreads words
 };
 
 template <bool FIRST> __device__ __forceinline__ int sort_key(const SortArgs& a, int p) {
     return FIRST ? row_of(a.ids, a.id_type, p, a.first, a.rows) : a.keys_in[p];
 }
 
-template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a) {
-    extern __shared__ int count[];
-    const int bins = 1 << a.bits;
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) count[d] = 0;
-    if (FIRST && a.flags) {
-        // words of four flags (the region is padded to 256 bytes)
-        for (int w = blockIdx.x * kSortThreads + threadIdx.x; w < (a.rows + 3) / 4; w += gridDim.x * kSortThreads)
-            reinterpret_cast<uint32_t*>(a.flags)[w] = 0;
+// Calls f(p, key) for the positions p of [lo, lo + count) below n that are
+// `stride` apart from lo + me on, kSortUnroll keys loaded at a time; f also
+// runs (with p >= n) on lanes whose position is past the end.
+template <bool FIRST, typename F>
+__device__ __forceinline__ void for_keys(const SortArgs& a, int lo, int count, int me, int stride, F f) {
+    for (int r = 0; r < count; r += stride * kSortUnroll) {
+        int key[kSortUnroll];
+#pragma unroll
+        for (int u = 0; u < kSortUnroll; ++u) {
+            const int p = lo + r + u * stride + me;
+            key[u] = r + u * stride < count && p < a.n ? sort_key<FIRST>(a, p) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kSortUnroll; ++u)
+            if (r + u * stride < count) f(lo + r + u * stride + me, key[u]);
     }
+}
+
+template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a, FillArgs f) {
+    extern __shared__ int cnt[];
+    if (int(blockIdx.x) >= a.n_tiles)
+        return fill_zeros(f.grad, f.bytes, (f.first_block + blockIdx.x - a.n_tiles) * kSortThreads + threadIdx.x);
+    const int bins = 1 << a.bits;
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) cnt[d] = 0;
+    if (FIRST && blockIdx.x == 0 && threadIdx.x == 0) *a.n_runs = 0;
     __syncthreads();
-    const int lo = blockIdx.x * a.tile, hi = a.n - lo < a.tile ? a.n : lo + a.tile;
-    for (int p = lo + threadIdx.x; p < hi; p += kSortThreads) atomicAdd(&count[sort_key<FIRST>(a, p) >> a.shift & (bins - 1)], 1);
+    for_keys<FIRST>(a, int(blockIdx.x) * a.tile, a.tile, threadIdx.x, kSortThreads, [&](int p, int key) {
+        if (p < a.n) atomicAdd(&cnt[key >> a.shift & (bins - 1)], 1);
+    });
     __syncthreads();
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) a.hist[int64_t(blockIdx.x) * bins + d] = count[d];
+    for (int d = threadIdx.x; d < bins; d += kSortThreads) a.hist[int64_t(blockIdx.x) * bins + d] = cnt[d];
 }
 
 // Exclusive sum of v over the block; `sum` receives the total.
@@ -333,10 +424,9 @@ template <bool FIRST> __device__ __forceinline__ void sort_scatter(const SortArg
     __syncthreads();
     const int part = a.tile / kSortWaves, lo = tile * a.tile + wave * part;
     int* mine = cnt + wave * bins;
-    for (int r = 0; r < part; r += 64) {
-        const int p = lo + r + lane;
-        if (p < a.n) atomicAdd(&mine[sort_key<FIRST>(a, p) >> a.shift & (bins - 1)], 1);
-    }
+    for_keys<FIRST>(a, lo, part, lane, 64, [&](int p, int key) {
+        if (p < a.n) atomicAdd(&mine[key >> a.shift & (bins - 1)], 1);
+    });
     __syncthreads();
     int carry = 0;
     for (int d0 = 0; d0 < bins; d0 += kSortThreads) {
@@ -367,10 +457,8 @@ template <bool FIRST> __device__ __forceinline__ void sort_scatter(const SortArg
     }
     __syncthreads();
     volatile int* place = mine;
-    for (int r = 0; r < part; r += 64) {
-        const int p = lo + r + lane;
+    for_keys<FIRST>(a, lo, part, lane, 64, [&](int p, int key) {
         const bool live = p < a.n;
-        const int key = live ? sort_key<FIRST>(a, p) : 0;
         const int digit = key >> a.shift & (bins - 1);
         uint64_t same = __ballot(live);
         for (int b = 0; b < a.bits; ++b) {
@@ -383,61 +471,17 @@ template <bool FIRST> __device__ __forceinline__ void sort_scatter(const SortArg
             if (rank == 0) place[digit] = at + __popcll(same);
             a.keys_out[at + rank] = key;
             a.pos_out[at + rank] = FIRST ? p : a.pos_in[p];
-            if (FIRST && a.flags && key < a.rows) a.flags[key] = 1;  // the same value by every writer
         }
         __builtin_amdgcn_wave_barrier();
-    }
+    });
 }
 
-__global__ __launch_bounds__(kSortThreads) void k_sort_first(SortArgs a) {
-    extern __shared__ int cnt[];
-    sort_scatter<true>(a, blockIdx.x, cnt);
-}
-
-// Zeros in the rows that no position has.  A block has `rows` whole rows of
-// at most 512 words, or a piece of 512 words of one longer row; a word that
-// two rows share is the first one's.
-struct FillArgs {
-    uint8_t* grad;
-    const uint8_t* flags;
-    int rows, cols, type;
-    int span;                // rows of a block
-    int pieces;              // blocks of a row, when span is 1
-    uint32_t inv_cols;       // ceil(2^32 / cols)
-    int64_t n_blocks;
-};
-
-__device__ __forceinline__ void fill_zeros(const FillArgs& a, int64_t block) {
-    const int per = a.type == kBF16 ? 8 : 4, es = 16 / per;
-    const int g = a.pieces == 1 ? int(block) : int(block / a.pieces), piece = int(block - int64_t(g) * a.pieces);
-    const int r0 = g * a.span, r1 = a.rows - r0 < a.span ? a.rows : r0 + a.span;
-    const int64_t total = int64_t(a.rows) * a.cols, begin = int64_t(r0) * a.cols, end = int64_t(r1) * a.cols;
-    const int64_t w = (begin + per - 1) / per + int64_t(piece) * kSortThreads + threadIdx.x;
-    const int64_t e = w * per;
-    if (e >= end) return;
-    const uint32_t x = uint32_t(e - begin);  // below the span's elements
-    if (a.cols >= per && e + per <= total) {
-        const int ra = r0 + int(a.span == 1 ? 0u : __umulhi(x, a.inv_cols));
-        const int rb = ra + (x + per - 1 - uint32_t(ra - r0) * uint32_t(a.cols) >= uint32_t(a.cols) ? 1 : 0);
-        const uint8_t fa = a.flags[ra], fb = a.flags[rb];
-        if (!fa && !fb) {
-            *reinterpret_cast<u32x4_t*>(a.grad + e * es) = u32x4_t{0u, 0u, 0u, 0u};
-            return;
-        }
-        if (fa && fb) return;
-    }
-    for (int64_t k = e; k < e + per && k < total; ++k)
-        if (!a.flags[k / a.cols]) store_elem(a.grad, a.type, k, 0.f);
-}
-
-// The second pass, and beside it the zeros: the sort keeps a few of the CUs
-// for some microseconds, the zeros all of HBM for the rest.
-__global__ __launch_bounds__(kSortThreads) void k_sort_last(SortArgs a, FillArgs f) {
+template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortArgs a, FillArgs f) {
     extern __shared__ int cnt[];
     if (int(blockIdx.x) < a.n_tiles)
-        sort_scatter<false>(a, blockIdx.x, cnt);
+        sort_scatter<FIRST>(a, blockIdx.x, cnt);
     else
-        for (int64_t b = int64_t(blockIdx.x) - a.n_tiles; b < f.n_blocks; b += int64_t(gridDim.x) - a.n_tiles) fill_zeros(f, b);
+        fill_zeros(f.grad, f.bytes, (f.first_block + blockIdx.x - a.n_tiles) * kSortThreads + threadIdx.x);
 }
 
 // Sums over the sorted order.  Work is cut into chunks of `chunk` sorted
@@ -453,6 +497,7 @@ struct SumArgs {
     GradArgs g;
     const int *keys, *pos;
     float* parts;            // [n_chunks][2][width]
+    int *n_runs, *runs;      // the chunks where a long run starts, in no order
     int width;               // columns rounded up to kPer
     int chunk, n_chunks;
 };
@@ -521,7 +566,9 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
             const int key = K[kRunMax + q + u];
             if (q + u + 1 < q1 && K[kRunMax + q + u + 1] == key) continue;
             if ((head && key == kf) || (tail && key == kt)) {
-                float* o = s.parts + (int64_t(chunk) * 2 + (head && key == kf ? 0 : 1)) * s.width + c;
+                const int slot = head && key == kf ? 0 : 1;
+                float* o = s.parts + (int64_t(chunk) * 2 + slot) * s.width + c;
+                if (slot == 1 && c == 0) s.runs[atomicAdd(s.n_runs, 1)] = chunk;
                 reinterpret_cast<f32x4_t*>(o)[0] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
                 reinterpret_cast<f32x4_t*>(o)[1] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
             } else {
@@ -533,48 +580,48 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
     }
 }
 
-// The long runs: the block of the chunk where one starts adds its pieces in
-// order (each group a stretch of them, then the groups); the others end at once.
-constexpr int kJoinThreads = 512;
+// The long runs, one at a time to a block: its pieces are added in order (each
+// group a stretch of them, then the groups).  The list's order differs from
+// run to run, the sums do not.
+constexpr int kJoinThreads = 512, kJoinBlocks = 512;
 
-template <int GD, bool ACC> __global__ __launch_bounds__(kJoinThreads) void k_embed_join(SumArgs s, uint32_t first_item) {
+template <int GD, bool ACC> __global__ __launch_bounds__(kJoinThreads) void k_embed_join(SumArgs s) {
     __shared__ float red[kJoinThreads * kPer];
-    __shared__ int start_at, more;
+    __shared__ int more;
     const GradArgs& a = s.g;
-    const uint32_t item = first_item + blockIdx.x;
-    const int chunk = int(item / uint32_t(a.slabs)), slab = int(item % uint32_t(a.slabs));
-    const int base = chunk * s.chunk, next = base + s.chunk;
-    if (next >= a.n) return;
-    const int key = s.keys[next - 1];
-    if (key >= a.rows || s.keys[next] != key || (base > 0 && s.keys[base - 1] == key)) return;
-    const int t = int(threadIdx.x);
-    if (t < s.chunk && s.keys[base + t] == key && (t == 0 || s.keys[base + t - 1] != key)) start_at = base + t;
-    if (t == 0) more = 0;
-    __syncthreads();
-    const int64_t past = int64_t(start_at) + kRunMax;
-    if (past >= a.n || s.keys[past] != key) return;  // short: its chunk has written it
-    // how many chunks behind this one the run reaches
-    for (int j = chunk + 1 + t; j < s.n_chunks && s.keys[int64_t(j) * s.chunk] == key; j += kJoinThreads) atomicAdd(&more, 1);
-    __syncthreads();
-    const int pieces = 1 + more, groups = kJoinThreads >> a.group_shift, g = t >> a.group_shift;
+    const int t = int(threadIdx.x), slab = int(blockIdx.y);
+    const int groups = kJoinThreads >> a.group_shift, g = t >> a.group_shift;
     const int c = ((slab << a.group_shift) + (t & ((1 << a.group_shift) - 1))) * kPer;
     const int width = a.cols - c < kPer ? a.cols - c : kPer;
-    const int share = (pieces + groups - 1) / groups, lo = g * share, hi = lo + share < pieces ? lo + share : pieces;
-    float acc[kPer] = {};
-    if (width > 0) {
+    const int n_runs = *s.n_runs;
+    for (int r = blockIdx.x; r < n_runs; r += int(gridDim.x)) {
+        const int chunk = s.runs[r], key = s.keys[int64_t(chunk + 1) * s.chunk - 1];
+        __syncthreads();
+        if (t == 0) more = 0;
+        __syncthreads();
+        // how many chunks behind this one the run reaches
+        int reach = 0;
+        for (int j = chunk + 1 + t; j < s.n_chunks && s.keys[int64_t(j) * s.chunk] == key; j += kJoinThreads) ++reach;
+        if (reach) atomicAdd(&more, reach);
+        __syncthreads();
+        const int pieces = 1 + more;
+        const int share = (pieces + groups - 1) / groups, lo = g * share, hi = lo + share < pieces ? lo + share : pieces;
+        float acc[kPer] = {};
+        if (width > 0) {
 #pragma unroll 4
-        for (int j = lo; j < hi; ++j) {
-            const float* o = s.parts + (int64_t(chunk + j) * 2 + (j == 0 ? 1 : 0)) * s.width + c;
-            const f32x4_t x = reinterpret_cast<const f32x4_t*>(o)[0], y = reinterpret_cast<const f32x4_t*>(o)[1];
+            for (int j = lo; j < hi; ++j) {
+                const float* o = s.parts + (int64_t(chunk + j) * 2 + (j == 0 ? 1 : 0)) * s.width + c;
+                const f32x4_t x = reinterpret_cast<const f32x4_t*>(o)[0], y = reinterpret_cast<const f32x4_t*>(o)[1];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                acc[k] += x[k];
-                acc[4 + k] += y[k];
+                for (int k = 0; k < 4; ++k) {
+                    acc[k] += x[k];
+                    acc[4 + k] += y[k];
+                }
             }
         }
+        add_groups<kJoinThreads>(red, a.group_shift, acc);
+        if (g == 0 && width > 0) write_row<GD, ACC>(a, key, c, width, acc);
     }
-    add_groups<kJoinThreads>(red, a.group_shift, acc);
-    if (g == 0 && width > 0) write_row<GD, ACC>(a, key, c, width, acc);
 }
 
 // ---- host side ----
@@ -595,7 +642,7 @@ struct GradShape {
     bool few;
     int group_shift, slabs, width;
     int bits[2], tile, n_tiles, chunk, n_chunks;
-    uint64_t keys[2], pos[2], hist, flags, parts, total;
+    uint64_t keys[2], pos[2], hist, runs, parts, total;
 };
 
 GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
@@ -610,8 +657,9 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     while ((int64_t(1) << bits) <= e.rows) ++bits;
     s.bits[0] = (bits + 1) / 2;
     s.bits[1] = bits - s.bits[0];
-    // at least 4096 positions a tile, at most 64 tiles
-    s.tile = int(std::max<int64_t>(4096, (n + 64 * kSortThreads - 1) / (64 * kSortThreads) * kSortThreads));
+    // at least 2048 positions a tile (every wave has four of each lane's in
+    // flight), at most 128 tiles (each adds up the digits of all others)
+    s.tile = int(std::max<int64_t>(2048, (n + 128 * kSortThreads - 1) / (128 * kSortThreads) * kSortThreads));
     s.n_tiles = int((n + s.tile - 1) / s.tile);
     // the longest chunk that still makes 4096 waves (16 a CU)
     s.chunk = s.group_shift < 5 ? 64 : 256;
@@ -628,7 +676,7 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
         s.pos[k] = region(uint64_t(n) * 4);
     }
     s.hist = region((uint64_t(s.n_tiles) * 4) << std::max(s.bits[0], s.bits[1]));
-    s.flags = region(uint64_t(e.rows));
+    s.runs = region((uint64_t(s.n_chunks) + 1) * 4);  // their number, then the list
     s.parts = region(uint64_t(s.n_chunks) * 2 * uint64_t(s.width) * 4);
     s.total = off;
     return s;
@@ -695,8 +743,20 @@ hipError_t zero_table(uint8_t* grad, int64_t bytes, hipStream_t stream) {
 }
 
 template <int OD, int GD, bool ACC> hipError_t launch_few(const GradArgs& a, hipStream_t stream) {
-    if (!ACC)
-        if (hipError_t e = zero_table(a.grad, int64_t(a.rows) * a.cols * Raw<GD, kPer>::kSize, stream); e != hipSuccess) return e;
+    if constexpr (!ACC) {
+        constexpr int kSize = Raw<GD, kPer>::kSize, kElems = 16 / kSize * kFewThreads;
+        const int64_t bytes = int64_t(a.rows) * a.cols * kSize;
+        if (a.n <= kFewSpanIds && bytes <= kFewBytes && a.cols >= 16 / kSize) {
+            SpanArgs s;
+            s.span = std::clamp(kElems / a.cols, 1, kFewSpanRows);
+            s.pieces = s.span > 1 ? 1 : (a.cols + kElems - 1) / kElems;
+            s.few_blocks = a.n * a.slabs;
+            const int blocks = s.few_blocks + (a.rows + s.span - 1) / s.span * s.pieces;
+            k_embed_few_fill<OD, GD><<<dim3(uint32_t(blocks)), dim3(kFewThreads), 0, stream>>>(a, s);
+            return hipGetLastError();
+        }
+        if (hipError_t e = zero_table(a.grad, bytes, stream); e != hipSuccess) return e;
+    }
     if (a.n > 0) k_embed_few<OD, GD, ACC><<<dim3(uint32_t(a.n), uint32_t(a.slabs)), dim3(kFewThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -713,50 +773,51 @@ hipError_t launch_sorted(const GradArgs& a, const GradShape& s, uint8_t* ws, hip
     t.tile = s.tile;
     t.n_tiles = s.n_tiles;
     t.hist = ints(s.hist);
-    t.flags = ACC ? nullptr : ws + s.flags;
+    t.n_runs = ints(s.runs);
     t.shift = 0;
     t.bits = s.bits[0];
     t.keys_out = ints(s.keys[0]);
     t.pos_out = ints(s.pos[0]);
+    // the four launches of the sort, each with a quarter of the zeros
+    FillArgs f = {a.grad, ACC ? 0 : int64_t(a.rows) * a.cols * Raw<GD, kPer>::kSize, 0};
+    int64_t fill = (f.bytes + kSortThreads * 16 - 1) / (kSortThreads * 16);
+    if (fill > 2 * kBlocksMax) {  // 137 GB: more than four launches hold
+        if (hipError_t e = zero_table(a.grad, f.bytes, stream); e != hipSuccess) return e;
+        fill = 0;
+    }
+    const int64_t quarter = (fill + 3) / 4;
+    auto grid = [&] { return dim3(uint32_t(s.n_tiles + std::max<int64_t>(0, std::min(quarter, fill - f.first_block)))); };
     const size_t lds0 = size_t(4) << s.bits[0], lds1 = size_t(4) << s.bits[1];
-    k_sort_count<true><<<dim3(s.n_tiles), dim3(kSortThreads), lds0, stream>>>(t);
-    k_sort_first<<<dim3(s.n_tiles), dim3(kSortThreads), lds0 * kSortWaves, stream>>>(t);
+    k_sort_count<true><<<grid(), dim3(kSortThreads), lds0, stream>>>(t, f);
+    f.first_block += quarter;
+    k_sort_scatter<true><<<grid(), dim3(kSortThreads), lds0 * kSortWaves, stream>>>(t, f);
+    f.first_block += quarter;
     t.shift = s.bits[0];
     t.bits = s.bits[1];
     t.keys_in = t.keys_out;
     t.pos_in = t.pos_out;
     t.keys_out = ints(s.keys[1]);
     t.pos_out = ints(s.pos[1]);
-    k_sort_count<false><<<dim3(s.n_tiles), dim3(kSortThreads), lds1, stream>>>(t);
-    FillArgs f = {};
-    if (!ACC) {
-        const int per = 16 / Raw<GD, kPer>::kSize, block = kSortThreads * per;
-        f.grad = a.grad;
-        f.flags = t.flags;
-        f.rows = a.rows;
-        f.cols = a.cols;
-        f.type = GD;
-        f.span = std::max(1, block / a.cols);
-        f.pieces = f.span > 1 ? 1 : (a.cols + block - 1) / block;
-        f.inv_cols = uint32_t((uint64_t(1) << 32) / uint32_t(a.cols) + 1);
-        f.n_blocks = int64_t((a.rows + f.span - 1) / f.span) * f.pieces;
-    }
-    const int64_t fill = std::min<int64_t>(f.n_blocks, (int64_t(1) << 22));
-    k_sort_last<<<dim3(uint32_t(s.n_tiles + fill)), dim3(kSortThreads), lds1 * kSortWaves, stream>>>(t, f);
+    k_sort_count<false><<<grid(), dim3(kSortThreads), lds1, stream>>>(t, f);
+    f.first_block += quarter;
+    k_sort_scatter<false><<<grid(), dim3(kSortThreads), lds1 * kSortWaves, stream>>>(t, f);
     SumArgs u = {};
     u.g = a;
     u.keys = t.keys_out;
     u.pos = t.pos_out;
     u.parts = reinterpret_cast<float*>(ws + s.parts);
     u.width = s.width;
+    u.n_runs = ints(s.runs);
+    u.runs = u.n_runs + 1;
     u.chunk = s.chunk;
     u.n_chunks = s.n_chunks;
     const int groups = kSumThreads >> a.group_shift;
     const int64_t items = int64_t(s.n_chunks) * a.slabs;
     const size_t lds = size_t(groups) * size_t(2 * s.chunk + 3 * kRunMax) * 4;
     k_embed_sum<OD, GD, ACC><<<dim3(uint32_t((items + groups - 1) / groups)), dim3(kSumThreads), lds, stream>>>(u);
-    for (int64_t first = 0; first < items; first += kBlocksMax)
-        k_embed_join<GD, ACC><<<dim3(uint32_t(std::min(items - first, kBlocksMax))), dim3(kJoinThreads), 0, stream>>>(u, uint32_t(first));
+    // a long run has more than kRunMax positions
+    const int runs = int(std::min<int64_t>(kJoinBlocks, (a.n + kRunMax) / (kRunMax + 1)));
+    k_embed_join<GD, ACC><<<dim3(uint32_t(runs), uint32_t(a.slabs)), dim3(kJoinThreads), 0, stream>>>(u);
     return hipGetLastError();
 }
 
