@@ -86,7 +86,7 @@ template <int DT, int N, bool STREAM> __device__ __forceinline__ void store(void
 
 // ---- lookup ----
 
-constexpr int kLookupThreads = 256;
+constexpr int kLookupThreads = 512;
 constexpr int64_t kBlocksMax = (int64_t(1) << 23) - 1;  // a launch holds fewer than 2^32 threads
 
 struct LookupArgs {
@@ -103,7 +103,10 @@ struct LookupArgs {
 // HBM-bound: each id's row is read and written once.  One word of the
 // narrower type a thread and no loop, the shape that copies fastest here
 // (grad.hip); 2^group_shift lanes share a position, so narrow rows fill the
-// wave too.  first_block: the launch's first block.
+// wave too.  Stores go past the caches and loads through them, which keeps
+// the rows that many ids share: 16384 ids into 128256 x 4096 bf16 take 36 us
+// (191 MB, 5.3 TB/s), 49 with ordinary stores, 47 with loads past the caches
+// too.  first_block: the launch's first block.
 template <int TD, int OD>
 __global__ __launch_bounds__(kLookupThreads) void k_embed_lookup(LookupArgs a, int64_t first_block) {
     constexpr int N = TD == kF32 && OD == kF32 ? 4 : 8;
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(kLookupThreads) void k_embed_lookup(LookupArgs a, i
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = 0.f;
     }
-    store<OD, N, false>(a.out + (i * a.out_stride + c) * Raw<OD, N>::kSize, width, v);
+    store<OD, N, true>(a.out + (i * a.out_stride + c) * Raw<OD, N>::kSize, width, v);
 }
 
 // ---- gradient ----
@@ -158,7 +161,7 @@ __device__ __forceinline__ void write_row(const GradArgs& a, int row, int c, int
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = a.scale * sum[k];
     }
-    store<GD, kPer, false>(p, width, v);
+    store<GD, kPer, true>(p, width, v);
 }
 
 // The sum of dout rows list[0..count), columns c .. c + width, kUnroll loads in flight.
@@ -330,13 +333,13 @@ template <int OD, int GD> __global__ __launch_bounds__(kFewThreads) void k_embed
 // half of the row's bits each: per pass one launch counts each tile's digits
 // and one ranks and scatters.  Ids outside the table sort last, as row `rows`.
 
-constexpr int kSortThreads = 512, kSortWaves = kSortThreads / 64, kSortUnroll = 4;
+constexpr int kSortUnroll = 4;
 
 struct SortArgs {
     const void* ids;          // first pass; else keys_in and pos_in
     int64_t first;
     int rows, n, id_type;
-    int tile, n_tiles;        // positions of a block, a multiple of kSortThreads
+    int tile, n_tiles;        // positions of a block, a multiple of 512
     int shift, bits;          // the pass's digit
     const int *keys_in, *pos_in;
     int* hist;                // [n_tiles][2^bits]
@@ -353,48 +356,51 @@ struct SortArgs {
 struct FillArgs {
     uint8_t* grad;
     int64_t bytes;
-    int64_t first_block;     // of kSortThreads words
+    int64_t first_block;     // of one word a thread
 };
 
 template <bool FIRST> __device__ __forceinline__ int sort_key(const SortArgs& a, int p) {
     return FIRST ? row_of(a.ids, a.id_type, p, a.first, a.rows) : a.keys_in[p];
 }
 
-// Calls f(p, key) for the positions p of [lo, lo + count) below n that are
-// `stride` apart from lo + me on, kSortUnroll keys loaded at a time; f also
-// runs (with p >= n) on lanes whose position is past the end.
-template <bool FIRST, typename F>
+// Calls f(p, key, position) for the places p of [lo, lo + count) that are `stride`
+// apart from lo + me on, kSortUnroll of them loaded at a time; f also runs
+// (with p >= n) on lanes whose place is past the end.  POS: the position that
+// goes with the key is loaded too.
+template <bool FIRST, bool POS, typename F>
 __device__ __forceinline__ void for_keys(const SortArgs& a, int lo, int count, int me, int stride, F f) {
     for (int r = 0; r < count; r += stride * kSortUnroll) {
-        int key[kSortUnroll];
+        int key[kSortUnroll], pos[kSortUnroll];
 #pragma unroll
         for (int u = 0; u < kSortUnroll; ++u) {
             const int p = lo + r + u * stride + me;
-            key[u] = r + u * stride < count && p < a.n ? sort_key<FIRST>(a, p) : 0;
+            const bool live = r + u * stride < count && p < a.n;
+            key[u] = live ? sort_key<FIRST>(a, p) : 0;
+            pos[u] = POS && !FIRST && live ? a.pos_in[p] : p;
         }
 #pragma unroll
         for (int u = 0; u < kSortUnroll; ++u)
-            if (r + u * stride < count) f(lo + r + u * stride + me, key[u]);
+            if (r + u * stride < count) f(lo + r + u * stride + me, key[u], pos[u]);
     }
 }
 
-template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a, FillArgs f) {
+template <bool FIRST, int T> __global__ __launch_bounds__(T) void k_sort_count(SortArgs a, FillArgs f) {
     extern __shared__ int cnt[];
     if (int(blockIdx.x) >= a.n_tiles)
-        return fill_zeros(f.grad, f.bytes, (f.first_block + blockIdx.x - a.n_tiles) * kSortThreads + threadIdx.x);
+        return fill_zeros(f.grad, f.bytes, (f.first_block + blockIdx.x - a.n_tiles) * T + threadIdx.x);
     const int bins = 1 << a.bits;
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) cnt[d] = 0;
+    for (int d = threadIdx.x; d < bins; d += T) cnt[d] = 0;
     if (FIRST && blockIdx.x == 0 && threadIdx.x == 0) *a.n_runs = 0;
     __syncthreads();
-    for_keys<FIRST>(a, int(blockIdx.x) * a.tile, a.tile, threadIdx.x, kSortThreads, [&](int p, int key) {
+    for_keys<FIRST, false>(a, int(blockIdx.x) * a.tile, a.tile, threadIdx.x, T, [&](int p, int key, int) {
         if (p < a.n) atomicAdd(&cnt[key >> a.shift & (bins - 1)], 1);
     });
     __syncthreads();
-    for (int d = threadIdx.x; d < bins; d += kSortThreads) a.hist[int64_t(blockIdx.x) * bins + d] = cnt[d];
+    for (int d = threadIdx.x; d < bins; d += T) a.hist[int64_t(blockIdx.x) * bins + d] = cnt[d];
 }
 
-// Exclusive sum of v over the block; `sum` receives the total.
-__device__ __forceinline__ int block_scan(int v, int* red, int& sum) {
+// Exclusive sum of v over a block of WAVES waves; `sum` receives the total.
+template <int WAVES> __device__ __forceinline__ int block_scan(int v, int* red, int& sum) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int x = v;
 #pragma unroll
@@ -406,7 +412,7 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& sum) {
     __syncthreads();
     int before = 0;
     sum = 0;
-    for (int w = 0; w < kSortWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         if (w < wave) before += red[w];
         sum += red[w];
     }
@@ -414,74 +420,177 @@ __device__ __forceinline__ int block_scan(int v, int* red, int& sum) {
     return before + x - v;
 }
 
-// One tile of a pass.  Wave w of the block has a contiguous eighth of the
-// tile; a key's place is the number of smaller digits, then of equal digits
-// in earlier tiles, earlier waves, earlier rounds and lower lanes: stable.
-template <bool FIRST> __device__ __forceinline__ void sort_scatter(const SortArgs& a, int tile, int* cnt) {
-    __shared__ int red[kSortWaves];
+// A wave's next 64 keys get their places: place[digit] is where the wave's next
+// key of that digit goes, moved on by as many as there are here.  Equal
+// digits keep their lanes' order.  Returns the lane's place (live lanes).
+__device__ __forceinline__ int take_places(int* place, int digit, int bits, bool live) {
+    // the live lanes whose digit agrees in every bit, in two halves: with t all
+    // ones where the lane's bit is set, a lane agrees where m and t do
+    const uint64_t all = __builtin_amdgcn_ballot_w64(live);
+    uint32_t lo = uint32_t(all), hi = uint32_t(all >> 32);
+    for (int b0 = 0; b0 < bits; b0 += 3)
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {  // bits behind the digit's last are zero in every lane
+            const bool set = digit & (1 << (b0 + b));
+            const uint64_t m = __builtin_amdgcn_ballot_w64(set);
+            const uint32_t t = set ? ~0u : 0u;
+            lo &= ~(uint32_t(m) ^ t);
+            hi &= ~(uint32_t(m >> 32) ^ t);
+        }
+    int at = 0;
+    if (live) {
+        const int rank = int(__builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0)));  // of them, in lower lanes
+        // (relaxed atomics: LDS accesses that stay where they are; a volatile pointer would make them flat ones)
+        at = __hip_atomic_load(place + digit, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT) + rank;
+        __builtin_amdgcn_wave_barrier();  // every lane has read its place before the first of them moves it on
+        if (rank == 0)
+            __hip_atomic_store(place + digit, at + __popc(lo) + __popc(hi), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+    }
+    __builtin_amdgcn_wave_barrier();
+    return at;
+}
+
+// One tile of a pass.  Wave w of the block has a contiguous part of the tile;
+// a key's place is the number of smaller digits, then of equal digits in
+// earlier tiles, earlier waves, earlier rounds and lower lanes: stable.
+template <bool FIRST, int T> __global__ __launch_bounds__(T) void k_sort_scatter(SortArgs a, FillArgs f) {
+    constexpr int kWaves = T / 64;
+    extern __shared__ int cnt[];
+    __shared__ int red[kWaves];
+    const int tile = int(blockIdx.x);
+    if (tile >= a.n_tiles)
+        return fill_zeros(f.grad, f.bytes, (f.first_block + tile - a.n_tiles) * T + threadIdx.x);
     const int bins = 1 << a.bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int d = threadIdx.x; d < kSortWaves * bins; d += kSortThreads) cnt[d] = 0;
+    // the digits of all tiles for this thread's first bin, on their way while the tile's own are counted
+    constexpr int kAhead = 32;
+    int ahead[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        ahead[u] = u < a.n_tiles && int(threadIdx.x) < bins ? a.hist[int64_t(u) * bins + threadIdx.x] : 0;
+    for (int d = threadIdx.x; d < kWaves * bins; d += T) cnt[d] = 0;
     __syncthreads();
-    const int part = a.tile / kSortWaves, lo = tile * a.tile + wave * part;
+    const int part = a.tile / kWaves, lo = tile * a.tile + wave * part;
     int* mine = cnt + wave * bins;
-    for_keys<FIRST>(a, lo, part, lane, 64, [&](int p, int key) {
+    for_keys<FIRST, false>(a, lo, part, lane, 64, [&](int p, int key, int) {
         if (p < a.n) atomicAdd(&mine[key >> a.shift & (bins - 1)], 1);
     });
     __syncthreads();
     int carry = 0;
-    for (int d0 = 0; d0 < bins; d0 += kSortThreads) {
+    for (int d0 = 0; d0 < bins; d0 += T) {
         const int d = d0 + int(threadIdx.x);
         int before = 0, total = 0;
+        auto add = [&](int t, int h) {
+            total += h;
+            before += t < tile ? h : 0;
+        };
+        if (d0 == 0)
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) add(u, ahead[u]);
         if (d < bins) {
             constexpr int kUnroll = 16;
-            for (int t0 = 0; t0 < a.n_tiles; t0 += kUnroll) {
+            for (int t0 = d0 == 0 ? kAhead : 0; t0 < a.n_tiles; t0 += kUnroll) {
                 int h[kUnroll];
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) h[u] = t0 + u < a.n_tiles ? a.hist[int64_t(t0 + u) * bins + d] : 0;
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    total += h[u];
-                    before += t0 + u < tile ? h[u] : 0;
-                }
+                for (int u = 0; u < kUnroll; ++u) add(t0 + u, h[u]);
             }
         }
         int sum;
-        int at = carry + block_scan(total, red, sum) + before;
+        int at = carry + block_scan<kWaves>(total, red, sum) + before;
         carry += sum;
-        if (d < bins)
-            for (int w = 0; w < kSortWaves; ++w) {
-                const int c = cnt[w * bins + d];
+        if (d < bins) {
+            int c[kWaves];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) c[w] = cnt[w * bins + d];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
                 cnt[w * bins + d] = at;
-                at += c;
+                at += c[w];
             }
+        }
     }
     __syncthreads();
-    volatile int* place = mine;
-    for_keys<FIRST>(a, lo, part, lane, 64, [&](int p, int key) {
-        const bool live = p < a.n;
-        const int digit = key >> a.shift & (bins - 1);
-        uint64_t same = __ballot(live);
-        for (int b = 0; b < a.bits; ++b) {
-            const uint64_t m = __ballot(digit >> b & 1);
-            same &= digit >> b & 1 ? m : ~m;
+    for_keys<FIRST, true>(a, lo, part, lane, 64, [&](int p, int key, int pos) {
+        const int at = take_places(mine, key >> a.shift & (bins - 1), a.bits, p < a.n);
+        if (p < a.n) {
+            a.keys_out[at] = key;
+            a.pos_out[at] = pos;
         }
-        if (live) {
-            const int at = place[digit], rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-            __builtin_amdgcn_wave_barrier();  // every lane has read its place before the first of them moves it on
-            if (rank == 0) place[digit] = at + __popcll(same);
-            a.keys_out[at + rank] = key;
-            a.pos_out[at + rank] = FIRST ? p : a.pos_in[p];
-        }
-        __builtin_amdgcn_wave_barrier();
     });
 }
 
-template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_scatter(SortArgs a, FillArgs f) {
-    extern __shared__ int cnt[];
-    if (int(blockIdx.x) < a.n_tiles)
-        sort_scatter<FIRST>(a, blockIdx.x, cnt);
-    else
-        fill_zeros(f.grad, f.bytes, (f.first_block + blockIdx.x - a.n_tiles) * kSortThreads + threadIdx.x);
+// Up to kBlockIds ids into a table of fewer than 2^18 rows: both passes in one
+// block, between them in LDS.
+constexpr int kBlockThreads = 1024, kBlockWaves = kBlockThreads / 64, kBlockRounds = 4;
+constexpr int kBlockIds = kBlockThreads * kBlockRounds, kBlockBits = 9;
+
+__global__ __launch_bounds__(kBlockThreads) void k_sort_block(SortArgs a, int bits0, int bits1) {
+    __shared__ int cnt[kBlockWaves << kBlockBits];
+    __shared__ int skey[kBlockIds];
+    __shared__ uint16_t spos[kBlockIds];
+    __shared__ int red[kBlockWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rounds = (a.n + kBlockThreads - 1) / kBlockThreads, lo = wave * rounds * 64 + lane;
+    if (threadIdx.x == 0) *a.n_runs = 0;
+    int key[kBlockRounds], pos[kBlockRounds];
+#pragma unroll
+    for (int r = 0; r < kBlockRounds; ++r) {
+        pos[r] = lo + r * 64;
+        key[r] = r < rounds && pos[r] < a.n ? row_of(a.ids, a.id_type, pos[r], a.first, a.rows) : 0;
+    }
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        const int shift = pass ? bits0 : 0, bits = pass ? bits1 : bits0, bins = 1 << bits;
+        for (int d = threadIdx.x; d < kBlockWaves * bins; d += kBlockThreads) cnt[d] = 0;
+        __syncthreads();
+        int* mine = cnt + wave * bins;
+#pragma unroll
+        for (int r = 0; r < kBlockRounds; ++r)
+            if (r < rounds && lo + r * 64 < a.n) atomicAdd(&mine[key[r] >> shift & (bins - 1)], 1);
+        __syncthreads();
+        const int d = int(threadIdx.x);
+        int total = 0, sum;
+        int c[kBlockWaves];
+#pragma unroll
+        for (int w = 0; w < kBlockWaves; ++w) {
+            c[w] = d < bins ? cnt[w * bins + d] : 0;
+            total += c[w];
+        }
+        int at = block_scan<kBlockWaves>(total, red, sum);
+        if (d < bins)
+#pragma unroll
+            for (int w = 0; w < kBlockWaves; ++w) {
+                cnt[w * bins + d] = at;
+                at += c[w];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kBlockRounds; ++r) {
+            if (r < rounds) {
+                const bool live = lo + r * 64 < a.n;
+                const int to = take_places(mine, key[r] >> shift & (bins - 1), bits, live);
+                if (live && pass == 0) {
+                    skey[to] = key[r];
+                    spos[to] = uint16_t(pos[r]);
+                } else if (live) {
+                    a.keys_out[to] = key[r];
+                    a.pos_out[to] = pos[r];
+                }
+            }
+        }
+        if (pass == 0) {
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kBlockRounds; ++r) {
+                const int p = lo + r * 64;
+                if (r < rounds && p < a.n) {
+                    key[r] = skey[p];
+                    pos[r] = spos[p];
+                }
+            }
+        }
+    }
 }
 
 // Sums over the sorted order.  Work is cut into chunks of `chunk` sorted
@@ -491,13 +600,14 @@ template <bool FIRST> __global__ __launch_bounds__(kSortThreads) void k_sort_sca
 // piece for each chunk (slot 1 of the chunk it starts in, slot 0 of the
 // others), and k_embed_join adds the pieces in order.  kRunMax: without it
 // every border costs two rows of fp32 pieces, written and read.
-constexpr int kSumThreads = 256, kRunMax = 64;
+constexpr int kSumThreads = 256, kRunMax = 16;
 
 struct SumArgs {
     GradArgs g;
     const int *keys, *pos;
     float* parts;            // [n_chunks][2][width]
-    int *n_runs, *runs;      // the chunks where a long run starts, in no order
+    int* n_runs;
+    int2* runs;              // of each long run the chunk it starts in, and its row; in no order
     int width;               // columns rounded up to kPer
     int chunk, n_chunks;
 };
@@ -550,32 +660,47 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
         // a short run that started before the chunk has moved q0 past the chunk's end already
         if (!tail && q0 < q1) q1 = lower_bound(K, kRunMax + q1, win, kt + 1) - kRunMax;
     }
-    constexpr int kUnroll = 8;
+    // of ACC, what a finished row's sum is added to is on its way with the batch that finishes it
+    constexpr int kUnroll = ACC ? 4 : 8;
     float acc[kPer] = {};
     for (int q = q0; q < q1; q += kUnroll) {
         Raw<OD, kPer> x[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (q + u < q1)
-                x[u].template load<true>(a.dout + (int64_t(P[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width);
+        Raw<GD, kPer> old[ACC ? kUnroll : 1];
+        int key[kUnroll + 1];
+        key[0] = K[kRunMax + q];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (q + u >= q1) break;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] += x[u].get(k);
-            const int key = K[kRunMax + q + u];
-            if (q + u + 1 < q1 && K[kRunMax + q + u + 1] == key) continue;
-            if ((head && key == kf) || (tail && key == kt)) {
-                const int slot = head && key == kf ? 0 : 1;
-                float* o = s.parts + (int64_t(chunk) * 2 + slot) * s.width + c;
-                if (slot == 1 && c == 0) s.runs[atomicAdd(s.n_runs, 1)] = chunk;
-                reinterpret_cast<f32x4_t*>(o)[0] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
-                reinterpret_cast<f32x4_t*>(o)[1] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
-            } else {
-                write_row<GD, ACC>(a, key, c, width, acc);
+            key[u + 1] = q + u + 1 < q1 ? K[kRunMax + q + u + 1] : -1;
+            if (q + u < q1) {
+                x[u].template load<true>(a.dout + (int64_t(P[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width);
+                if constexpr (ACC)
+                    if (key[u + 1] != key[u])
+                        old[u].template load<false>(a.grad + (int64_t(key[u]) * a.cols + c) * Raw<GD, kPer>::kSize, width);
             }
+        }
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+        for (int u = 0; u < kUnroll; ++u) {
+            if (q + u < q1) {
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc[k] += x[u].get(k);
+            }
+            if (q + u < q1 && key[u + 1] != key[u]) {
+                if ((head && key[u] == kf) || (tail && key[u] == kt)) {
+                    const int slot = head && key[u] == kf ? 0 : 1;
+                    float* o = s.parts + (int64_t(chunk) * 2 + slot) * s.width + c;
+                    if (slot == 1 && c == 0) s.runs[atomicAdd(s.n_runs, 1)] = make_int2(chunk, key[u]);
+                    reinterpret_cast<f32x4_t*>(o)[0] = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+                    reinterpret_cast<f32x4_t*>(o)[1] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
+                } else {
+                    float v[kPer];
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k)
+                        v[k] = ACC ? __builtin_fmaf(a.scale, acc[k], old[ACC ? u : 0].get(k)) : a.scale * acc[k];
+                    store<GD, kPer, true>(a.grad + (int64_t(key[u]) * a.cols + c) * Raw<GD, kPer>::kSize, width, v);
+                }
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+            }
         }
     }
 }
@@ -583,7 +708,7 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
 // The long runs, one at a time to a block: its pieces are added in order (each
 // group a stretch of them, then the groups).  The list's order differs from
 // run to run, the sums do not.
-constexpr int kJoinThreads = 512, kJoinBlocks = 512;
+constexpr int kJoinThreads = 256, kJoinBlocks = 1024;
 
 template <int GD, bool ACC> __global__ __launch_bounds__(kJoinThreads) void k_embed_join(SumArgs s) {
     __shared__ float red[kJoinThreads * kPer];
@@ -595,7 +720,7 @@ template <int GD, bool ACC> __global__ __launch_bounds__(kJoinThreads) void k_em
     const int width = a.cols - c < kPer ? a.cols - c : kPer;
     const int n_runs = *s.n_runs;
     for (int r = blockIdx.x; r < n_runs; r += int(gridDim.x)) {
-        const int chunk = s.runs[r], key = s.keys[int64_t(chunk + 1) * s.chunk - 1];
+        const int chunk = s.runs[r].x, key = s.runs[r].y;
         __syncthreads();
         if (t == 0) more = 0;
         __syncthreads();
@@ -608,15 +733,25 @@ template <int GD, bool ACC> __global__ __launch_bounds__(kJoinThreads) void k_em
         const int share = (pieces + groups - 1) / groups, lo = g * share, hi = lo + share < pieces ? lo + share : pieces;
         float acc[kPer] = {};
         if (width > 0) {
-#pragma unroll 4
-            for (int j = lo; j < hi; ++j) {
-                const float* o = s.parts + (int64_t(chunk + j) * 2 + (j == 0 ? 1 : 0)) * s.width + c;
-                const f32x4_t x = reinterpret_cast<const f32x4_t*>(o)[0], y = reinterpret_cast<const f32x4_t*>(o)[1];
+            constexpr int kUnroll = 8;
+            for (int j = lo; j < hi; j += kUnroll) {
+                f32x4_t x[kUnroll], y[kUnroll];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[k] += x[k];
-                    acc[4 + k] += y[k];
+                for (int u = 0; u < kUnroll; ++u) {
+                    const float* o = s.parts + (int64_t(chunk + j + u) * 2 + (j + u == 0 ? 1 : 0)) * s.width + c;
+                    x[u] = y[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    if (j + u < hi) {
+                        x[u] = reinterpret_cast<const f32x4_t*>(o)[0];
+                        y[u] = reinterpret_cast<const f32x4_t*>(o)[1];
+                    }
                 }
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        acc[k] += x[u][k];
+                        acc[4 + k] += y[u][k];
+                    }
             }
         }
         add_groups<kJoinThreads>(red, a.group_shift, acc);
@@ -639,7 +774,7 @@ int pick_group(int words, int most_shift) {
 
 // How a gradient of n ids is cut, and where its workspace regions lie.
 struct GradShape {
-    bool few;
+    bool few, block;         // which way the ids are grouped: by search, by one block's sort, else by launches
     int group_shift, slabs, width;
     int bits[2], tile, n_tiles, chunk, n_chunks;
     uint64_t keys[2], pos[2], hist, runs, parts, total;
@@ -657,13 +792,15 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     while ((int64_t(1) << bits) <= e.rows) ++bits;
     s.bits[0] = (bits + 1) / 2;
     s.bits[1] = bits - s.bits[0];
-    // at least 2048 positions a tile (every wave has four of each lane's in
-    // flight), at most 128 tiles (each adds up the digits of all others)
-    s.tile = int(std::max<int64_t>(2048, (n + 128 * kSortThreads - 1) / (128 * kSortThreads) * kSortThreads));
+    s.block = n <= kBlockIds && bits <= 2 * kBlockBits;
+    // at least 2048 positions a tile, at most 128 tiles (each adds up the
+    // digits of all others)
+    s.tile = int(std::max<int64_t>(2048, (n + 128 * 512 - 1) / (128 * 512) * 512));
     s.n_tiles = int((n + s.tile - 1) / s.tile);
-    // the longest chunk that still makes 4096 waves (16 a CU)
+    // the longest chunk that still makes 2048 waves (8 a CU; 65536 ids of 768
+    // columns take 73.6 us so, 75.7 with 4096 or 8192 waves, 94 with 1024)
     s.chunk = s.group_shift < 5 ? 64 : 256;
-    while (s.chunk > 16 && ((n / s.chunk * s.slabs) << s.group_shift) / 64 < 4096) s.chunk /= 2;
+    while (s.chunk > 16 && ((n / s.chunk * s.slabs) << s.group_shift) / 64 < 2048) s.chunk /= 2;
     s.n_chunks = int((n + s.chunk - 1) / s.chunk);
     uint64_t off = 0;
     auto region = [&](uint64_t bytes) {
@@ -676,7 +813,7 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
         s.pos[k] = region(uint64_t(n) * 4);
     }
     s.hist = region((uint64_t(s.n_tiles) * 4) << std::max(s.bits[0], s.bits[1]));
-    s.runs = region((uint64_t(s.n_chunks) + 1) * 4);  // their number, then the list
+    s.runs = region((uint64_t(s.n_chunks) + 1) * 8);  // their number, then the list
     s.parts = region(uint64_t(s.n_chunks) * 2 * uint64_t(s.width) * 4);
     s.total = off;
     return s;
@@ -726,7 +863,7 @@ namespace {
 template <int TD, int OD> hipError_t launch_lookup(LookupArgs a, hipStream_t stream) {
     constexpr int N = TD == kF32 && OD == kF32 ? 4 : 8;
     const int words = (a.cols + N - 1) / N;
-    a.group_shift = pick_group(words, 8);
+    a.group_shift = pick_group(words, 9);
     const uint32_t slabs = uint32_t((words + (1 << a.group_shift) - 1) >> a.group_shift);
     const int64_t rows = kLookupThreads >> a.group_shift, blocks = (a.n + rows - 1) / rows;
     for (int64_t first = 0; first < blocks; first += kBlocksMax)
@@ -761,6 +898,40 @@ template <int OD, int GD, bool ACC> hipError_t launch_few(const GradArgs& a, hip
     return hipGetLastError();
 }
 
+// The sort in four launches, each with a quarter of the zeros.
+template <int T>
+hipError_t launch_sort(SortArgs t, const GradShape& s, uint8_t* ws, uint8_t* grad, int64_t bytes, hipStream_t stream) {
+    auto ints = [&](uint64_t off) { return reinterpret_cast<int*>(ws + off); };
+    FillArgs f = {grad, bytes, 0};
+    int64_t fill = (bytes + T * 16 - 1) / (T * 16);
+    if (fill > kBlocksMax) {  // 34 GB (256 threads): more than a launch holds
+        if (hipError_t e = zero_table(grad, bytes, stream); e != hipSuccess) return e;
+        fill = 0;
+    }
+    const int64_t part = (fill + 3) / 4;
+    auto grid = [&] { return dim3(uint32_t(s.n_tiles + std::max<int64_t>(0, std::min(part, fill - f.first_block)))); };
+    for (int pass = 0; pass < 2; ++pass) {
+        t.shift = pass ? s.bits[0] : 0;
+        t.bits = s.bits[pass];
+        t.keys_in = ints(s.keys[0]);
+        t.pos_in = ints(s.pos[0]);
+        t.keys_out = ints(s.keys[pass]);
+        t.pos_out = ints(s.pos[pass]);
+        const size_t row = size_t(4) << t.bits;
+        if (pass == 0)
+            k_sort_count<true, T><<<grid(), dim3(T), row, stream>>>(t, f);
+        else
+            k_sort_count<false, T><<<grid(), dim3(T), row, stream>>>(t, f);
+        f.first_block += part;
+        if (pass == 0)
+            k_sort_scatter<true, T><<<grid(), dim3(T), row * (T / 64), stream>>>(t, f);
+        else
+            k_sort_scatter<false, T><<<grid(), dim3(T), row * (T / 64), stream>>>(t, f);
+        f.first_block += part;
+    }
+    return hipGetLastError();
+}
+
 template <int OD, int GD, bool ACC>
 hipError_t launch_sorted(const GradArgs& a, const GradShape& s, uint8_t* ws, hipStream_t stream) {
     auto ints = [&](uint64_t off) { return reinterpret_cast<int*>(ws + off); };
@@ -774,41 +945,27 @@ hipError_t launch_sorted(const GradArgs& a, const GradShape& s, uint8_t* ws, hip
     t.n_tiles = s.n_tiles;
     t.hist = ints(s.hist);
     t.n_runs = ints(s.runs);
-    t.shift = 0;
-    t.bits = s.bits[0];
-    t.keys_out = ints(s.keys[0]);
-    t.pos_out = ints(s.pos[0]);
-    // the four launches of the sort, each with a quarter of the zeros
-    FillArgs f = {a.grad, ACC ? 0 : int64_t(a.rows) * a.cols * Raw<GD, kPer>::kSize, 0};
-    int64_t fill = (f.bytes + kSortThreads * 16 - 1) / (kSortThreads * 16);
-    if (fill > 2 * kBlocksMax) {  // 137 GB: more than four launches hold
-        if (hipError_t e = zero_table(a.grad, f.bytes, stream); e != hipSuccess) return e;
-        fill = 0;
+    const int64_t bytes = ACC ? 0 : int64_t(a.rows) * a.cols * Raw<GD, kPer>::kSize;
+    if (s.block) {
+        if (bytes > 0)
+            if (hipError_t e = zero_table(a.grad, bytes, stream); e != hipSuccess) return e;
+        t.keys_out = ints(s.keys[1]);
+        t.pos_out = ints(s.pos[1]);
+        k_sort_block<<<dim3(1), dim3(kBlockThreads), 0, stream>>>(t, s.bits[0], s.bits[1]);
+    } else {
+        // 256 threads clear faster (6.7 TB/s in four launches, 6.2 with 512), 512 sort faster
+        if (hipError_t e = ACC ? launch_sort<512>(t, s, ws, a.grad, bytes, stream) : launch_sort<256>(t, s, ws, a.grad, bytes, stream);
+            e != hipSuccess)
+            return e;
     }
-    const int64_t quarter = (fill + 3) / 4;
-    auto grid = [&] { return dim3(uint32_t(s.n_tiles + std::max<int64_t>(0, std::min(quarter, fill - f.first_block)))); };
-    const size_t lds0 = size_t(4) << s.bits[0], lds1 = size_t(4) << s.bits[1];
-    k_sort_count<true><<<grid(), dim3(kSortThreads), lds0, stream>>>(t, f);
-    f.first_block += quarter;
-    k_sort_scatter<true><<<grid(), dim3(kSortThreads), lds0 * kSortWaves, stream>>>(t, f);
-    f.first_block += quarter;
-    t.shift = s.bits[0];
-    t.bits = s.bits[1];
-    t.keys_in = t.keys_out;
-    t.pos_in = t.pos_out;
-    t.keys_out = ints(s.keys[1]);
-    t.pos_out = ints(s.pos[1]);
-    k_sort_count<false><<<grid(), dim3(kSortThreads), lds1, stream>>>(t, f);
-    f.first_block += quarter;
-    k_sort_scatter<false><<<grid(), dim3(kSortThreads), lds1 * kSortWaves, stream>>>(t, f);
     SumArgs u = {};
     u.g = a;
-    u.keys = t.keys_out;
-    u.pos = t.pos_out;
+    u.keys = ints(s.keys[1]);
+    u.pos = ints(s.pos[1]);
     u.parts = reinterpret_cast<float*>(ws + s.parts);
     u.width = s.width;
     u.n_runs = ints(s.runs);
-    u.runs = u.n_runs + 1;
+    u.runs = reinterpret_cast<int2*>(u.n_runs) + 1;
     u.chunk = s.chunk;
     u.n_chunks = s.n_chunks;
     const int groups = kSumThreads >> a.group_shift;

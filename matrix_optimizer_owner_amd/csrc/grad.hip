@@ -190,8 +190,13 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
     for (int k = int(threadIdx.x >> 4); k < a.n_large; k += kNormThreads / 16) {
         const int e = a.large[k], b1 = a.entry_begin[e + 1];
         double t = 0.0;
-#pragma unroll 4
-        for (int i = a.entry_begin[e] + lane; i < b1; i += 16) t += get_partial(a.partials + i);
+        for (int i = a.entry_begin[e] + lane; i < b1; i += 16 * kNormFew) {
+            double v[kNormFew];
+#pragma unroll
+            for (int u = 0; u < kNormFew; ++u) v[u] = i + 16 * u < b1 ? get_partial(a.partials + i + 16 * u) : 0.0;
+#pragma unroll
+            for (int u = 0; u < kNormFew; ++u) t += v[u];
+        }
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) t += __shfl_xor(t, off, 16);
         if (lane == 0) a.entry_norms[e] = float(sqrt(t));

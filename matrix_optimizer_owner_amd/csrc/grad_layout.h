@@ -52,7 +52,7 @@ constexpr int64_t kGradChunkMax = int64_t(1) << 30;
 // that many small tensors spread over more blocks.  One share for every
 // kNormShareMin of cost, at most kNormBlocks.
 constexpr int64_t kNormPieceCost = 2;
-constexpr int64_t kNormShareMin = 4;
+constexpr int64_t kNormShareMin = 8;
 constexpr int64_t kNormBlocks = 1024;
 constexpr int kNormFew = 8;
 constexpr uint32_t kNormGroups = 32;
