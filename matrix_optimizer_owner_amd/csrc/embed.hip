@@ -272,12 +272,13 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) vo
 }
 
 // The same with the zeros of the other rows beside it: a block has `span`
-// whole rows of at most kFewThreads words, or a piece of kFewThreads words of
-// one longer row, and looks through the ids for its rows first.  A word that
-// two rows share is the first one's.  One launch instead of two saves 3 us on
-// a small table; a large one clears faster without the ids (kFewBytes).
-constexpr int kFewSpanIds = 512, kFewSpanRows = 1024;
-constexpr int64_t kFewBytes = int64_t(32) << 20;
+// whole rows of at most kSpanWords words, or a piece of that many of one
+// longer row, and looks through the ids for its rows first.  A word that two
+// rows share is the first one's.  One launch instead of two saves 3 us on a
+// small table (500 ids into 61 MB: 12.6 us, 15.3 apart); past kFewBytes
+// clearing without looking at ids wins (1.05 GB: 195 us, 183 apart).
+constexpr int kFewSpanIds = 512, kSpanWords = kFewThreads * 2, kSpanRows = 1024;
+constexpr int64_t kFewBytes = int64_t(128) << 20;
 
 struct SpanArgs {
     int span, pieces;        // rows of a block, or blocks of a row
@@ -286,35 +287,41 @@ struct SpanArgs {
 
 template <int GD> __device__ __forceinline__ void fill_span(const GradArgs& a, const SpanArgs& s, int block) {
     constexpr int kElems = GD == kBF16 ? 8 : 4, kSize = 16 / kElems;
-    __shared__ uint8_t hit[kFewSpanRows + 4];
+    __shared__ uint8_t hit[kSpanRows + 4];
     const int g = block / s.pieces, piece = block - g * s.pieces, r0 = g * s.span;
     const int r1 = a.rows - r0 < s.span ? a.rows : r0 + s.span;
-    for (int r = threadIdx.x; r <= s.span; r += kFewThreads) hit[r] = 0;
-    __syncthreads();
+    int row[kFewSpanIds / kFewThreads];
 #pragma unroll
     for (int k = 0; k < kFewSpanIds / kFewThreads; ++k) {
         const int p = k * kFewThreads + int(threadIdx.x);
-        if (p < a.n) {
-            const int r = row_of(a.ids, a.id_type, p, a.first, a.rows);
-            if (r >= r0 && r <= r1 && r < a.rows) hit[r - r0] = 1;
-        }
+        row[k] = p < a.n ? row_of(a.ids, a.id_type, p, a.first, a.rows) : a.rows;
     }
+    for (int r = threadIdx.x; r <= s.span; r += kFewThreads) hit[r] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kFewSpanIds / kFewThreads; ++k)
+        if (row[k] >= r0 && row[k] <= r1 && row[k] < a.rows) hit[row[k] - r0] = 1;
     __syncthreads();
     const int64_t total = int64_t(a.rows) * a.cols, begin = int64_t(r0) * a.cols, end = int64_t(r1) * a.cols;
-    const int64_t e = ((begin + kElems - 1) / kElems + int64_t(piece) * kFewThreads + threadIdx.x) * kElems;
-    if (e >= end) return;
-    uint32_t x = uint32_t(e - begin), r = x / uint32_t(a.cols), c = x - r * uint32_t(a.cols);
-    if (c + kElems <= uint32_t(a.cols)) {  // a word of one row
-        if (!hit[r]) *reinterpret_cast<u32x4_t*>(a.grad + e * kSize) = u32x4_t{0u, 0u, 0u, 0u};
-        return;
-    }
-    // a word over a row's end reaches into one more row (rows are at least a word wide here), at most into r1,
-    // whose ids were looked for too
-    for (int k = 0; k < kElems && e + k < total; ++k) {
-        if (!hit[r]) store_elem(a.grad, GD, e + k, 0.f);
-        if (++c == uint32_t(a.cols)) {
-            c = 0;
-            ++r;
+    const int64_t first = (begin + kElems - 1) / kElems + int64_t(piece) * kSpanWords + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kSpanWords / kFewThreads; ++k) {
+        const int64_t e = (first + k * kFewThreads) * kElems;
+        if (e >= end) return;
+        const uint32_t x = uint32_t(e - begin);
+        uint32_t r = x / uint32_t(a.cols), c = x - r * uint32_t(a.cols);
+        if (c + kElems <= uint32_t(a.cols)) {  // a word of one row
+            if (!hit[r]) *reinterpret_cast<u32x4_t*>(a.grad + e * kSize) = u32x4_t{0u, 0u, 0u, 0u};
+            continue;
+        }
+        // a word over a row's end reaches into one more row (rows are at least a word wide here), at most into
+        // r1, whose ids were looked for too
+        for (int j = 0; j < kElems && e + j < total; ++j) {
+            if (!hit[r]) store_elem(a.grad, GD, e + j, 0.f);
+            if (++c == uint32_t(a.cols)) {
+                c = 0;
+                ++r;
+            }
         }
     }
 }
@@ -881,11 +888,11 @@ hipError_t zero_table(uint8_t* grad, int64_t bytes, hipStream_t stream) {
 
 template <int OD, int GD, bool ACC> hipError_t launch_few(const GradArgs& a, hipStream_t stream) {
     if constexpr (!ACC) {
-        constexpr int kSize = Raw<GD, kPer>::kSize, kElems = 16 / kSize * kFewThreads;
+        constexpr int kSize = Raw<GD, kPer>::kSize, kElems = 16 / kSize * kSpanWords;
         const int64_t bytes = int64_t(a.rows) * a.cols * kSize;
         if (a.n <= kFewSpanIds && bytes <= kFewBytes && a.cols >= 16 / kSize) {
             SpanArgs s;
-            s.span = std::clamp(kElems / a.cols, 1, kFewSpanRows);
+            s.span = std::clamp(kElems / a.cols, 1, kSpanRows);
             s.pieces = s.span > 1 ? 1 : (a.cols + kElems - 1) / kElems;
             s.few_blocks = a.n * a.slabs;
             const int blocks = s.few_blocks + (a.rows + s.span - 1) / s.span * s.pieces;
