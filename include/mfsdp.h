@@ -262,7 +262,8 @@ mfsdp_status mfsdp_plan_destroy(mfsdp_plan_t plan);
  * (mfsdp_grad_clip) or formed as the step reads it (mfsdp_owner_step_scaled,
  * which moves no byte more than mfsdp_owner_step).  The scale stays on the
  * device throughout: nothing here synchronises, and every call below can be
- * captured into a graph once its descriptors are resident.
+ * captured into a graph once its descriptors are resident.  As for
+ * mfsdp_owner_step, the current device must be the stream's and the buffers'.
  *
  * Squares and sums are fp64 in a fixed order: results are bitwise the same
  * from run to run, and no finite gradient overflows or vanishes in them.
@@ -281,8 +282,11 @@ typedef struct mfsdp_grad_stats {
 } mfsdp_grad_stats;
 
 /* Device workspace of mfsdp_grad_norm and mfsdp_grad_clip on this plan's
- * table (descriptors and partial sums; separate from the step's).  It may
- * serve any number of calls, one at a time. */
+ * table (descriptors, partial sums and the norm's counters; separate from the
+ * step's).  It may serve any number of calls, one at a time: two calls that
+ * overlap (two streams, two graphs) need a workspace each.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (a table of more than 2^31 - 1 work
+ * items). */
 mfsdp_status mfsdp_plan_grad_workspace_bytes(mfsdp_plan_t plan, uint64_t* bytes);
 
 typedef struct mfsdp_grad_norm_args {
@@ -303,8 +307,8 @@ typedef struct mfsdp_grad_norm_args {
 
 /* Enqueue the norm pass.  An empty table gives norm 0 and scale 1.
  * Errors: INVALID_ARGUMENT (null pointer, misaligned buffer, max_norm or eps
- * out of range, unknown flag), WORKSPACE_TOO_SMALL, UNSUPPORTED (a table of
- * more than 2^31 - 1 work chunks), HIP. */
+ * out of range, unknown flag), WORKSPACE_TOO_SMALL, UNSUPPORTED (as above),
+ * HIP. */
 mfsdp_status mfsdp_grad_norm(mfsdp_plan_t plan, const mfsdp_grad_norm_args* args);
 
 /* Join the records of several owners: stats->sumsq = the sum of parts[0..count)
@@ -356,10 +360,12 @@ mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* a
  * An id outside first_id .. first_id + rows - 1 has a zero row in the
  * lookup and no part in the gradient: a vocabulary cut into several entries
  * is looked up in each with its own first_id and the results added, and a
- * negative id marks padding.  Sums are fp32, formed in an order that depends
- * on the ids and sizes alone (bitwise the same from run to run, no atomics on
- * values), multiplied by scale in fp32, and rounded once to the entry's
- * type. */
+ * negative id marks padding.  Whatever dout holds at such a position (NaN
+ * too) is not read into a result.  Sums are fp32, formed in an order that
+ * depends on the ids and sizes alone (bitwise the same from run to run, no
+ * atomics on values), multiplied by scale in fp32, and rounded once to the
+ * entry's type.  Both calls only enqueue launches on the stream, so they can
+ * be captured; the current device must be the stream's and the buffers'. */
 typedef enum mfsdp_id_type {
     MFSDP_I32 = 0,
     MFSDP_I64 = 1
@@ -385,8 +391,9 @@ typedef struct mfsdp_embed_lookup_args {
  * (id_type, out_type), HIP. */
 mfsdp_status mfsdp_embed_lookup(mfsdp_plan_t plan, int64_t entry, const mfsdp_embed_lookup_args* args);
 
-/* Device workspace of mfsdp_embed_grad for up to n_ids ids (it grows with
- * n_ids; 0 ids need 0 bytes).  Errors: INVALID_ARGUMENT. */
+/* Device workspace of mfsdp_embed_grad for up to n_ids ids: it never falls as
+ * n_ids grows, so one for the largest batch serves every smaller one.  Small
+ * batches need 0 bytes.  Errors: INVALID_ARGUMENT. */
 mfsdp_status mfsdp_plan_embed_workspace_bytes(mfsdp_plan_t plan, int64_t entry, int64_t n_ids, uint64_t* bytes);
 
 typedef struct mfsdp_embed_grad_args {

@@ -804,11 +804,17 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     // digits of all others)
     s.tile = int(std::max<int64_t>(2048, (n + 128 * 512 - 1) / (128 * 512) * 512));
     s.n_tiles = int((n + s.tile - 1) / s.tile);
-    // the longest chunk that still makes 2048 waves (8 a CU; 65536 ids of 768
-    // columns take 73.6 us so, 75.7 with 4096 or 8192 waves, 94 with 1024)
-    s.chunk = s.group_shift < 5 ? 64 : 256;
-    while (s.chunk > 16 && ((n / s.chunk * s.slabs) << s.group_shift) / 64 < 2048) s.chunk /= 2;
-    s.n_chunks = int((n + s.chunk - 1) / s.chunk);
+    // The longest chunk that still makes 2048 waves (8 a CU; 65536 ids of 768
+    // columns take 73.6 us so, 75.7 with 4096 or 8192 waves, 94 with 1024).
+    auto parts = [&](int64_t len) { return (n + len - 1) / len; };
+    const int longest = s.group_shift < 5 ? 64 : 256;
+    const int64_t most = std::max<int64_t>(1, (int64_t(2 * 2048) * 64 >> s.group_shift) / s.slabs);
+    s.chunk = 16;
+    while (s.chunk < longest && parts(s.chunk) > most) s.chunk *= 2;
+    s.n_chunks = int(parts(s.chunk));
+    // a workspace for n ids serves fewer of them too: regions are sized by what any smaller batch may need
+    const uint64_t max_chunks = uint64_t(std::min(parts(16), std::max(most, parts(longest))));
+    const uint64_t max_tiles = uint64_t(std::min<int64_t>(128, parts(2048)));
     uint64_t off = 0;
     auto region = [&](uint64_t bytes) {
         const uint64_t at = off;
@@ -819,9 +825,9 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
         s.keys[k] = region(uint64_t(n) * 4);
         s.pos[k] = region(uint64_t(n) * 4);
     }
-    s.hist = region((uint64_t(s.n_tiles) * 4) << std::max(s.bits[0], s.bits[1]));
-    s.runs = region((uint64_t(s.n_chunks) + 1) * 8);  // their number, then the list
-    s.parts = region(uint64_t(s.n_chunks) * 2 * uint64_t(s.width) * 4);
+    s.hist = region((max_tiles * 4) << std::max(s.bits[0], s.bits[1]));
+    s.runs = region((max_chunks + 1) * 8);  // their number, then the list
+    s.parts = region(max_chunks * 2 * uint64_t(s.width) * 4);
     s.total = off;
     return s;
 }

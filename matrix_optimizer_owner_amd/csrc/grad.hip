@@ -126,8 +126,9 @@ __device__ __forceinline__ bool last_to_finish(uint32_t* counters) {
 }
 
 struct NormArgs {
+    const NormBlock* blocks;
     const GradRun* pieces;
-    const int32_t *block_begin, *entry_begin, *large;
+    const int32_t *entry_begin, *large;
     const uint8_t* grads;
     double* partials;
     uint32_t* counters;
@@ -144,23 +145,37 @@ struct NormArgs {
 __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
     __shared__ double red[kNormWaves];
     __shared__ bool last;
-    if (a.n_pieces > 0) {
-        const int p1 = a.block_begin[blockIdx.x + 1];
-        for (int p = a.block_begin[blockIdx.x]; p < p1; ++p) {
-            const GradRun r = a.pieces[p];
-            double s[2] = {0.0, 0.0};
-            if (r.dtype == kBF16)
-                run_squares<kBF16>(a.grads + r.off, r.numel, s);
-            else
-                run_squares<kF32>(a.grads + r.off, r.numel, s);
-            const double sum = block_sum(s[0] + s[1], red);
-            if (threadIdx.x == 0) put_partial(a.partials + p, sum);
-        }
+    const NormBlock b = a.blocks[blockIdx.x];
+    GradRun r = b.first;
+    for (int p = b.begin; p < b.end; ++p) {
+        GradRun next = r;
+        if (p + 1 < b.end) next = a.pieces[p + 1];
+        double s[2] = {0.0, 0.0};
+        if (r.dtype == kBF16)
+            run_squares<kBF16>(a.grads + r.off, r.numel, s);
+        else
+            run_squares<kF32>(a.grads + r.off, r.numel, s);
+        const double sum = block_sum(s[0] + s[1], red);
+        if (threadIdx.x == 0) put_partial(a.partials + p, sum);
+        r = next;
     }
     if (threadIdx.x == 0) last = last_to_finish(a.counters);
     __syncthreads();
     if (!last) return;
 
+    // an entry of at most kNormFew pieces is one thread's; the first 512 start on their way before the total's sum
+    auto small_entry = [&](int e, int b0, int b1) {
+        if (e >= a.n_entries || b1 - b0 > kNormFew) return;
+        double v[kNormFew], t = 0.0;
+#pragma unroll
+        for (int k = 0; k < kNormFew; ++k) v[k] = b0 + k < b1 ? get_partial(a.partials + b0 + k) : 0.0;
+#pragma unroll
+        for (int k = 0; k < kNormFew; ++k) t += v[k];
+        a.entry_norms[e] = float(sqrt(t));
+    };
+    const int e0 = threadIdx.x;
+    const bool mine = a.entry_norms && e0 < a.n_entries;
+    const int b0 = mine ? a.entry_begin[e0] : 0, b1 = mine ? a.entry_begin[e0 + 1] : 0;
     double s = 0.0;
     for (int i = threadIdx.x; i < a.n_pieces; i += kNormThreads * kNormUnroll) {
         double v[kNormUnroll];
@@ -170,20 +185,11 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
 #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) s += v[u];
     }
+    if (mine) small_entry(e0, b0, b1);
     s = block_sum(s, red);
     if (threadIdx.x == 0) write_stats(a.stats, s, a.max_norm, a.eps);
     if (!a.entry_norms) return;
-    // an entry of at most kNormFew pieces is one thread's
-    for (int e = threadIdx.x; e < a.n_entries; e += kNormThreads) {
-        const int b0 = a.entry_begin[e], b1 = a.entry_begin[e + 1];
-        if (b1 - b0 > kNormFew) continue;
-        double v[kNormFew], t = 0.0;
-#pragma unroll
-        for (int k = 0; k < kNormFew; ++k) v[k] = b0 + k < b1 ? get_partial(a.partials + b0 + k) : 0.0;
-#pragma unroll
-        for (int k = 0; k < kNormFew; ++k) t += v[k];
-        a.entry_norms[e] = float(sqrt(t));
-    }
+    for (int e = e0 + kNormThreads; e < a.n_entries; e += kNormThreads) small_entry(e, a.entry_begin[e], a.entry_begin[e + 1]);
     // one of more is 16 lanes', 32 entries at a time (a wave for each took 35
     // us for the 28 matrices of the 1.7 GB share)
     const int lane = int(threadIdx.x & 15);
@@ -302,7 +308,7 @@ extern "C" mfsdp_status mfsdp_grad_norm(mfsdp_plan_t plan, const mfsdp_grad_norm
     uint8_t* ws = static_cast<uint8_t*>(args->workspace);
     NormArgs a;
     a.pieces = reinterpret_cast<const GradRun*>(ws + t->off_pieces);
-    a.block_begin = reinterpret_cast<const int32_t*>(ws + t->off_block_begin);
+    a.blocks = reinterpret_cast<const NormBlock*>(ws + t->off_blocks);
     a.entry_begin = reinterpret_cast<const int32_t*>(ws + t->off_entry_begin);
     a.grads = static_cast<const uint8_t*>(args->grads);
     a.partials = reinterpret_cast<double*>(ws + t->off_partials);
@@ -315,7 +321,7 @@ extern "C" mfsdp_status mfsdp_grad_norm(mfsdp_plan_t plan, const mfsdp_grad_norm
     a.n_entries = t->n_entries;
     a.large = reinterpret_cast<const int32_t*>(ws + t->off_large);
     a.n_large = t->n_large;
-    k_grad_norm<<<dim3(std::max(t->n_blocks, 1)), dim3(kNormThreads), 0, static_cast<hipStream_t>(args->stream)>>>(a);
+    k_grad_norm<<<dim3(t->n_blocks), dim3(kNormThreads), 0, static_cast<hipStream_t>(args->stream)>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return hip_fail(e, "gradient norm launch");
     return MFSDP_OK;
 }

@@ -2,8 +2,8 @@
 // lowering (grad_plan.cpp) and the kernels (grad.hip).
 //
 // Workspace map (byte offsets, 256-byte aligned):
-//   [desc]      GradRun[n_chunks] (clipping), GradRun[n_pieces] and int32
-//               block_begin[n_blocks + 1], entry_begin[n_entries + 1] and
+//   [desc]      GradRun[n_chunks] (clipping), NormBlock[n_blocks],
+//               GradRun[n_pieces], int32 entry_begin[n_entries + 1] and
 //               large[n_large] (norm), and the norm's counters of finished
 //               blocks (0 between calls): kNormGroups + 1 uint32 at a pitch of
 //               kNormCounterPitch
@@ -25,18 +25,26 @@ struct GradRun {
 };
 static_assert(sizeof(GradRun) == 24, "GradRun layout");
 
+// A block's share of the norm: pieces begin .. end-1, the first one here too,
+// so that a block of one piece starts on it a load earlier.
+struct NormBlock {
+    GradRun first;
+    int32_t begin, end;
+};
+static_assert(sizeof(NormBlock) == 32, "NormBlock layout");
+
 struct GradTables {
     std::vector<uint8_t> blob;  // [desc], uploaded by one copy
-    uint64_t off_pieces = 0, off_block_begin = 0, off_entry_begin = 0, off_large = 0, off_counters = 0,
+    uint64_t off_blocks = 0, off_pieces = 0, off_entry_begin = 0, off_large = 0, off_counters = 0,
              off_partials = 0;
     uint64_t total_bytes = 0;
     int32_t n_entries = 0;
     // Clipping: chunk c is 2^slice_shift slices of kGradSlice bytes (its last
     // ones may be empty), one slice a block.
     int32_t n_chunks = 0, slice_shift = 0;
-    // The norm: block b sums pieces block_begin[b] .. block_begin[b+1]-1, which
-    // cut the table into n_blocks shares of the same cost (a piece ends where
-    // its share or its entry does).  Entry e is pieces entry_begin[e] ..
+    // The norm: the blocks' pieces cut the table into n_blocks shares of the
+    // same cost (a piece ends where its share or its entry does; an empty table
+    // has one block of no piece).  Entry e is pieces entry_begin[e] ..
     // entry_begin[e+1]-1; `large` are the entries of more than kNormFew.
     int32_t n_pieces = 0, n_blocks = 0, n_large = 0;
 };

@@ -51,7 +51,11 @@ std::unique_ptr<GradTables> lower(const mfsdp_plan_s& plan) {
     t->n_entries = int32_t(plan.entries.size());
     t->n_chunks = int32_t(chunks.size());
     t->n_pieces = int32_t(pieces.size());
-    t->n_blocks = int32_t(block_begin.size()) - 1;
+    std::vector<NormBlock> blocks;
+    for (size_t b = 0; b + 1 < block_begin.size(); ++b)
+        blocks.push_back(NormBlock{pieces[size_t(block_begin[b])], block_begin[b], block_begin[b + 1]});
+    if (blocks.empty()) blocks.push_back(NormBlock{});
+    t->n_blocks = int32_t(blocks.size());
     t->n_large = int32_t(large.size());
     uint64_t off = 0;
     auto put = [&](const auto& v) {
@@ -62,8 +66,8 @@ std::unique_ptr<GradTables> lower(const mfsdp_plan_s& plan) {
         return at;
     };
     put(chunks);
+    t->off_blocks = put(blocks);
     t->off_pieces = put(pieces);
-    t->off_block_begin = put(block_begin);
     t->off_entry_begin = put(entry_begin);
     t->off_large = put(large);
     t->off_counters = put(std::vector<uint32_t>((kNormGroups + 1) * kNormCounterPitch, 0));

@@ -68,6 +68,9 @@ def _ids(kind, n, rows, first, rng):
         r = rng.choice([0, rows - 1], n)
     elif kind == "falling":
         r = (np.arange(n)[::-1] * rows) // max(n, 1)
+    elif kind == "lengths":  # row k has k % 40 + 1 positions, anywhere
+        r = np.repeat(np.arange(rows), np.arange(rows) % 40 + 1)
+        r = rng.permutation(np.resize(r, n))
     elif kind == "outside":
         return rng.choice([first - 1, first + rows, -1, -(1 << 31), (1 << 31) - 1], n)
     else:
@@ -191,6 +194,22 @@ GRADS = [  # rows, cols, n, table, dout, ids, kind, scale, stride pad, shift
     (129, 9, 131073, F, F, B.I64, "mixed", 1.0, 0, 0),
     (1 << 21, 1, 12000, F, F, B.I64, "any", 1.0, 0, 0),
     (1 << 22, 2, 40000, BF, BF, B.I32, "zipf", 1.0, 0, 0),
+    (500, 515, 512, BF, BF, B.I64, "zipf", 1.0, 0, 0),
+    (500, 515, 513, BF, BF, B.I64, "zipf", 1.0, 0, 0),
+    (90, 12, 511, F, F, B.I32, "mixed", 1.0, 0, 0),
+    (9000, 5, 300, F, BF, B.I64, "any", 1.0, 0, 0),
+    (40000, 2051, 100, BF, BF, B.I64, "any", 1.0, 0, 0),
+    (5000, 100, 2048, BF, F, B.I64, "zipf", 1.0, 0, 0),
+    (5000, 100, 2049, F, F, B.I64, "zipf", 1.0, 0, 0),
+    (700, 768, 3000, BF, BF, B.I32, "lengths", 1.0, 0, 0),
+    (200000, 24, 4096, F, BF, B.I64, "mixed", 1.0, 3, 1),
+    (3, 33, 4096, BF, BF, B.I64, "any", 1.0, 0, 0),
+    (262143, 8, 4000, F, F, B.I64, "any", 1.0, 0, 0),
+    (262144, 8, 4000, F, F, B.I64, "any", 1.0, 0, 0),
+    (900, 200, 18000, F, BF, B.I64, "lengths", 1.0, 0, 0),
+    (3000, 1024, 61000, BF, BF, B.I32, "lengths", 1.0, 0, 0),
+    (1000, 8, 300001, F, BF, B.I64, "zipf", 1.0, 0, 0),
+    (1 << 21, 9, 140000, BF, BF, B.I32, "zipf", 1.0, 0, 0),
 ]
 
 
@@ -263,6 +282,96 @@ def test_gradient(rows, cols, n, dt, ot, it, kind, scale, pad, shift, accumulate
         call()
         t.torch.cuda.synchronize()
         assert t.torch.equal(result.view(t.torch.uint8), t.w.view(t.torch.uint8))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_of_wide_rows(accumulate):
+    """14001 positions of 20000 columns on 50 rows (chunks at their longest), against sums in 64 bits on the device."""
+    import torch
+
+    rows, cols, n = 50, 20000, 14001
+    t = Table(rows, cols, F, seed=8)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(-2, rows + 1, (n,), generator=gen, device="cuda")
+    dout = torch.randn(n, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    old = t.w.double()
+    ws = t.plan.embed_workspace_bytes(1, n)
+    space = torch.full((ws,), CANARY, dtype=torch.uint8, device="cuda")
+    t.plan.embed_grad(1, t.buf.data_ptr(), ids.data_ptr(), n, dout.data_ptr(), space.data_ptr(), ws, scale=0.5,
+                      accumulate=accumulate)
+    keep = (ids >= 0) & (ids < rows)
+    x, at = dout[keep].double(), ids[keep]
+    sums = torch.zeros(rows, cols, dtype=torch.float64, device="cuda").index_add_(0, at, x)
+    size = torch.zeros(rows, cols, dtype=torch.float64, device="cuda").index_add_(0, at, x.abs_())
+    count = torch.bincount(at, minlength=rows)[:, None]
+    want = 0.5 * sums + (old if accumulate else 0.0)
+    bound = 1.01 * (0.5 * (count - 1) * U * size + U * (0.5 * sums).abs() + 2 * U * want.abs())
+    assert bool(((t.w.double() - want).abs() <= bound).all())
+    assert t.outside_untouched()
+
+
+def test_a_workspace_serves_smaller_batches():
+    """One workspace sized for the largest batch, for batches of every way of grouping, in turn."""
+    import torch
+
+    rows, cols, most = 6000, 64, 70000
+    t = Table(rows, cols, F)
+    ws = t.plan.embed_workspace_bytes(1, most)
+    space = torch.full((ws + 256,), CANARY, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(1)
+    for n in (70000, 100, 3000, 33000, 2048, 16500, 5000, 70000):
+        ids = _ids("zipf", n, rows, 0, rng)
+        dout = rng.standard_normal((n, cols)).astype(np.float32)
+        dev, d = _device_ids(ids, B.I64), torch.from_numpy(dout).cuda()
+        t.plan.embed_grad(1, t.buf.data_ptr(), dev.data_ptr(), n, d.data_ptr(), space.data_ptr(), ws, dout_type=F)
+        torch.cuda.synchronize()
+        want, err, _ = _grad_reference(ids, 0, rows, dout, 1.0, None)
+        assert (np.abs(_f32(t.w) - want) <= err + U * (np.abs(want) + err)).all(), n
+        assert bool((space[ws:] == CANARY).all())
+
+
+@pytest.mark.parametrize("n", [300, 3000, 9000])
+def test_table_past_32_bits(n):
+    """A table of 4.6 G elements (9.2 GB): offsets of rows, words and bytes pass 32 bits."""
+    import torch
+
+    rows, cols = 1 << 22, 1100
+    at = 256
+    plan = B.OwnerPlan([B.TableEntry(0, 1, 4, F), B.TableEntry(at, rows, cols, BF, B.ROLE_ADAMW)], at + rows * cols * 2,
+                       B.make_hparams())
+    buf = torch.full((at + rows * cols * 2,), 0x11, dtype=torch.uint8, device="cuda")
+    w = buf[at:].view(torch.bfloat16).view(rows, cols)
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    ids = torch.randint(0, rows, (n,), generator=gen, device="cuda")
+    ids[:6] = torch.tensor([rows - 1, 0, rows - 1, rows // 2, rows - 2, 3904516], device="cuda")
+    dout = torch.randn(n, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    ws = plan.embed_workspace_bytes(1, n)
+    space = torch.empty(ws + 256, dtype=torch.uint8, device="cuda")
+    plan.embed_grad(1, buf.data_ptr(), ids.data_ptr(), n, dout.data_ptr(), space.data_ptr(), ws)
+    out = torch.empty(n, cols, dtype=torch.float32, device="cuda")
+    plan.embed_lookup(1, buf.data_ptr(), ids.data_ptr(), n, out.data_ptr(), out_type=F)
+    uniq, inv = torch.unique(ids, return_inverse=True)
+    sums = torch.zeros(len(uniq), cols, dtype=torch.float64, device="cuda").index_add_(0, inv, dout.double())
+    # one rounding to bf16, and the fp32 sum of at most 4 terms below 7: 3 * 2^-24 * 28 = 5e-6
+    got = w[uniq].double()
+    assert int(torch.bincount(inv).max()) <= 4 and float(dout.abs().max()) < 7
+    assert bool(((got - sums).abs() <= 2.0 ** -8 * (sums.abs() + 5.1e-6) + 5.1e-6).all())
+    assert torch.equal(out, w[ids].float())
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[uniq] = False
+    for k in range(0, rows, 1 << 19):  # every other row is zero
+        part = w[k:k + (1 << 19)][rest[k:k + (1 << 19)]]
+        assert not bool(part.view(torch.int16).any()), k
+    # the norm and clipping of the same buffer
+    gws = torch.empty(plan.grad_workspace_bytes, dtype=torch.uint8, device="cuda")
+    stats = torch.zeros(4, device="cuda")
+    buf[:at] = 0
+    plan.grad_norm(buf.data_ptr(), gws.data_ptr(), gws.numel(), stats.data_ptr(), 1.0)
+    total = float(got.square().sum()) ** 0.5
+    assert abs(float(stats[2]) - total) <= 2.0 ** -23 * total
+    plan.grad_clip(buf.data_ptr(), buf.data_ptr(), stats.data_ptr() + 12, gws.data_ptr(), gws.numel(),
+                   flags=B.STEP_DESCRIPTORS_RESIDENT)
+    assert torch.equal(w[uniq], (got.float() * stats[3]).to(torch.bfloat16))
 
 
 def test_gradient_matches_differences():

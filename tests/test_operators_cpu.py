@@ -170,10 +170,19 @@ def test_embed_grad_refusals():
 def test_embed_workspace_sizes():
     p = _plan()
     assert p.embed_workspace_bytes(3, 0) == 0
-    last = 0
-    for n in (1, 100, 5000, 70_000, 1_000_000):
-        b = p.embed_workspace_bytes(3, n)
-        assert b >= last
-        last = b
     for bad in ((-1, 5), (4, 5), (3, -1), (3, (1 << 30) + 1)):
         assert _status(p.embed_workspace_bytes, *bad) == INVALID
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 12), (5000, 64), (300000, 515), (1 << 22, 3), (1000, 4096), (257, 20000),
+                                       (128256, 4096)])
+def test_embed_workspace_for_more_ids_serves_fewer(rows, cols):
+    """What a batch needs never falls as the batch grows."""
+    p = _plan([E(0, rows, cols, B.BF16, B.ROLE_ADAMW)], rows * cols * 2)
+    sizes = sorted({int(1.07 ** k) + d for k in range(300) for d in (-1, 0, 1)} |
+                   {2 ** k + d for k in range(30) for d in (-1, 0, 1)})
+    last = 0
+    for n in [s for s in sizes if 0 <= s <= 1 << 30]:
+        b = p.embed_workspace_bytes(0, n)
+        assert b >= last, n
+        last = b
