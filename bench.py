@@ -25,6 +25,7 @@ from __future__ import annotations
 import argparse
 import ctypes
 import json
+import math
 import os
 import sys
 import time
@@ -212,6 +213,11 @@ def main() -> int:
     ap.add_argument("--copy-probe-gib", type=float, default=0.0)
     ap.add_argument("--momentum-dtype", choices=("f32", "bf16"), default="f32",
                     help="storage type of the Muon momentum (the workloads state fp32)")
+    ap.add_argument("--max-grad-norm", type=float, default=0.0,
+                    help="above 0: each step first takes the global gradient norm and clips to this (scaled step)")
+    ap.add_argument("--embed-tokens", type=int, default=0,
+                    help="above 0, with --config 6: each step first looks this many token ids up in the table and "
+                         "forms its gradient from them")
     args = ap.parse_args()
 
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -264,10 +270,47 @@ def main() -> int:
     ev_sets = [hip.create(n_ev) for _ in range(args.steps)]
     stream = torch.cuda.current_stream().cuda_stream
 
-    def one(step, events=(), resident=True):
+    # optional operators before the step: embedding lookup and gradient, gradient norm
+    before_events = [[torch.cuda.Event(enable_timing=True) for _ in range(3)] for _ in range(args.steps)]
+    embed = None
+    if args.embed_tokens > 0:
+        embed = [i for i, s in enumerate(wl.specs) if s.name == "embed"]
+        if not embed:
+            print("--embed-tokens needs a workload with an embedding table (--config 6)", file=sys.stderr)
+            return 2
+        spec, n_tok = wl.specs[embed[0]], args.embed_tokens
+        gen = torch.Generator(device=dev).manual_seed(wl.seed)
+        # token ids as in text: the frequency of a rank falls as its inverse
+        ids = (torch.exp(torch.rand(n_tok, generator=gen, device=dev, dtype=torch.float64)
+                         * math.log(spec.rows + 1)).long() - 1).clamp_(0, spec.rows - 1)
+        acts = torch.empty(n_tok, spec.cols, dtype=torch.bfloat16, device=dev)
+        dout = (torch.randn(n_tok, spec.cols, generator=gen, device=dev) * 1e-4).to(torch.bfloat16)
+        ews = torch.empty(plan.embed_workspace_bytes(embed[0], n_tok) + 256, dtype=u8, device=dev)
+    if args.max_grad_norm > 0:
+        gws = torch.empty(plan.grad_workspace_bytes, dtype=u8, device=dev)
+        stats = torch.zeros(4, dtype=torch.float32, device=dev)
+
+    def one(step, events=(), resident=True, marks=None):
         grads = grad_pool[(step - 1) % n_grad]
+        flags = B.STEP_DESCRIPTORS_RESIDENT if resident else 0
+        if marks:
+            marks[0].record()
+        if embed:
+            plan.embed_lookup(embed[0], params.data_ptr(), ids.data_ptr(), n_tok, acts.data_ptr(), stream=stream)
+            plan.embed_grad(embed[0], grads.data_ptr(), ids.data_ptr(), n_tok, dout.data_ptr(), ews.data_ptr(),
+                            ews.numel(), stream=stream)
+        if marks:
+            marks[1].record()
+        if args.max_grad_norm > 0:
+            plan.grad_norm(grads.data_ptr(), gws.data_ptr(), gws.numel(), stats.data_ptr(), args.max_grad_norm,
+                           stream=stream, flags=flags)
+            if marks:
+                marks[2].record()
+            plan.step_scaled(params.data_ptr(), grads.data_ptr(), state.data_ptr(), ws.data_ptr(), ws_bytes, step,
+                             stats.data_ptr() + B.GradStats.SCALE_OFFSET, stream=stream, flags=flags, events=events)
+            return
         plan.step(params.data_ptr(), grads.data_ptr(), state.data_ptr(), ws.data_ptr(), ws_bytes, step,
-                  stream=stream, flags=B.STEP_DESCRIPTORS_RESIDENT if resident else 0, events=events)
+                  stream=stream, flags=flags, events=events)
 
     one(1, resident=False)  # uploads descriptors
     for i in range(args.warmup):
@@ -276,7 +319,7 @@ def main() -> int:
     log(f"[bench] warmup done ({args.warmup} steps); timing {args.steps} steps")
     t0 = time.perf_counter()
     for k in range(args.steps):
-        one(2 + args.warmup + k, events=ev_sets[k])
+        one(2 + args.warmup + k, events=ev_sets[k], marks=before_events[k] if embed or args.max_grad_norm > 0 else None)
     torch.cuda.synchronize()
     t1 = time.perf_counter()
     ms = (t1 - t0) * 1e3 / args.steps
@@ -449,6 +492,12 @@ def main() -> int:
         "roofline": roofline,
         "cpu_baseline": None,
     }
+    if embed or args.max_grad_norm > 0:
+        out["operators_ms"] = {
+            "embed_lookup_and_grad": round(mean([m[0].elapsed_time(m[1]) for m in before_events]), 4) if embed else None,
+            "grad_norm": (round(mean([m[1].elapsed_time(m[2]) for m in before_events]), 4)
+                          if args.max_grad_norm > 0 else None),
+            "embed_tokens": args.embed_tokens, "max_grad_norm": args.max_grad_norm}
     log(f"[bench] {ms:.3f} ms/step; NS {out['ns_tflops_nominal']} TFLOP/s nominal")
     if not args.no_cpu_baseline:
         log(f"[bench] timing the fp64 oracle on host cores (budget {args.cpu_budget_s:.0f} s)")

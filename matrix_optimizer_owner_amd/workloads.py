@@ -178,7 +178,18 @@ def adamw_tail_probe() -> Workload:
     return Workload("adamw-tail-64x4Mi-fp32", sp, seed=7, hparams=dict(MUON_DEFAULTS, ns_precision=0))
 
 
-WORKLOADS = [single_fp32, gpt2_small, llama3_8b_share, mixed_stress, llama3_70b_share, adamw_tail_probe]
+def embedding_owner() -> Workload:
+    """The owner of Llama-3-8B's embedding table: 128256 x 4096 bf16 on AdamW
+    (entry 1) beside the final norm's gain.  The table's gradient comes from
+    token ids, so the benchmark forms it with the library's embedding
+    gradient.  Not one of the five workloads."""
+    sp = [TensorSpec("norm", 1, 4096, "f32", "ones", grad_std=1e-4),
+          TensorSpec("embed", 128256, 4096, grad_std=1e-4, role="adamw")]
+    return Workload("llama3-8b-embedding-owner", sp, seed=8, hparams=dict(MUON_DEFAULTS, ns_precision=0))
+
+
+WORKLOADS = [single_fp32, gpt2_small, llama3_8b_share, mixed_stress, llama3_70b_share, adamw_tail_probe,
+             embedding_owner]
 
 
 def config(i: int) -> Workload:
