@@ -208,25 +208,32 @@ __global__ __launch_bounds__(kZeroThreads) void k_embed_zero(uint8_t* grad, int6
     fill_zeros(grad, bytes, (first_block + blockIdx.x) * kZeroThreads + threadIdx.x);
 }
 
-// Few ids: the block of position i looks through all of them, ends if an
+// Few ids: a block of position i looks through all of them, ends if an
 // earlier one has the same row, and else sums that row's positions in order.
 // No sort and no workspace; the work grows with n^2, so only up to kFewIds.
-constexpr int kFewThreads = 256, kFewWaves = kFewThreads / 64, kFewRounds = 8;
-constexpr int kFewIds = kFewThreads * kFewRounds;
+// A block has kFewSlabs groups' worth of columns: with one, every row is
+// looked for once more per group of columns, with all, a hot row is summed by
+// one block (2000 ids of 4096 columns: 52 us with 1, 28 with 3, 30 with 4).
+// 512 threads (2000 ids of 1001 columns: 25 us, 32 with 256); past kFewIds the
+// sort is faster (at 1500 ids of 256 columns this takes 9 us, the sort 22; at
+// 4096 of 768 columns this 48, the sort 30).
+constexpr int kFewIds = 2048, kFewThreads = 512, kFewSlabs = 3;
 
-template <int OD, int GD, bool ACC> __device__ __forceinline__ void few_ids(const GradArgs& a, int i, int slab) {
-    __shared__ int list[kFewIds];
-    __shared__ int wave_first[kFewWaves], wave_n[kFewWaves];
-    __shared__ float red[kFewThreads * kPer];
+template <int T, int IDS, int OD, int GD, bool ACC>
+__device__ __forceinline__ void few_ids(const GradArgs& a, int i, int part) {
+    constexpr int kWaves = T / 64, kRounds = IDS / T;
+    __shared__ int list[IDS];
+    __shared__ int wave_first[kWaves], wave_n[kWaves];
+    __shared__ float red[T * kPer];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = row_of(a.ids, a.id_type, i, a.first, a.rows);
     if (row == a.rows) return;
     // wave w has the positions from w * rounds * 64 on, in order
-    const int rounds = (a.n + kFewThreads - 1) / kFewThreads;
-    uint64_t hits[kFewRounds];
+    const int rounds = (a.n + T - 1) / T;
+    uint64_t hits[kRounds];
     int found = 0, first = INT32_MAX;
 #pragma unroll
-    for (int k = 0; k < kFewRounds; ++k) {
+    for (int k = 0; k < kRounds; ++k) {
         const int p = (wave * rounds + k) * 64 + lane;
         hits[k] = __ballot(k < rounds && p < a.n && row_of(a.ids, a.id_type, k < rounds && p < a.n ? p : 0, a.first, a.rows) == row);
         if (hits[k] && first == INT32_MAX) first = p - lane + __builtin_ctzll(hits[k]);
@@ -239,36 +246,46 @@ template <int OD, int GD, bool ACC> __device__ __forceinline__ void few_ids(cons
     __syncthreads();
     int at = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
         if (wave_first[w] < i) return;  // an earlier position's block has this row
         at += w < wave ? wave_n[w] : 0;
         total += wave_n[w];
     }
 #pragma unroll
-    for (int k = 0; k < kFewRounds; ++k) {
+    for (int k = 0; k < kRounds; ++k) {
         if (hits[k] >> lane & 1) list[at + __popcll(hits[k] & ((uint64_t(1) << lane) - 1))] = (wave * rounds + k) * 64 + lane;
         at += __popcll(hits[k]);
     }
     __syncthreads();
-    const int g = threadIdx.x >> a.group_shift, groups = kFewThreads >> a.group_shift;
-    const int c = ((slab << a.group_shift) + (int(threadIdx.x) & ((1 << a.group_shift) - 1))) * kPer;
-    const int width = a.cols - c < kPer ? a.cols - c : kPer;
-    float acc[kPer] = {};
-    if (total <= 8) {  // one group has them all in flight at once
-        if (g == 0 && width > 0) {
+    const int slab0 = part * kFewSlabs, slab1 = a.slabs - slab0 < kFewSlabs ? a.slabs : slab0 + kFewSlabs;
+    if (total <= 8) {  // a thread has them all in flight at once
+        const int end = (slab1 << a.group_shift) * kPer < a.cols ? (slab1 << a.group_shift) * kPer : a.cols;
+        for (int c = ((slab0 << a.group_shift) + int(threadIdx.x)) * kPer; c < end; c += T * kPer) {
+            const int width = a.cols - c < kPer ? a.cols - c : kPer;
+            float acc[kPer] = {};
             sum_rows<OD>(a, list, total, c, width, acc);
             write_row<GD, ACC>(a, row, c, width, acc);
         }
         return;
     }
+    const int g = threadIdx.x >> a.group_shift, groups = T >> a.group_shift;
     const int share = (total + groups - 1) / groups, lo = g * share;
-    if (width > 0 && lo < total) sum_rows<OD>(a, list + lo, total - lo < share ? total - lo : share, c, width, acc);
-    add_groups<kFewThreads>(red, a.group_shift, acc);
-    if (g == 0 && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
+    for (int slab = slab0; slab < slab1; ++slab) {
+        const int c = ((slab << a.group_shift) + (int(threadIdx.x) & ((1 << a.group_shift) - 1))) * kPer;
+        const int width = a.cols - c < kPer ? a.cols - c : kPer;
+        float acc[kPer] = {};
+        if (width > 0 && lo < total) sum_rows<OD>(a, list + lo, total - lo < share ? total - lo : share, c, width, acc);
+        add_groups<T>(red, a.group_shift, acc);
+        if (g == 0 && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
+        __syncthreads();
+    }
 }
 
+// Blocks of a position.
+__host__ __device__ constexpr int few_parts(int slabs) { return (slabs + kFewSlabs - 1) / kFewSlabs; }
+
 template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) void k_embed_few(GradArgs a) {
-    few_ids<OD, GD, ACC>(a, int(blockIdx.x), int(blockIdx.y));
+    few_ids<kFewThreads, kFewIds, OD, GD, ACC>(a, int(blockIdx.x), int(blockIdx.y));
 }
 
 // The same with the zeros of the other rows beside it: a block has `span`
@@ -277,7 +294,7 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kFewThreads) vo
 // rows share is the first one's.  One launch instead of two saves 3 us on a
 // small table (500 ids into 61 MB: 12.6 us, 15.3 apart); past kFewBytes
 // clearing without looking at ids wins (1.05 GB: 195 us, 183 apart).
-constexpr int kFewSpanIds = 512, kSpanWords = kFewThreads * 2, kSpanRows = 1024;
+constexpr int kSpanIds = 512, kSpanThreads = 256, kSpanWords = kSpanThreads * 2, kSpanRows = 1024;
 constexpr int64_t kFewBytes = int64_t(128) << 20;
 
 struct SpanArgs {
@@ -290,23 +307,23 @@ template <int GD> __device__ __forceinline__ void fill_span(const GradArgs& a, c
     __shared__ uint8_t hit[kSpanRows + 4];
     const int g = block / s.pieces, piece = block - g * s.pieces, r0 = g * s.span;
     const int r1 = a.rows - r0 < s.span ? a.rows : r0 + s.span;
-    int row[kFewSpanIds / kFewThreads];
+    int row[kSpanIds / kSpanThreads];
 #pragma unroll
-    for (int k = 0; k < kFewSpanIds / kFewThreads; ++k) {
-        const int p = k * kFewThreads + int(threadIdx.x);
+    for (int k = 0; k < kSpanIds / kSpanThreads; ++k) {
+        const int p = k * kSpanThreads + int(threadIdx.x);
         row[k] = p < a.n ? row_of(a.ids, a.id_type, p, a.first, a.rows) : a.rows;
     }
-    for (int r = threadIdx.x; r <= s.span; r += kFewThreads) hit[r] = 0;
+    for (int r = threadIdx.x; r <= s.span; r += kSpanThreads) hit[r] = 0;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kFewSpanIds / kFewThreads; ++k)
+    for (int k = 0; k < kSpanIds / kSpanThreads; ++k)
         if (row[k] >= r0 && row[k] <= r1 && row[k] < a.rows) hit[row[k] - r0] = 1;
     __syncthreads();
     const int64_t total = int64_t(a.rows) * a.cols, begin = int64_t(r0) * a.cols, end = int64_t(r1) * a.cols;
     const int64_t first = (begin + kElems - 1) / kElems + int64_t(piece) * kSpanWords + threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < kSpanWords / kFewThreads; ++k) {
-        const int64_t e = (first + k * kFewThreads) * kElems;
+    for (int k = 0; k < kSpanWords / kSpanThreads; ++k) {
+        const int64_t e = (first + k * kSpanThreads) * kElems;
         if (e >= end) return;
         const uint32_t x = uint32_t(e - begin);
         uint32_t r = x / uint32_t(a.cols), c = x - r * uint32_t(a.cols);
@@ -326,10 +343,10 @@ template <int GD> __device__ __forceinline__ void fill_span(const GradArgs& a, c
     }
 }
 
-template <int OD, int GD> __global__ __launch_bounds__(kFewThreads) void k_embed_few_fill(GradArgs a, SpanArgs s) {
+template <int OD, int GD> __global__ __launch_bounds__(kSpanThreads) void k_embed_few_fill(GradArgs a, SpanArgs s) {
     const int b = int(blockIdx.x);
     if (b < s.few_blocks)
-        few_ids<OD, GD, false>(a, b / a.slabs, b % a.slabs);
+        few_ids<kSpanThreads, kSpanIds, OD, GD, false>(a, b / few_parts(a.slabs), b % few_parts(a.slabs));
     else
         fill_span<GD>(a, s, b - s.few_blocks);
 }
@@ -896,18 +913,18 @@ template <int OD, int GD, bool ACC> hipError_t launch_few(const GradArgs& a, hip
     if constexpr (!ACC) {
         constexpr int kSize = Raw<GD, kPer>::kSize, kElems = 16 / kSize * kSpanWords;
         const int64_t bytes = int64_t(a.rows) * a.cols * kSize;
-        if (a.n <= kFewSpanIds && bytes <= kFewBytes && a.cols >= 16 / kSize) {
+        if (a.n <= kSpanIds && bytes <= kFewBytes && a.cols >= 16 / kSize) {
             SpanArgs s;
             s.span = std::clamp(kElems / a.cols, 1, kSpanRows);
             s.pieces = s.span > 1 ? 1 : (a.cols + kElems - 1) / kElems;
-            s.few_blocks = a.n * a.slabs;
+            s.few_blocks = a.n * few_parts(a.slabs);
             const int blocks = s.few_blocks + (a.rows + s.span - 1) / s.span * s.pieces;
-            k_embed_few_fill<OD, GD><<<dim3(uint32_t(blocks)), dim3(kFewThreads), 0, stream>>>(a, s);
+            k_embed_few_fill<OD, GD><<<dim3(uint32_t(blocks)), dim3(kSpanThreads), 0, stream>>>(a, s);
             return hipGetLastError();
         }
         if (hipError_t e = zero_table(a.grad, bytes, stream); e != hipSuccess) return e;
     }
-    if (a.n > 0) k_embed_few<OD, GD, ACC><<<dim3(uint32_t(a.n), uint32_t(a.slabs)), dim3(kFewThreads), 0, stream>>>(a);
+    if (a.n > 0) k_embed_few<OD, GD, ACC><<<dim3(uint32_t(a.n), uint32_t(few_parts(a.slabs))), dim3(kFewThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
