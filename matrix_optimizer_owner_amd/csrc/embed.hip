@@ -810,7 +810,8 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     s.group_shift = pick_group(std::max(words, 1), 6);
     s.slabs = std::max(1, (words + (1 << s.group_shift) - 1) >> s.group_shift);
     s.width = words * kPer;
-    s.few = n <= kFewIds || e.rows == 0 || e.cols == 0;
+    // wide rows sooner go to the sort, where a hot row is spread over more blocks
+    s.few = n <= (s.slabs > kFewSlabs ? kFewIds / 2 : kFewIds) || e.rows == 0 || e.cols == 0;
     if (s.few) return s;
     int bits = 2;  // of the largest key, `rows`
     while ((int64_t(1) << bits) <= e.rows) ++bits;

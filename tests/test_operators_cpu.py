@@ -79,6 +79,20 @@ def test_grad_tables_from_two_threads():
     assert len(got) == 8 and len(set(got)) == 1
 
 
+def test_grad_tables_cover_every_element_once(tmp_path):
+    """The work lists of 309 tables (empty, single elements, 40000 tensors, 4 TiB, random ones) in C++."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("g++ not available")
+    csrc = os.path.join(ROOT, "matrix_optimizer_owner_amd", "csrc")
+    exe = str(tmp_path / "check")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-pthread", "-I", os.path.join(ROOT, "include"), "-I", csrc,
+                    os.path.join(csrc, "plan.cpp"), os.path.join(csrc, "grad_plan.cpp"),
+                    os.path.join(ROOT, "tests", "grad_plan_check.cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.startswith("OK 309"), out.stdout
+
+
 def test_grad_norm_refusals():
     p = _plan()
     ws = p.grad_workspace_bytes
