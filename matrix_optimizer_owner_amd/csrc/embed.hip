@@ -31,25 +31,48 @@ template <int DT, int N> struct Raw {
     static constexpr int kWords = N * (DT == kBF16 ? 2 : 4) / 16;
     static constexpr int kSize = DT == kBF16 ? 2 : 4;
     u32x4_t w[kWords];
-    // the first `width` of N elements at p (elements); nothing behind them is read
-    template <bool STREAM> __device__ __forceinline__ void load(const void* p, int width) {
-        if (width == N) {
+    // The first `width` of N elements at p, the end of a row; nothing behind it is read.  A row of N elements or more
+    // (`wide`) is read by whole words: its last lane takes the N that end with the row, and settle() moves its own
+    // down.  The two are apart so that a batch of loads is on its way before the first is waited for (4144 ids of
+    // 2764 columns take 66 us with them together, or element by element).
+    template <bool STREAM> __device__ __forceinline__ void load(const uint8_t* p, int width, bool wide) {
+        if (width == N || wide) {
+            const int back = N - width;
+            const word_t* q = reinterpret_cast<const word_t*>(p - back * kSize);
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) {
-                const word_t* q = static_cast<const word_t*>(p) + k;
-                w[k] = STREAM ? __builtin_nontemporal_load(q) : *q;
-            }
+            for (int k = 0; k < kWords; ++k) w[k] = STREAM ? __builtin_nontemporal_load(q + k) : q[k];
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 uint32_t v = 0;
-                if (k < width) v = DT == kBF16 ? uint32_t(static_cast<const uint16_t*>(p)[k]) : static_cast<const uint32_t*>(p)[k];
+                if (k < width)
+                    v = DT == kBF16 ? uint32_t(reinterpret_cast<const uint16_t*>(p)[k]) : reinterpret_cast<const uint32_t*>(p)[k];
                 if (DT == kBF16)
                     w[k / 8][k / 2 % 4] = k % 2 ? w[k / 8][k / 2 % 4] | v << 16 : v;
                 else
                     w[k / 4][k % 4] = v;
             }
         }
+    }
+    __device__ __forceinline__ void settle(int width, bool wide) {
+        if (width == N || !wide) return;
+#pragma unroll
+        for (int step = N / 2; step > 0; step /= 2)
+            if ((N - width) & step) move_down(step);
+    }
+    // element k becomes element k + n, for the elements that there are (n a compile-time power of two after unrolling)
+    __device__ __forceinline__ void move_down(int n) {
+        constexpr int kDwords = kWords * 4;
+        if (DT == kBF16 && n == 1) {
+#pragma unroll
+            for (int d = 0; d < kDwords; ++d)
+                w[d / 4][d % 4] = w[d / 4][d % 4] >> 16 | (d + 1 < kDwords ? w[(d + 1) / 4][(d + 1) % 4] << 16 : 0u);
+            return;
+        }
+        const int dn = DT == kBF16 ? n / 2 : n;
+#pragma unroll
+        for (int d = 0; d < kDwords; ++d)
+            if (d + dn < kDwords) w[d / 4][d % 4] = w[(d + dn) / 4][(d + dn) % 4];
     }
     __device__ __forceinline__ float get(int k) const {
         if (DT == kBF16) {
@@ -119,7 +142,8 @@ __global__ __launch_bounds__(kLookupThreads) void k_embed_lookup(LookupArgs a, i
     float v[N];
     if (r < a.rows) {
         Raw<TD, N> x;
-        x.template load<false>(a.table + (int64_t(r) * a.cols + c) * Raw<TD, N>::kSize, width);
+        x.template load<false>(a.table + (int64_t(r) * a.cols + c) * Raw<TD, N>::kSize, width, a.cols >= N);
+        x.settle(width, a.cols >= N);
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = a.scale * x.get(k);
     } else {
@@ -154,7 +178,8 @@ __device__ __forceinline__ void write_row(const GradArgs& a, int row, int c, int
     float v[kPer];
     if constexpr (ACC) {
         Raw<GD, kPer> old;
-        old.template load<false>(p, width);
+        old.template load<false>(p, width, a.cols >= kPer);
+        old.settle(width, a.cols >= kPer);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] = __builtin_fmaf(a.scale, sum[k], old.get(k));
     } else {
@@ -164,34 +189,43 @@ __device__ __forceinline__ void write_row(const GradArgs& a, int row, int c, int
     store<GD, kPer, true>(p, width, v);
 }
 
-// The sum of dout rows list[0..count), columns c .. c + width, kUnroll loads in flight.
-template <int OD>
-__device__ __forceinline__ void sum_rows(const GradArgs& a, const int* list, int count, int c, int width, float (&acc)[kPer]) {
+// The sum of dout rows at(0) .. at(count-1), columns c .. c + width, kUnroll loads in flight.
+template <int OD, typename F>
+__device__ __forceinline__ void sum_rows(const GradArgs& a, F at, int count, int c, int width, float (&acc)[kPer]) {
     constexpr int kUnroll = 8;
     for (int q = 0; q < count; q += kUnroll) {
         Raw<OD, kPer> x[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
             if (q + u < count)
-                x[u].template load<true>(a.dout + (int64_t(list[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width);
+                x[u].template load<true>(a.dout + (int64_t(at(q + u)) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width,
+                                            a.cols >= kPer);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            if (q + u < count)
+            if (q + u < count) {
+                x[u].settle(width, a.cols >= kPer);
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) acc[k] += x[u].get(k);
+            }
     }
 }
 
-// Every thread's acc of a block of THREADS, added over its groups in their
-// order; valid in group 0.
+// Every thread's acc, added over the groups of a block of THREADS: within a
+// wave pairwise, then wave by wave (an order that the sizes alone fix).
+// Valid in group 0.  All threads call it.
 template <int THREADS> __device__ __forceinline__ void add_groups(float* red, int group_shift, float (&acc)[kPer]) {
+    const int lane = threadIdx.x & 63, G = 1 << group_shift;
+    for (int off = G; off < 64; off <<= 1)
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) red[k * THREADS + threadIdx.x] = acc[k];
+        for (int k = 0; k < kPer; ++k) acc[k] += __shfl_xor(acc[k], off, 64);
+    if (lane < G)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) red[k * THREADS + threadIdx.x] = acc[k];
     __syncthreads();
-    if ((threadIdx.x >> group_shift) != 0) return;
-    for (int g = 1; g < (THREADS >> group_shift); ++g)
+    if (threadIdx.x >= unsigned(G)) return;
+    for (int w = 1; w < THREADS / 64; ++w)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) acc[k] += red[k * THREADS + (g << group_shift) + threadIdx.x];
+        for (int k = 0; k < kPer; ++k) acc[k] += red[k * THREADS + w * 64 + lane];
 }
 
 // Zeros over the whole table's gradient: one word a thread, the shape that
@@ -263,7 +297,7 @@ __device__ __forceinline__ void few_ids(const GradArgs& a, int i, int part) {
         for (int c = ((slab0 << a.group_shift) + int(threadIdx.x)) * kPer; c < end; c += T * kPer) {
             const int width = a.cols - c < kPer ? a.cols - c : kPer;
             float acc[kPer] = {};
-            sum_rows<OD>(a, list, total, c, width, acc);
+            sum_rows<OD>(a, [&](int q) { return list[q]; }, total, c, width, acc);
             write_row<GD, ACC>(a, row, c, width, acc);
         }
         return;
@@ -274,7 +308,8 @@ __device__ __forceinline__ void few_ids(const GradArgs& a, int i, int part) {
         const int c = ((slab << a.group_shift) + (int(threadIdx.x) & ((1 << a.group_shift) - 1))) * kPer;
         const int width = a.cols - c < kPer ? a.cols - c : kPer;
         float acc[kPer] = {};
-        if (width > 0 && lo < total) sum_rows<OD>(a, list + lo, total - lo < share ? total - lo : share, c, width, acc);
+        if (width > 0 && lo < total)
+            sum_rows<OD>(a, [&](int q) { return list[lo + q]; }, total - lo < share ? total - lo : share, c, width, acc);
         add_groups<T>(red, a.group_shift, acc);
         if (g == 0 && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
         __syncthreads();
@@ -351,13 +386,78 @@ template <int OD, int GD> __global__ __launch_bounds__(kSpanThreads) void k_embe
         fill_span<GD>(a, s, b - s.few_blocks);
 }
 
+// More ids than that into few rows: a block of each row (and `span` groups of
+// columns) looks through all ids, each wave through its part, and sums what
+// it finds; rows without an id get their zeros here too.  One launch: 9660
+// ids into 1218 x 15 take 17 us, sorted 51; 4144 into 154 x 2768 29 and 41.
+// The search grows with ids times rows (kRowsWork), and one block sums a row
+// that most ids point to (kRowsHot: with 16000 ids and span 4, a tenth of
+// them on one row, 218 us against 63).
+constexpr int kRowsThreads = 512, kRowsWaves = kRowsThreads / 64, kRowsHot = 10240;
+constexpr int64_t kRowsWork = int64_t(16) << 20;
+
+template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kRowsThreads) void k_embed_rows(GradArgs a, int span) {
+    __shared__ uint16_t hits[kRowsWaves][kRowsHot / kRowsWaves];
+    __shared__ int wave_n[kRowsWaves];
+    __shared__ float red[kRowsThreads * kPer];
+    const int row = int(blockIdx.x), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int part = ((a.n + kRowsWaves - 1) / kRowsWaves + 63) / 64 * 64, base = wave * part;
+    const int end = a.n - base < part ? a.n : base + part;
+    int found = 0;
+    constexpr int kUnroll = 8;
+    for (int r = base; r < end; r += 64 * kUnroll) {
+        int key[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int p = r + u * 64 + lane;
+            key[u] = p < end ? row_of(a.ids, a.id_type, p, a.first, a.rows) : a.rows;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint64_t m = __builtin_amdgcn_ballot_w64(key[u] == row);
+            if (key[u] == row)
+                hits[wave][found + __popcll(m & ((uint64_t(1) << lane) - 1))] = uint16_t(r - base + u * 64 + lane);
+            found += __popcll(m);
+        }
+    }
+    if (lane == 0) wave_n[wave] = found;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kRowsWaves; ++w) total += wave_n[w];
+    const int slab0 = int(blockIdx.y) * span, slab1 = a.slabs - slab0 < span ? a.slabs : slab0 + span;
+    if (total == 0) {
+        if (ACC) return;
+        const int last = (slab1 << a.group_shift) * kPer < a.cols ? (slab1 << a.group_shift) * kPer : a.cols;
+        const float zero[kPer] = {};
+        for (int c = ((slab0 << a.group_shift) + int(threadIdx.x)) * kPer; c < last; c += kRowsThreads * kPer)
+            write_row<GD, false>(a, row, c, a.cols - c < kPer ? a.cols - c : kPer, zero);
+        return;
+    }
+    // a wave's groups each take a stretch of what the wave found
+    const int groups = 64 >> a.group_shift, g = lane >> a.group_shift;
+    const int share = (found + groups - 1) / groups, lo = g * share;
+    for (int slab = slab0; slab < slab1; ++slab) {
+        const int c = ((slab << a.group_shift) + (lane & ((1 << a.group_shift) - 1))) * kPer;
+        const int width = a.cols - c < kPer ? a.cols - c : kPer;
+        float acc[kPer] = {};
+        if (width > 0 && lo < found)
+            sum_rows<OD>(a, [&](int q) { return base + int(hits[wave][lo + q]); }, found - lo < share ? found - lo : share, c,
+                         width, acc);
+        add_groups<kRowsThreads>(red, a.group_shift, acc);
+        if (int(threadIdx.x) < (1 << a.group_shift) && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
+        __syncthreads();
+    }
+}
+
 // ---- many ids: sort positions by row, then sum runs of the sorted order ----
 //
-// The sort is a stable radix sort of (row, position) in two passes over about
-// half of the row's bits each: per pass one launch counts each tile's digits
+// The sort is a stable radix sort of (row, position), in one pass for fewer
+// than 2048 rows and else in two over about half of the row's bits each: per
+// pass one launch counts each tile's digits
 // and one ranks and scatters.  Ids outside the table sort last, as row `rows`.
 
-constexpr int kSortUnroll = 4;
+constexpr int kSortUnroll = 4, kOnePassBits = 11;
 
 struct SortArgs {
     const void* ids;          // first pass; else keys_in and pos_in
@@ -372,7 +472,7 @@ struct SortArgs {
 };
 
 // Zeros beside the sort: the table's gradient is cleared by blocks that the
-// sort's four launches carry behind their own, a quarter each, so that the
+// sort's launches carry behind their own, an equal part each, so that the
 // sort, which keeps a few CUs for some microseconds a launch, takes no time
 // of its own.  One word a thread, the shape that writes fastest here.  (Clearing
 // only the rows without an id, by a flag a row, saves their bytes but waits
@@ -545,8 +645,10 @@ template <bool FIRST, int T> __global__ __launch_bounds__(T) void k_sort_scatter
 }
 
 // Up to kBlockIds ids into a table of fewer than 2^18 rows: both passes in one
-// block, between them in LDS.
-constexpr int kBlockThreads = 1024, kBlockWaves = kBlockThreads / 64, kBlockRounds = 4;
+// block, between them in LDS.  Of a whole gradient of 4096 ids of 768 columns
+// this saves 11 of 43 us, of 8000 into 10000 x 256 3 of 40; at 16384 the block
+// sorts for 42 us where the four launches take 24.
+constexpr int kBlockThreads = 1024, kBlockWaves = kBlockThreads / 64, kBlockRounds = 8;
 constexpr int kBlockIds = kBlockThreads * kBlockRounds, kBlockBits = 9;
 
 __global__ __launch_bounds__(kBlockThreads) void k_sort_block(SortArgs a, int bits0, int bits1) {
@@ -696,15 +798,18 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
         for (int u = 0; u < kUnroll; ++u) {
             key[u + 1] = q + u + 1 < q1 ? K[kRunMax + q + u + 1] : -1;
             if (q + u < q1) {
-                x[u].template load<true>(a.dout + (int64_t(P[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width);
+                x[u].template load<true>(a.dout + (int64_t(P[q + u]) * a.dout_stride + c) * Raw<OD, kPer>::kSize, width,
+                                            a.cols >= kPer);
                 if constexpr (ACC)
                     if (key[u + 1] != key[u])
-                        old[u].template load<false>(a.grad + (int64_t(key[u]) * a.cols + c) * Raw<GD, kPer>::kSize, width);
+                        old[u].template load<false>(a.grad + (int64_t(key[u]) * a.cols + c) * Raw<GD, kPer>::kSize, width,
+                                                    a.cols >= kPer);
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (q + u < q1) {
+                x[u].settle(width, a.cols >= kPer);
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) acc[k] += x[u].get(k);
             }
@@ -717,6 +822,7 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
                     reinterpret_cast<f32x4_t*>(o)[1] = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
                 } else {
                     float v[kPer];
+                    if constexpr (ACC) old[u].settle(width, a.cols >= kPer);
 #pragma unroll
                     for (int k = 0; k < kPer; ++k)
                         v[k] = ACC ? __builtin_fmaf(a.scale, acc[k], old[ACC ? u : 0].get(k)) : a.scale * acc[k];
@@ -798,8 +904,11 @@ int pick_group(int words, int most_shift) {
 
 // How a gradient of n ids is cut, and where its workspace regions lie.
 struct GradShape {
-    bool few, block;         // which way the ids are grouped: by search, by one block's sort, else by launches
+    // which way positions are grouped by row: searched for by each position's or by each row's block, sorted by one
+    // block, else sorted by several launches
+    bool few, by_row, block;
     int group_shift, slabs, width;
+    int span;                // by_row: groups of columns of a block
     int bits[2], tile, n_tiles, chunk, n_chunks;
     uint64_t keys[2], pos[2], hist, runs, parts, total;
 };
@@ -813,11 +922,17 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     // wide rows sooner go to the sort, where a hot row is spread over more blocks
     s.few = n <= (s.slabs > kFewSlabs ? kFewIds / 2 : kFewIds) || e.rows == 0 || e.cols == 0;
     if (s.few) return s;
+    // a row's columns in as many blocks as keep the search small
+    s.span = 1;
+    while (s.span < s.slabs && n * e.rows * ((s.slabs + s.span - 1) / s.span) > 2 * kRowsWork) ++s.span;
+    s.by_row = n * s.span <= kRowsHot && n * e.rows <= kRowsWork;
+    if (s.by_row) return s;
     int bits = 2;  // of the largest key, `rows`
     while ((int64_t(1) << bits) <= e.rows) ++bits;
-    s.bits[0] = (bits + 1) / 2;
-    s.bits[1] = bits - s.bits[0];
     s.block = n <= kBlockIds && bits <= 2 * kBlockBits;
+    // one pass where LDS holds its counts and the fill beside it still has room, else two
+    s.bits[0] = !s.block && bits <= kOnePassBits ? bits : (bits + 1) / 2;
+    s.bits[1] = bits - s.bits[0];
     // at least 2048 positions a tile, at most 128 tiles (each adds up the
     // digits of all others)
     s.tile = int(std::max<int64_t>(2048, (n + 128 * 512 - 1) / (128 * 512) * 512));
@@ -929,7 +1044,7 @@ template <int OD, int GD, bool ACC> hipError_t launch_few(const GradArgs& a, hip
     return hipGetLastError();
 }
 
-// The sort in four launches, each with a quarter of the zeros.
+// The sort, two launches a pass, each with an equal part of the zeros.
 template <int T>
 hipError_t launch_sort(SortArgs t, const GradShape& s, uint8_t* ws, uint8_t* grad, int64_t bytes, hipStream_t stream) {
     auto ints = [&](uint64_t off) { return reinterpret_cast<int*>(ws + off); };
@@ -939,15 +1054,16 @@ hipError_t launch_sort(SortArgs t, const GradShape& s, uint8_t* ws, uint8_t* gra
         if (hipError_t e = zero_table(grad, bytes, stream); e != hipSuccess) return e;
         fill = 0;
     }
-    const int64_t part = (fill + 3) / 4;
+    const int passes = s.bits[1] > 0 ? 2 : 1;
+    const int64_t part = (fill + 2 * passes - 1) / (2 * passes);
     auto grid = [&] { return dim3(uint32_t(s.n_tiles + std::max<int64_t>(0, std::min(part, fill - f.first_block)))); };
-    for (int pass = 0; pass < 2; ++pass) {
+    for (int pass = 0; pass < passes; ++pass) {
         t.shift = pass ? s.bits[0] : 0;
         t.bits = s.bits[pass];
         t.keys_in = ints(s.keys[0]);
         t.pos_in = ints(s.pos[0]);
-        t.keys_out = ints(s.keys[pass]);
-        t.pos_out = ints(s.pos[pass]);
+        t.keys_out = ints(s.keys[pass + 2 - passes]);
+        t.pos_out = ints(s.pos[pass + 2 - passes]);
         const size_t row = size_t(4) << t.bits;
         if (pass == 0)
             k_sort_count<true, T><<<grid(), dim3(T), row, stream>>>(t, f);
@@ -984,7 +1100,7 @@ hipError_t launch_sorted(const GradArgs& a, const GradShape& s, uint8_t* ws, hip
         t.pos_out = ints(s.pos[1]);
         k_sort_block<<<dim3(1), dim3(kBlockThreads), 0, stream>>>(t, s.bits[0], s.bits[1]);
     } else {
-        // 256 threads clear faster (6.7 TB/s in four launches, 6.2 with 512), 512 sort faster
+        // 256 threads clear faster (6.7 TB/s in four parts, 6.2 with 512), 512 sort faster
         if (hipError_t e = ACC ? launch_sort<512>(t, s, ws, a.grad, bytes, stream) : launch_sort<256>(t, s, ws, a.grad, bytes, stream);
             e != hipSuccess)
             return e;
@@ -1011,6 +1127,11 @@ hipError_t launch_sorted(const GradArgs& a, const GradShape& s, uint8_t* ws, hip
 
 template <int OD, int GD, bool ACC>
 hipError_t launch_grad(const GradArgs& a, const GradShape& s, uint8_t* ws, hipStream_t stream) {
+    if (s.by_row) {
+        const uint32_t parts = uint32_t((a.slabs + s.span - 1) / s.span);
+        k_embed_rows<OD, GD, ACC><<<dim3(uint32_t(a.rows), parts), dim3(kRowsThreads), 0, stream>>>(a, s.span);
+        return hipGetLastError();
+    }
     return s.few ? launch_few<OD, GD, ACC>(a, stream) : launch_sorted<OD, GD, ACC>(a, s, ws, stream);
 }
 
