@@ -365,7 +365,9 @@ mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* a
  * depends on the ids and sizes alone (bitwise the same from run to run, no
  * atomics on values), multiplied by scale in fp32, and rounded once to the
  * entry's type.  Both calls only enqueue launches on the stream, so they can
- * be captured; the current device must be the stream's and the buffers'. */
+ * be captured; the current device must be the stream's and the buffers'.
+ * What a call writes (out, or grads and workspace) must not overlap what it
+ * reads (params, ids, dout). */
 typedef enum mfsdp_id_type {
     MFSDP_I32 = 0,
     MFSDP_I64 = 1

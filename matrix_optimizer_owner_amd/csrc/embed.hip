@@ -924,8 +924,9 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     if (s.few) return s;
     // a row's columns in as many blocks as keep the search small
     s.span = 1;
-    while (s.span < s.slabs && n * e.rows * ((s.slabs + s.span - 1) / s.span) > 2 * kRowsWork) ++s.span;
-    s.by_row = n * s.span <= kRowsHot && n * e.rows <= kRowsWork;
+    s.by_row = n * e.rows <= kRowsWork;
+    while (s.by_row && s.span < s.slabs && n * e.rows * ((s.slabs + s.span - 1) / s.span) > 2 * kRowsWork) ++s.span;
+    s.by_row = s.by_row && n * s.span <= kRowsHot;
     if (s.by_row) return s;
     int bits = 2;  // of the largest key, `rows`
     while ((int64_t(1) << bits) <= e.rows) ++bits;

@@ -374,6 +374,32 @@ def test_table_past_32_bits(n):
     assert torch.equal(w[uniq], (got.float() * stats[3]).to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("n", [5, 700, 1100])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_widest_rows(n, accumulate):
+    """Rows of 2^22 columns, the widest an entry can have; activations past 2^32 elements.  Whole numbers below 2^24:
+    every sum is exact."""
+    import torch
+
+    rows, cols = 3, 1 << 22
+    plan = B.OwnerPlan([B.TableEntry(0, rows, cols, F, B.ROLE_ADAMW)], rows * cols * 4, B.make_hparams())
+    w = torch.full((rows, cols), 3.0, device="cuda")
+    i, c = torch.arange(n, device="cuda"), (torch.arange(cols, device="cuda") % 5).float()
+    ids = torch.where(i % 11 == 10, -1, i % (rows - 1))  # the last row has none
+    dout = (i[:, None] % 7).to(torch.bfloat16) + c.to(torch.bfloat16)
+    ws = plan.embed_workspace_bytes(0, n)
+    space = torch.empty(ws + 256, dtype=torch.uint8, device="cuda")
+    plan.embed_grad(0, w.data_ptr(), ids.data_ptr(), n, dout.data_ptr(), space.data_ptr(), ws, accumulate=accumulate)
+    for r in range(rows):
+        mine = ids == r
+        want = c * int(mine.sum()) + float((i % 7)[mine].sum()) + (3.0 if accumulate else 0.0)
+        assert torch.equal(w[r], want), r
+    for ot in (BF, F):
+        out = torch.empty(5, cols, dtype=_torch_type(ot), device="cuda")
+        plan.embed_lookup(0, w.data_ptr(), ids.data_ptr(), 5, out.data_ptr(), out_type=ot, scale=0.5)
+        assert torch.equal(out, (0.5 * w[ids[:5]]).to(_torch_type(ot)))
+
+
 def test_gradient_matches_differences():
     """loss = sum(dout * lookup(W)): (loss(W + d) - loss(W - d)) / 2 = <grad, d>.
 
