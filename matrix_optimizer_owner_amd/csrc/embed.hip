@@ -386,22 +386,30 @@ template <int OD, int GD> __global__ __launch_bounds__(kSpanThreads) void k_embe
         fill_span<GD>(a, s, b - s.few_blocks);
 }
 
-// More ids than that into few rows: a block of each row (and `span` groups of
-// columns) looks through all ids, each wave through its part, and sums what
-// it finds; rows without an id get their zeros here too.  One launch: 9660
-// ids into 1218 x 15 take 17 us, sorted 51; 4144 into 154 x 2768 29 and 41.
-// The search grows with ids times rows (kRowsWork), and one block sums a row
-// that most ids point to (kRowsHot: with 16000 ids and span 4, a tenth of
-// them on one row, 218 us against 63).
-constexpr int kRowsThreads = 512, kRowsWaves = kRowsThreads / 64, kRowsHot = 10240;
+// More ids than that into few rows, or at least twice as many ids as rows: a
+// block of each row (and `span` groups of columns) looks through all ids, each
+// wave through its part, and sums what it finds; rows without an id get their
+// zeros here too.  One launch: 9660 ids into 1218 x 15 take 17 us, sorted 51;
+// 4144 into 154 x 2764 31 and 41; 1000 into 490 x 768 8.8, by the positions'
+// blocks 11.3 (2000 into 2900 x 768 27 and 15).  The search grows with ids
+// times rows (kRowsWork), and one block sums a row that most ids point to
+// (kRowsHot: with 16000 ids and span 4, a tenth of them on one row, 218 us
+// against 63), by more groups side by side if it is narrow, of at most
+// 2^kRowsNarrow lanes (kRowsIds: 16000 of 96 columns 22 us, sorted 35; 12000
+// of 256 fp32 columns 48 and 35).
+constexpr int kRowsThreads = 512, kRowsWaves = kRowsThreads / 64, kRowsHot = 10240, kRowsIds = 16384, kRowsNarrow = 4;
 constexpr int64_t kRowsWork = int64_t(16) << 20;
 
+// Ids of a wave, a multiple of 64.
+__host__ __device__ constexpr int rows_part(int n) { return ((n + kRowsWaves - 1) / kRowsWaves + 63) / 64 * 64; }
+
 template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kRowsThreads) void k_embed_rows(GradArgs a, int span) {
-    __shared__ uint16_t hits[kRowsWaves][kRowsHot / kRowsWaves];
+    extern __shared__ uint16_t row_hits[];  // kRowsWaves parts
     __shared__ int wave_n[kRowsWaves];
     __shared__ float red[kRowsThreads * kPer];
     const int row = int(blockIdx.x), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int part = ((a.n + kRowsWaves - 1) / kRowsWaves + 63) / 64 * 64, base = wave * part;
+    const int part = rows_part(a.n), base = wave * part;
+    uint16_t* const hits = row_hits + base;
     const int end = a.n - base < part ? a.n : base + part;
     int found = 0;
     constexpr int kUnroll = 8;
@@ -416,7 +424,7 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kRowsThreads) v
         for (int u = 0; u < kUnroll; ++u) {
             const uint64_t m = __builtin_amdgcn_ballot_w64(key[u] == row);
             if (key[u] == row)
-                hits[wave][found + __popcll(m & ((uint64_t(1) << lane) - 1))] = uint16_t(r - base + u * 64 + lane);
+                hits[found + __popcll(m & ((uint64_t(1) << lane) - 1))] = uint16_t(r - base + u * 64 + lane);
             found += __popcll(m);
         }
     }
@@ -442,7 +450,7 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kRowsThreads) v
         const int width = a.cols - c < kPer ? a.cols - c : kPer;
         float acc[kPer] = {};
         if (width > 0 && lo < found)
-            sum_rows<OD>(a, [&](int q) { return base + int(hits[wave][lo + q]); }, found - lo < share ? found - lo : share, c,
+            sum_rows<OD>(a, [&](int q) { return base + int(hits[lo + q]); }, found - lo < share ? found - lo : share, c,
                          width, acc);
         add_groups<kRowsThreads>(red, a.group_shift, acc);
         if (int(threadIdx.x) < (1 << a.group_shift) && width > 0) write_row<GD, ACC>(a, row, c, width, acc);
@@ -919,15 +927,17 @@ GradShape grad_shape(const mfsdp_entry& e, int64_t n) {
     s.group_shift = pick_group(std::max(words, 1), 6);
     s.slabs = std::max(1, (words + (1 << s.group_shift) - 1) >> s.group_shift);
     s.width = words * kPer;
-    // wide rows sooner go to the sort, where a hot row is spread over more blocks
-    s.few = n <= (s.slabs > kFewSlabs ? kFewIds / 2 : kFewIds) || e.rows == 0 || e.cols == 0;
+    s.few = e.rows == 0 || e.cols == 0;
     if (s.few) return s;
     // a row's columns in as many blocks as keep the search small
     s.span = 1;
-    s.by_row = n * e.rows <= kRowsWork;
+    s.by_row = n <= kRowsIds && n * e.rows <= kRowsWork;
     while (s.by_row && s.span < s.slabs && n * e.rows * ((s.slabs + s.span - 1) / s.span) > 2 * kRowsWork) ++s.span;
-    s.by_row = s.by_row && n * s.span <= kRowsHot;
-    if (s.by_row) return s;
+    s.by_row = s.by_row && n * s.span <= (s.group_shift <= kRowsNarrow ? kRowsIds : kRowsHot);
+    // wide rows sooner go to the sort, where a hot row is spread over more blocks
+    s.few = n <= (s.slabs > kFewSlabs ? kFewIds / 2 : kFewIds) && !(s.by_row && 2 * e.rows <= n);
+    s.by_row = s.by_row && !s.few;
+    if (s.few || s.by_row) return s;
     int bits = 2;  // of the largest key, `rows`
     while ((int64_t(1) << bits) <= e.rows) ++bits;
     s.block = n <= kBlockIds && bits <= 2 * kBlockBits;
@@ -1130,7 +1140,8 @@ template <int OD, int GD, bool ACC>
 hipError_t launch_grad(const GradArgs& a, const GradShape& s, uint8_t* ws, hipStream_t stream) {
     if (s.by_row) {
         const uint32_t parts = uint32_t((a.slabs + s.span - 1) / s.span);
-        k_embed_rows<OD, GD, ACC><<<dim3(uint32_t(a.rows), parts), dim3(kRowsThreads), 0, stream>>>(a, s.span);
+        const size_t lds = size_t(rows_part(a.n)) * kRowsWaves * sizeof(uint16_t);
+        k_embed_rows<OD, GD, ACC><<<dim3(uint32_t(a.rows), parts), dim3(kRowsThreads), lds, stream>>>(a, s.span);
         return hipGetLastError();
     }
     return s.few ? launch_few<OD, GD, ACC>(a, stream) : launch_sorted<OD, GD, ACC>(a, s, ws, stream);

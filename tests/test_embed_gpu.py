@@ -210,6 +210,16 @@ GRADS = [  # rows, cols, n, table, dout, ids, kind, scale, stride pad, shift
     (3000, 1024, 61000, BF, BF, B.I32, "lengths", 1.0, 0, 0),
     (1000, 8, 300001, F, BF, B.I64, "zipf", 1.0, 0, 0),
     (1 << 21, 9, 140000, BF, BF, B.I32, "zipf", 1.0, 0, 0),
+    (900, 96, 16384, BF, F, B.I64, "zipf", 1.0, 0, 0),
+    (900, 96, 16385, BF, F, B.I64, "zipf", 1.0, 0, 0),
+    (1000, 128, 16384, F, BF, B.I32, "lengths", 0.5, 0, 0),
+    (1, 130, 10240, F, F, B.I32, "mixed", 1.0, 0, 0),
+    (500, 64, 999, BF, BF, B.I64, "any", 1.0, 0, 0),
+    (500, 64, 1000, BF, BF, B.I64, "any", 1.0, 0, 0),
+    (7, 21, 13, F, BF, B.I64, "any", 1.0, 0, 0),
+    (7, 21, 14, F, BF, B.I64, "mixed", 1.0, 2, 1),
+    (1, 1, 2, BF, F, B.I32, "same", 1.0, 0, 0),
+    (1000, 4100, 2000, BF, BF, B.I64, "zipf", 1.0, 0, 0),
 ]
 
 
