@@ -437,9 +437,10 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kRowsThreads) v
     if (total == 0) {
         if (ACC) return;
         const int last = (slab1 << a.group_shift) * kPer < a.cols ? (slab1 << a.group_shift) * kPer : a.cols;
-        const float zero[kPer] = {};
+        const float zero[kPer] = {};  // stored as they are: a product with a negative or infinite scale is no zero
         for (int c = ((slab0 << a.group_shift) + int(threadIdx.x)) * kPer; c < last; c += kRowsThreads * kPer)
-            write_row<GD, false>(a, row, c, a.cols - c < kPer ? a.cols - c : kPer, zero);
+            store<GD, kPer, true>(a.grad + (int64_t(row) * a.cols + c) * Raw<GD, kPer>::kSize,
+                                  a.cols - c < kPer ? a.cols - c : kPer, zero);
         return;
     }
     // a wave's groups each take a stretch of what the wave found
