@@ -11,6 +11,7 @@
 //  * k_final_from_x: the parameter update straight from X0 when there are
 //    no Newton-Schulz iterations.
 //  * k_adamw: AdamW for the tensors that are not matrices (Abstract).
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -270,6 +271,7 @@ struct AdamArgs {
     float inv_bc1, inv_bc2;    // 1/(1 - beta^t)
     float lr, lrwd, eps;
     const float* gscale;       // SCALED kernel: the factor of every gradient
+    int first_chunk;           // the launch's first chunk
 };
 
 // Four consecutive parameter / gradient elements (fp32, or bf16 rounded to
@@ -311,11 +313,14 @@ __device__ __forceinline__ void adamw_elem(const AdamArgs& a, float gv, float& w
 // threads' bytes, or ordinary loads or stores, at 5.2 - 5.4.  SCALED as in
 // k_momentum.
 constexpr int kAdamPer = 4, kAdamThreads = kTailChunk / kAdamPer;
+// A launch of 2^32 threads or more runs their number modulo 2^32, with no
+// error; a tail of 2^34 bf16 elements (206 GB with its moments) has that many.
+constexpr int64_t kAdamBlocksMax = (int64_t(1) << 32) / kAdamThreads - 1;
 template <bool SCALED>
 __global__ __launch_bounds__(kAdamThreads) void k_adamw(AdamArgs a) {
     float gs = 1.f;
     if constexpr (SCALED) gs = *a.gscale;
-    const int chunk = blockIdx.x;
+    const int chunk = a.first_chunk + int(blockIdx.x);
     const int ti = upper_index(a.tail_begin, a.n_tail, chunk);
     const TailDesc t = a.tails[ti];
     const int64_t begin = int64_t(chunk - a.tail_begin[ti]) * kTailChunk;
@@ -434,10 +439,14 @@ hipError_t launch_adamw(const WorkspaceMap& map, const mfsdp_hparams& hp, int64_
     a.lrwd = float(double(hp.adam_lr) * double(hp.adam_weight_decay));
     a.eps = hp.adam_eps;
     a.gscale = b.grad_scale;
-    if (a.gscale)
-        k_adamw<true><<<dim3(map.n_tail_chunks), dim3(kAdamThreads), 0, stream>>>(a);
-    else
-        k_adamw<false><<<dim3(map.n_tail_chunks), dim3(kAdamThreads), 0, stream>>>(a);
+    for (int64_t first = 0; first < map.n_tail_chunks; first += kAdamBlocksMax) {
+        a.first_chunk = int(first);
+        const dim3 grid(uint32_t(std::min(map.n_tail_chunks - first, kAdamBlocksMax)));
+        if (a.gscale)
+            k_adamw<true><<<grid, dim3(kAdamThreads), 0, stream>>>(a);
+        else
+            k_adamw<false><<<grid, dim3(kAdamThreads), 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
