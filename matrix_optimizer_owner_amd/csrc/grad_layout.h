@@ -50,9 +50,13 @@ struct GradTables {
 };
 
 constexpr int64_t kGradSlice = 8192;
-// A chunk is the smallest power of two of bytes that cuts the table into at
-// most kGradChunks chunks: short enough not to leave many empty slices
-// behind small tensors, few enough for a short list.
+// A chunk is the smallest power of two of bytes (at most kGradChunkMax) that
+// cuts the table into at most kGradChunks chunks and two more for each tensor
+// that is not empty: few enough for a short list, short enough not to leave
+// many empty slices behind small tensors.  With N tensors and S slices that
+// hold elements, half the length would make more than kGradChunks + 2 N
+// chunks, so S / (slices of half a chunk) > kGradChunks + N, and the empty
+// slices, less than a chunk's for each tensor, are fewer than 2 S.
 constexpr int64_t kGradChunks = 16384;
 constexpr int64_t kGradChunkMax = int64_t(1) << 30;
 // The norm's shares.  Cost counts slices, and kNormPieceCost more for each

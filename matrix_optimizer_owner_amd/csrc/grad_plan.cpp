@@ -17,12 +17,13 @@ std::unique_ptr<GradTables> lower(const mfsdp_plan_s& plan) {
         for (const mfsdp_entry& e : plan.entries) c += (e.rows * e.cols * es(e) + len - 1) / len;
         return c;
     };
+    int64_t held = 0;  // tensors that are not empty
+    for (const mfsdp_entry& e : plan.entries) held += e.rows * e.cols > 0;
     int64_t len = kGradSlice;
-    while (len < kGradChunkMax && count(len) > kGradChunks) len *= 2;
+    while (len < kGradChunkMax && count(len) > kGradChunks + 2 * held) len *= 2;
     if (count(len) > int64_t(INT32_MAX)) return t;  // refused below: total_bytes stays 0
     for (int64_t l = kGradSlice; l < len; l *= 2) ++t->slice_shift;
-    int64_t cost = count(kGradSlice);
-    for (const mfsdp_entry& e : plan.entries) cost += e.rows * e.cols > 0 ? kNormPieceCost : 0;
+    const int64_t cost = count(kGradSlice) + held * kNormPieceCost;
     const int64_t share = std::max(kNormShareMin, kNormPieceCost + (cost + kNormBlocks - 1) / kNormBlocks);
     std::vector<GradRun> chunks, pieces;
     std::vector<int32_t> block_begin(1, 0), entry_begin(1, 0), large;

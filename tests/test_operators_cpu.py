@@ -93,6 +93,20 @@ def test_grad_tables_cover_every_element_once(tmp_path):
     assert out.returncode == 0 and out.stdout.startswith("OK 309"), out.stdout
 
 
+def test_clip_work_list_launches_few_empty_blocks(tmp_path):
+    """Blocks of a clip against the slices that hold elements, for 118 tables of up to 100000 tensors, in C++."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("g++ not available")
+    csrc = os.path.join(ROOT, "matrix_optimizer_owner_amd", "csrc")
+    exe = str(tmp_path / "check")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-pthread", "-I", os.path.join(ROOT, "include"), "-I", csrc,
+                    os.path.join(csrc, "plan.cpp"), os.path.join(csrc, "grad_plan.cpp"),
+                    os.path.join(ROOT, "tests", "clip_plan_check.cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.startswith("OK 118"), out.stdout
+
+
 def test_grad_norm_refusals():
     p = _plan()
     ws = p.grad_workspace_bytes
