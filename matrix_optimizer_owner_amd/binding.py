@@ -132,7 +132,8 @@ _PACK = {ctypes.c_void_p: "P", ctypes.c_uint64: "Q", ctypes.c_int64: "q", ctypes
 def _packer(mirror):
     """The fields of a ctypes struct -> the bytes of that struct.  A call that
     takes microseconds is made per step: packing its arguments takes 0.3 us,
-    filling a ctypes struct 0.9 (pointers are plain addresses, 0 for NULL)."""
+    filling a ctypes struct 0.9 (pointers are plain addresses, 0 for NULL; the
+    callers below turn None into 0)."""
     fmt = struct.Struct("@" + "".join(_PACK.get(t, "P") for _, t in mirror._fields_) + "0P")
     assert fmt.size == ctypes.sizeof(mirror), mirror
     return fmt.pack
@@ -324,8 +325,8 @@ class OwnerPlan:
         """mfsdp_owner_step_scaled: the step with every gradient times the
         device float at grad_scale (a mfsdp_grad_stats' scale field)."""
         ev = (ctypes.c_void_p * len(events))(*events) if events else None
-        args = _pack_step(params, grads, state, workspace, workspace_bytes, step, stream, ns_out, flags,
-                          ctypes.addressof(ev) if events else 0, len(events))
+        args = _pack_step(params or 0, grads or 0, state or 0, workspace or 0, workspace_bytes, step, stream or 0,
+                          ns_out or 0, flags, ctypes.addressof(ev) if events else 0, len(events))
         status = self._lib.mfsdp_owner_step_scaled(self._h, args, grad_scale)
         if status:
             _check(status)
@@ -338,8 +339,8 @@ class OwnerPlan:
                   eps: float = 1e-6, entry_norms: int = 0, stream: int = 0, flags: int = 0) -> None:
         """mfsdp_grad_norm: norm and clipping scale of the whole buffer into
         the GradStats at `stats`, and each entry's norm into entry_norms."""
-        status = self._lib.mfsdp_grad_norm(self._h, _pack_norm(grads, workspace, workspace_bytes, max_norm, eps, stats,
-                                                               entry_norms, stream, flags))
+        status = self._lib.mfsdp_grad_norm(self._h, _pack_norm(grads or 0, workspace or 0, workspace_bytes, max_norm, eps,
+                                                               stats or 0, entry_norms or 0, stream or 0, flags))
         if status:
             _check(status)
 
@@ -347,8 +348,8 @@ class OwnerPlan:
                   flags: int = 0) -> None:
         """mfsdp_grad_clip: out <- (device float at scale) * grads; out may be
         grads."""
-        status = self._lib.mfsdp_grad_clip(self._h, _pack_clip(grads, out, scale, workspace, workspace_bytes, stream,
-                                                               flags))
+        status = self._lib.mfsdp_grad_clip(self._h, _pack_clip(grads or 0, out or 0, scale or 0, workspace or 0,
+                                                               workspace_bytes, stream or 0, flags))
         if status:
             _check(status)
 
@@ -357,8 +358,9 @@ class OwnerPlan:
                      stream: int = 0) -> None:
         """mfsdp_embed_lookup: out[i] = scale * row (ids[i] - first_id) of the
         entry in params, zeros for an id outside."""
-        status = self._lib.mfsdp_embed_lookup(self._h, entry, _pack_lookup(params, ids, n_ids, id_type, out_type,
-                                                                           first_id, out, out_stride, scale, stream))
+        status = self._lib.mfsdp_embed_lookup(self._h, entry, _pack_lookup(params or 0, ids or 0, n_ids, id_type,
+                                                                           out_type, first_id, out or 0, out_stride,
+                                                                           scale, stream or 0))
         if status:
             _check(status)
 
@@ -374,8 +376,9 @@ class OwnerPlan:
         gradients dout of a lookup of ids (written, or added with
         accumulate)."""
         status = self._lib.mfsdp_embed_grad(
-            self._h, entry, _pack_embed(grads, ids, n_ids, id_type, dout_type, first_id, dout, dout_stride, scale,
-                                        1 if accumulate else 0, workspace, workspace_bytes, stream))
+            self._h, entry, _pack_embed(grads or 0, ids or 0, n_ids, id_type, dout_type, first_id, dout or 0,
+                                        dout_stride, scale, 1 if accumulate else 0, workspace or 0, workspace_bytes,
+                                        stream or 0))
         if status:
             _check(status)
 

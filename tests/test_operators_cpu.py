@@ -195,6 +195,32 @@ def test_embed_grad_refusals():
     assert _status(p.embed_grad, **dict(ok, n_ids=0, ids=0, dout=0, accumulate=True, workspace=0, workspace_bytes=0)) == 0
 
 
+def test_none_is_a_null_address():
+    """None stands for NULL in the operators' calls as it does in the step's: a refusal or a call that needs none."""
+    p = _plan()
+    ws = p.grad_workspace_bytes
+    norm = dict(grads=ADDR, workspace=ADDR, workspace_bytes=ws, stats=ADDR)
+    clip = dict(grads=ADDR, out=ADDR, scale=ADDR, workspace=ADDR, workspace_bytes=ws)
+    step = dict(params=ADDR, grads=ADDR, state=ADDR, workspace=ADDR, workspace_bytes=p.workspace_bytes, step=1,
+                grad_scale=ADDR)
+    lookup = dict(entry=3, params=ADDR, ids=ADDR, n_ids=4, out=ADDR)
+    embed = dict(entry=3, grads=ADDR, ids=ADDR, n_ids=50_000, dout=ADDR, workspace=ADDR, workspace_bytes=1 << 30)
+    for fn, ok, names in ((p.grad_norm, norm, ("grads", "workspace", "stats")),
+                          (p.grad_clip, clip, ("grads", "out", "scale", "workspace")),
+                          (p.step_scaled, step, ("params", "grads", "state", "workspace", "grad_scale")),
+                          (p.embed_lookup, lookup, ("params", "ids", "out")),
+                          (p.embed_grad, embed, ("grads", "ids", "dout", "workspace"))):
+        for name in names:
+            assert _status(fn, **dict(ok, **{name: None, "stream": None})) == INVALID, (fn, name)
+    assert _status(p.grad_norm, **dict(norm, entry_norms=None, stream=None, max_norm=0.0)) == INVALID
+    empty = _plan([E(0, 0, 5)])  # nothing to step: the call returns before any HIP call
+    assert _status(empty.step_scaled, **dict(step, stream=None, ns_out=None)) == 0
+    assert _status(empty.step, **{k: v for k, v in step.items() if k != "grad_scale"}, stream=None, ns_out=None) == 0
+    assert _status(p.embed_lookup, **dict(lookup, n_ids=0, ids=None, out=None, stream=None)) == 0
+    assert _status(p.embed_grad, **dict(embed, n_ids=0, ids=None, dout=None, accumulate=True, workspace=None,
+                                        workspace_bytes=0, stream=None)) == 0
+
+
 def test_embed_workspace_sizes():
     p = _plan()
     assert p.embed_workspace_bytes(3, 0) == 0
