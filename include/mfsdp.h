@@ -268,7 +268,8 @@ mfsdp_status mfsdp_plan_destroy(mfsdp_plan_t plan);
  * Squares and sums are fp64 in a fixed order: results are bitwise the same
  * from run to run, and no finite gradient overflows or vanishes in them.
  * Non-finite gradients propagate by the formulas: a NaN makes norm and scale
- * NaN; an Inf makes norm Inf and scale 0 (so the Inf itself becomes NaN).
+ * NaN; an Inf makes norm Inf and scale 0 (so the Inf itself becomes NaN); with
+ * max_norm INFINITY the scale is 1 all the same.
  * Bytes of the buffers that belong to no entry are neither read into a
  * result nor written. */
 
@@ -343,6 +344,8 @@ mfsdp_status mfsdp_grad_clip(mfsdp_plan_t plan, const mfsdp_grad_clip_args* args
  * the storage type, takes the place of g in the Muon momentum and in AdamW.
  * For fp32 gradients the result is bitwise that of mfsdp_grad_clip followed
  * by mfsdp_owner_step; a scale of 1 gives bitwise mfsdp_owner_step.
+ * It takes the caller's workspace; the step on the library's own
+ * (mfsdp_owner_step_static) has no scaled form: clip the gradients there.
  * Errors: those of mfsdp_owner_step, plus INVALID_ARGUMENT (NULL or
  * misaligned grad_scale). */
 mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* args, const float* grad_scale);
@@ -410,7 +413,7 @@ typedef struct mfsdp_embed_grad_args {
     int64_t dout_stride;      /* elements from one row of dout to the next, >= cols; 0 = cols */
     float scale;
     int32_t accumulate;       /* 0: every row of the entry's gradient is written, zeros where no id
-                                 points; 1: the sums are added to what is there, and rows without an id
+                                 points, whatever the scale; 1: the sums are added to what is there, and rows without an id
                                  are not touched */
     void* workspace;          /* device, mfsdp_plan_embed_workspace_bytes, 256-byte aligned; written
                                  before it is read, so it needs no clearing and may be shared by calls

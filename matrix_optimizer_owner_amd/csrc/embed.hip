@@ -247,8 +247,12 @@ __global__ __launch_bounds__(kZeroThreads) void k_embed_zero(uint8_t* grad, int6
 // No sort and no workspace; the work grows with n^2, so only up to kFewIds.
 // A block has kFewSlabs groups' worth of columns: with one, every row is
 // looked for once more per group of columns, with all, a hot row is summed by
-// one block (2000 ids of 4096 columns: 52 us with 1, 28 with 3, 30 with 4).
-// 512 threads (2000 ids of 1001 columns: 25 us, 32 with 256); past kFewIds the
+// one block.  Added to 5000 rows of bf16, us with 1, 2, 3 and 4: 1000 ids of
+// 4096 columns as in text 26, 18, 16, 19, spread evenly 32, 21, 17, 13, one id
+// over and over 43, 63, 88, 116; 2000 of 1536 columns 21, 16, 20, 20, then 26,
+// 21, 14, 14, then 64, 113, 167, 167.  So a batch of one id is what this is
+// slow at (2000 of 512 columns 56 us, as in text 9).  512 threads (2000 ids of
+// 1536 columns: 20 us, 31 with 256; spread evenly 14 and 11); past kFewIds the
 // sort is faster (at 1500 ids of 256 columns this takes 9 us, the sort 22; at
 // 4096 of 768 columns this 48, the sort 30).
 constexpr int kFewIds = 2048, kFewThreads = 512, kFewSlabs = 3;
@@ -396,7 +400,10 @@ template <int OD, int GD> __global__ __launch_bounds__(kSpanThreads) void k_embe
 // (kRowsHot: with 16000 ids and span 4, a tenth of them on one row, 218 us
 // against 63), by more groups side by side if it is narrow, of at most
 // 2^kRowsNarrow lanes (kRowsIds: 16000 of 96 columns 22 us, sorted 35; 12000
-// of 256 fp32 columns 48 and 35).
+// of 256 fp32 columns 48 and 35).  Below these limits one id over and over is
+// still one block's for each group of columns: 10240 times into 1000 x 512 it
+// takes 273 us (as in text 38), where the sort takes 64 for a table of 50000
+// rows; 8192 times into 2 x 768 it takes 112.
 constexpr int kRowsThreads = 512, kRowsWaves = kRowsThreads / 64, kRowsHot = 10240, kRowsIds = 16384, kRowsNarrow = 4;
 constexpr int64_t kRowsWork = int64_t(16) << 20;
 
@@ -656,7 +663,9 @@ template <bool FIRST, int T> __global__ __launch_bounds__(T) void k_sort_scatter
 // Up to kBlockIds ids into a table of fewer than 2^18 rows: both passes in one
 // block, between them in LDS.  Of a whole gradient of 4096 ids of 768 columns
 // this saves 11 of 43 us, of 8000 into 10000 x 256 3 of 40; at 16384 the block
-// sorts for 42 us where the four launches take 24.
+// sorts for 42 us where the four launches take 24.  The zeros of a written
+// gradient run before this sort, beside the other: in a large table that costs
+// what the block saves (8192 ids into 128256 x 4096 take 208 us, 8193 190).
 constexpr int kBlockThreads = 1024, kBlockWaves = kBlockThreads / 64, kBlockRounds = 8;
 constexpr int kBlockIds = kBlockThreads * kBlockRounds, kBlockBits = 9;
 
@@ -795,7 +804,8 @@ template <int OD, int GD, bool ACC> __global__ __launch_bounds__(kSumThreads) vo
         // a short run that started before the chunk has moved q0 past the chunk's end already
         if (!tail && q0 < q1) q1 = lower_bound(K, kRunMax + q1, win, kt + 1) - kRunMax;
     }
-    // of ACC, what a finished row's sum is added to is on its way with the batch that finishes it
+    // of ACC, what a finished row's sum is added to is on its way with the batch that finishes it; eight of both in
+    // flight take the same time as four (65536 ids of 768 fp32 columns 74.4 us both, 4096 29.6 and 30.6)
     constexpr int kUnroll = ACC ? 4 : 8;
     float acc[kPer] = {};
     for (int q = q0; q < q1; q += kUnroll) {

@@ -209,6 +209,8 @@ __global__ __launch_bounds__(kNormThreads) void k_grad_norm(NormArgs a) {
     }
 }
 
+// One thread, a record after another: a call takes 4.3 us for 8 owners, 4.5
+// for 64, 166 for 4096.
 __global__ void k_grad_total(const mfsdp_grad_stats* parts, int count, mfsdp_grad_stats* stats, double max_norm,
                              double eps) {
     double s = 0.0;

@@ -62,7 +62,9 @@ constexpr int64_t kGradChunkMax = int64_t(1) << 30;
 // The norm's shares.  Cost counts slices, and kNormPieceCost more for each
 // piece (about what its descriptor, its sum and its drained loads take), so
 // that many small tensors spread over more blocks.  One share for every
-// kNormShareMin of cost, at most kNormBlocks.
+// kNormShareMin of cost, at most kNormBlocks.  (65 tensors of 16 KB take 5.6,
+// 5.5, 6.2 and 8.2 us with a kNormShareMin of 2, 4, 8 and 16; 71 ragged ones,
+// 7.1 MB, 7.3, 7.4, 7.5 and 12.1.)
 constexpr int64_t kNormPieceCost = 2;
 constexpr int64_t kNormShareMin = 8;
 constexpr int64_t kNormBlocks = 1024;
