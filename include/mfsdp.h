@@ -24,7 +24,8 @@
  * Per AdamW tail tensor (1-based step t):
  *   m <- b1*m + (1-b1)*g;  v <- b2*v + (1-b2)*g^2;
  *   W <- W*(1 - lr_a*wd_a) - lr_a*(m/(1-b1^t)) / (sqrt(v/(1-b2^t)) + eps_a).
- * Every stored value is rounded once to its storage type, to nearest-even.
+ * Every stored value is rounded once to its storage type, to nearest-even
+ * (moments in 8 bits as described at mfsdp_moments_args).
  *
  * Ownership.  The caller allocates every device buffer (params, grads,
  * state, workspace, ns_out).  The library never allocates device memory.
@@ -62,7 +63,8 @@ typedef enum mfsdp_dtype {
 typedef enum mfsdp_role {
     MFSDP_ROLE_AUTO = 0,   /* Muon iff rows > 1 and cols > 1, else AdamW */
     MFSDP_ROLE_MUON = 1,   /* force Muon (rows >= 1, cols >= 1) */
-    MFSDP_ROLE_ADAMW = 2   /* force AdamW */
+    MFSDP_ROLE_ADAMW = 2,  /* force AdamW */
+    MFSDP_ROLE_ADAMW8 = 3  /* AdamW with its moments in 8 bits: 2.06 state bytes an element in place of 8 */
 } mfsdp_role;
 
 /* One whole tensor of the owner buffer (one row of the owner table).
@@ -120,11 +122,13 @@ typedef struct mfsdp_plan_s* mfsdp_plan_t;
 
 /* Per-entry layout facts a caller needs to read or seed state. */
 typedef struct mfsdp_entry_info {
-    int32_t role;             /* resolved: MFSDP_ROLE_MUON, MFSDP_ROLE_ADAMW, or -1 for an empty entry */
+    int32_t role;             /* resolved: MFSDP_ROLE_MUON, MFSDP_ROLE_ADAMW, MFSDP_ROLE_ADAMW8, or -1 for an
+                                 empty entry */
     int32_t transposed;       /* Muon: 1 if rows > cols (Newton-Schulz runs on the transpose) */
     int64_t m, n;             /* Muon: oriented shape, m = min(rows, cols) */
-    uint64_t state_offset;    /* Muon: momentum (momentum_dtype); AdamW: fp32 first moment (bytes into state) */
-    uint64_t state_offset2;   /* AdamW: fp32 second moment (bytes into state); 0 otherwise */
+    uint64_t state_offset;    /* Muon: momentum (momentum_dtype); AdamW: fp32 first moment, or its codes and
+                                 scales for MFSDP_ROLE_ADAMW8 (bytes into state) */
+    uint64_t state_offset2;   /* AdamW: the second moment likewise (bytes into state); 0 otherwise */
     uint64_t ns_out_offset;   /* Muon: element offset of the fp32 O export in ns_out */
     float lr_scale;           /* Muon: the shape scale applied to lr */
 } mfsdp_entry_info;
@@ -181,7 +185,7 @@ mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n, uint64_t p
 
 /* Bytes of optimizer state the plan lays out (momentum for Muon entries, fp32
  * or bf16 by hp->momentum_dtype, then fp32 first and second moments for AdamW
- * entries), each region 256-byte aligned. */
+ * entries, then those in 8 bits), each region 256-byte aligned. */
 mfsdp_status mfsdp_plan_state_bytes(mfsdp_plan_t plan, uint64_t* bytes);
 
 /* Bytes of device workspace one step needs (descriptors, norm partials,
@@ -350,6 +354,63 @@ mfsdp_status mfsdp_grad_clip(mfsdp_plan_t plan, const mfsdp_grad_clip_args* args
  * misaligned grad_scale). */
 mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* args, const float* grad_scale);
 
+/* ---- AdamW moments in 8 bits ----
+ *
+ * An entry with the role MFSDP_ROLE_ADAMW8 takes the AdamW step of
+ * mfsdp_owner_step (and its scaled and static forms) with both moments held
+ * in 8 bits; entries of either kind may share a table, and the small ones
+ * are best left in 32.  A group of 128 consecutive elements (the last one of
+ * a tensor may be shorter) shares an fp32 scale for each moment, the largest
+ * magnitude in it:
+ *
+ *   m = scale_m * c*|c| / 127^2,  c an int8 in -127..127;
+ *   sqrt(v) = scale_r * (d / 255)^2,  d a uint8 in 0..255, at least 1 where v > 0.
+ *
+ * In the state each moment is a byte an element at state_offset (first) or
+ * state_offset2 (second), and from the next multiple of 256 bytes after
+ * rows*cols of them on, one scale a group.  A state of zeros is m = v = 0.
+ *
+ * The step forms m, v and the parameter in fp32 from the values held, the
+ * parameter from m and v before they are rounded.  Codes are rounded down
+ * after a dither in (0, 1) is added that step count (its low 32 bits), entry
+ * index and element index alone fix, so that slow averages (beta2 = 0.999)
+ * move by less than a code step on average and results are bitwise the same
+ * from run to run:
+ *   mix(h): h ^= h>>16; h *= 0x85ebca6b; h ^= h>>13; h *= 0xc2b2ae35; h ^= h>>16;
+ *   key = mix(step + 0x9e3779b9 * (entry + 1));
+ *   word = mix((index>>1) + 0x9e3779b9 * (index>>33) + key), in 32 bits;
+ *   bytes 0 and 1 of it are of an even element's m and sqrt(v), 2 and 3 of
+ *   the odd one's; the dither is (byte + 0.5) / 256.
+ * Non-finite moments: a group that holds one is NaN from then on (its
+ * parameters of that step follow the formulas).  Both moments are kept for
+ * gradients down to 1e-37; a squared gradient above the fp32 range counts as
+ * non-finite.
+ *
+ * mfsdp_moments_read and mfsdp_moments_write turn an entry's state into
+ * values and back, for a run that goes over to 8 bits or back, or a
+ * checkpoint in another form. */
+typedef struct mfsdp_moments_args {
+    void* state;              /* device, the owner's state; 256-byte aligned; read does not write it */
+    void* first;              /* device, rows*cols values of type: the first moment; 16-byte aligned */
+    void* second;             /* device, as first: the second moment (v, not its root) */
+    int32_t type;             /* mfsdp_dtype of first and second */
+    void* stream;
+} mfsdp_moments_args;
+
+/* first, second <- the moments of entry `entry` (MFSDP_ROLE_ADAMW or
+ * MFSDP_ROLE_ADAMW8), rounded once to type.  Enqueues one launch (more for
+ * more than 2^35 elements), so it can be captured; the current device must be
+ * the stream's and the buffers'.  An empty entry does nothing.
+ * Errors: INVALID_ARGUMENT (null or misaligned pointer, entry out of range),
+ * UNSUPPORTED (type, an entry with another role), HIP. */
+mfsdp_status mfsdp_moments_read(mfsdp_plan_t plan, int64_t entry, const mfsdp_moments_args* args);
+
+/* The entry's state <- first, second: in 8 bits to the nearest code (no
+ * dither), else rounded to fp32.  A negative or NaN second moment makes its
+ * group NaN in 8 bits.  What is read must not overlap the state.
+ * Errors: as mfsdp_moments_read. */
+mfsdp_status mfsdp_moments_write(mfsdp_plan_t plan, int64_t entry, const mfsdp_moments_args* args);
+
 /* ---- An embedding table of the owner buffer ----
  *
  * An embedding is a 2D tensor that trains with AdamW (role
@@ -442,9 +503,11 @@ mfsdp_status mfsdp_embed_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_embe
  * read, param read and write, momentum read and write, the Newton-Schulz
  * input write; es = param bytes, em = momentum bytes (4, or 2 with
  * momentum_dtype MFSDP_BF16), es_ns = 2 for bf16 Newton-Schulz, 4 for fp32);
- * AdamW: rows*cols * (3 es + 16) / byte_rate.
+ * AdamW: rows*cols * (3 es + 16) / byte_rate; MFSDP_ROLE_ADAMW8: rows*cols *
+ * (3 es + 4) / byte_rate and 16 B for each group of 128 elements.
  * Memory of a tensor on its owner: params and grads (2 es per element),
- * state (em B per element for Muon, 8 for AdamW), and for Muon the
+ * state (em B per element for Muon, 8 for AdamW, a byte for each moment and
+ * the scales for MFSDP_ROLE_ADAMW8), and for Muon the
  * Newton-Schulz buffers of mfsdp_plan_create (two X^T of n_p x m_p and A, B
  * of m_p x m_p, m_p and n_p padded to 256, es_ns per element), each region
  * rounded up to 256 bytes.  (The plan's descriptor blob and norm partials,
@@ -475,7 +538,8 @@ typedef struct mfsdp_partition_params {
 
 typedef struct mfsdp_tensor_place {
     int32_t owner;            /* 0 .. n_owners-1 */
-    int32_t role;             /* resolved: MFSDP_ROLE_MUON or MFSDP_ROLE_ADAMW (empty tensors: ADAMW) */
+    int32_t role;             /* resolved: MFSDP_ROLE_MUON, MFSDP_ROLE_ADAMW or MFSDP_ROLE_ADAMW8 (empty
+                                 tensors: ADAMW) */
     uint64_t offset;          /* bytes into the owner's flat parameter buffer: the owner's tensors in
                                  input order, each at a 256-byte aligned offset */
     double cost;              /* seconds, by the model above */
@@ -507,8 +571,10 @@ mfsdp_status mfsdp_owner_partition(const mfsdp_tensor* tensors, int64_t n, const
  *
  * For entry i of the plan's table (numel = rows*cols):
  *   tensors[i]  numel parameter elements in the entry's dtype, row-major;
- *   state1[i]   numel elements: Muon momentum (the plan's momentum_dtype), or AdamW first moment (fp32);
- *   state2[i]   numel fp32: AdamW second moment (unused for Muon).
+ *   state1[i]   numel elements: Muon momentum (the plan's momentum_dtype), or AdamW first moment (fp32;
+ *               MFSDP_ROLE_ADAMW8: the codes and scales as they lie in the state, from state_offset to the
+ *               last scale, numel rounded up to 256 and 4 bytes for each group of 128 elements);
+ *   state2[i]   numel fp32: AdamW second moment (likewise; unused for Muon).
  * Any array pointer may be NULL (that part is not copied); an element may be
  * NULL where numel is 0 or the part does not apply.  params / state are the
  * owner's buffers (param_bytes >= the end of its last tensor, state_bytes >=

@@ -19,7 +19,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmfsdp.so")
 
 F32, BF16 = 0, 1
-ROLE_AUTO, ROLE_MUON, ROLE_ADAMW = 0, 1, 2
+ROLE_AUTO, ROLE_MUON, ROLE_ADAMW, ROLE_ADAMW8 = 0, 1, 2, 3
 STEP_DESCRIPTORS_RESIDENT = 1
 I32, I64 = 0, 1  # mfsdp_id_type
 STATIC_WORKSPACE_BYTES = 64 << 20  # MFSDP_STATIC_WORKSPACE_BYTES
@@ -125,6 +125,11 @@ class EmbedGradArgs(ctypes.Structure):
                 ("stream", ctypes.c_void_p)]
 
 
+class MomentsArgs(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("first", ctypes.c_void_p), ("second", ctypes.c_void_p),
+                ("type", ctypes.c_int32), ("stream", ctypes.c_void_p)]
+
+
 _PACK = {ctypes.c_void_p: "P", ctypes.c_uint64: "Q", ctypes.c_int64: "q", ctypes.c_uint32: "I", ctypes.c_int32: "i",
          ctypes.c_double: "d", ctypes.c_float: "f"}
 
@@ -141,6 +146,7 @@ def _packer(mirror):
 
 _pack_norm, _pack_clip = _packer(GradNormArgs), _packer(GradClipArgs)
 _pack_lookup, _pack_embed, _pack_step = _packer(EmbedLookupArgs), _packer(EmbedGradArgs), _packer(StepArgs)
+_pack_moments = _packer(MomentsArgs)
 
 EXPORTS = (
     "mfsdp_plan_create", "mfsdp_plan_state_bytes", "mfsdp_plan_workspace_bytes", "mfsdp_plan_ns_out_elems",
@@ -148,6 +154,7 @@ EXPORTS = (
     "mfsdp_owner_step", "mfsdp_owner_step_static", "mfsdp_owner_step_scaled", "mfsdp_plan_destroy",
     "mfsdp_plan_grad_workspace_bytes", "mfsdp_grad_norm", "mfsdp_grad_total", "mfsdp_grad_clip",
     "mfsdp_plan_embed_workspace_bytes", "mfsdp_embed_lookup", "mfsdp_embed_grad",
+    "mfsdp_moments_read", "mfsdp_moments_write",
     "mfsdp_owner_partition", "mfsdp_owner_gather", "mfsdp_owner_scatter", "mfsdp_status_string",
     "mfsdp_last_error_message", "mfsdp_probe_mfma_bf16", "mfsdp_probe_hbm",
 )
@@ -184,6 +191,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mfsdp_plan_embed_workspace_bytes.argtypes = [P, ctypes.c_int64, ctypes.c_int64, u64p]
     lib.mfsdp_embed_lookup.argtypes = [P, ctypes.c_int64, P]
     lib.mfsdp_embed_grad.argtypes = [P, ctypes.c_int64, P]
+    lib.mfsdp_moments_read.argtypes = [P, ctypes.c_int64, P]
+    lib.mfsdp_moments_write.argtypes = [P, ctypes.c_int64, P]
     lib.mfsdp_plan_destroy.argtypes = [P]
     lib.mfsdp_owner_partition.argtypes = [ctypes.POINTER(Tensor), ctypes.c_int64, ctypes.POINTER(PartitionParams),
                                           ctypes.POINTER(TensorPlace), ctypes.POINTER(ctypes.c_double), u64p, u64p]
@@ -379,6 +388,22 @@ class OwnerPlan:
             self._h, entry, _pack_embed(grads or 0, ids or 0, n_ids, id_type, dout_type, first_id, dout or 0,
                                         dout_stride, scale, 1 if accumulate else 0, workspace or 0, workspace_bytes,
                                         stream or 0))
+        if status:
+            _check(status)
+
+    def moments_read(self, entry: int, state: int, first: int, second: int, type: int = F32, stream: int = 0) -> None:
+        """mfsdp_moments_read: the entry's AdamW moments in state, held in 32
+        bits or in 8, as values of `type` into first and second."""
+        status = self._lib.mfsdp_moments_read(self._h, entry, _pack_moments(state or 0, first or 0, second or 0, type,
+                                                                            stream or 0))
+        if status:
+            _check(status)
+
+    def moments_write(self, entry: int, state: int, first: int, second: int, type: int = F32, stream: int = 0) -> None:
+        """mfsdp_moments_write: the entry's moments in state from the values
+        at first and second."""
+        status = self._lib.mfsdp_moments_write(self._h, entry, _pack_moments(state or 0, first or 0, second or 0, type,
+                                                                             stream or 0))
         if status:
             _check(status)
 

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libmfsdp.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["plan.cpp", "grad_plan.cpp", "owner_planner.cpp", "checkpoint.cpp", "step.hip", "elementwise.hip",
-           "grad.hip", "embed.hip", "ns_gemm.hip", "probe.hip"]
+           "adam8.hip", "grad.hip", "embed.hip", "ns_gemm.hip", "probe.hip"]
 ARCH = "gfx950"
 
 

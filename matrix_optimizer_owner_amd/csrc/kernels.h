@@ -30,6 +30,10 @@ hipError_t launch_final_from_x(int ns_precision, const WorkspaceMap& map, const 
 hipError_t launch_adamw(const WorkspaceMap& map, const mfsdp_hparams& hp, int64_t step,
                         const StepBuffers& b, hipStream_t stream);
 
+// AdamW over every tail tensor with moments in 8 bits.
+hipError_t launch_adamw8(const WorkspaceMap& map, const mfsdp_hparams& hp, int64_t step,
+                         const StepBuffers& b, hipStream_t stream);
+
 // One phase of Newton-Schulz iteration `iter` (1-based) over every matrix:
 // phase 0 Gram, 1 polynomial, 2 update (the last iteration's update applies
 // the parameter update).

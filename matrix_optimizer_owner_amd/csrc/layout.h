@@ -4,7 +4,8 @@
 // Workspace map (byte offsets, all 256-byte aligned):
 //   [desc]      descriptor blob written by the step from the plan:
 //                 MatDesc[n_mat], k1_begin[n_mat+1], Tile gram[], Tile poly[],
-//                 Tile upd[], TailDesc[n_tail], tail_begin[n_tail+1]
+//                 Tile upd[], TailDesc[n_tail], tail_begin[n_tail+1], and the
+//                 same two of the tail tensors with moments in 8 bits
 //   [s]         float[n_mat]: 1/(||U||_F + eps) per Muon matrix
 //   [partials]  float[n_k1_blocks]: sum of u^2 over one momentum-kernel tile
 //   per matrix: XT0 and XT1 (np x mp, ping-pong), A and B (mp x mp) in the
@@ -47,6 +48,7 @@ constexpr int kK1Tile = 128;       // tile edge of the momentum kernel
 constexpr int kBlockRows = 256;    // rows of a panel block of the Newton-Schulz buffers
 constexpr int kBlockBytes = 128;   // bytes of a panel block's row
 constexpr int kTailChunk = 2048;   // elements per AdamW block
+constexpr int kGroup = 128;        // elements of a moment in 8 bits that share a scale
 constexpr uint64_t kAlign = 256;
 
 enum Dtype : int32_t { kF32 = 0, kBF16 = 1 };
@@ -77,11 +79,11 @@ struct Tile {
 
 struct TailDesc {
     uint64_t param_off;    // bytes into params and grads
-    uint64_t m1_off;       // bytes into state (fp32)
-    uint64_t m2_off;       // bytes into state (fp32)
+    uint64_t m1_off;       // bytes into state (fp32; or codes and scales, see Codes)
+    uint64_t m2_off;       // bytes into state (likewise)
     int64_t numel;
     int32_t dtype;
-    int32_t pad_;
+    int32_t entry;         // its index in the table
 };
 
 static_assert(sizeof(MatDesc) == 8 * 8 + 4 * 10, "MatDesc layout");
@@ -93,15 +95,24 @@ static_assert(sizeof(TailDesc) == 40, "TailDesc layout");
 struct WorkspaceMap {
     uint64_t desc_bytes;
     uint64_t off_mat, off_k1_begin, off_gram, off_poly, off_upd, off_upd_tail, off_tail, off_tail_begin;
+    uint64_t off_tail8, off_tail8_begin;     // tail tensors with moments in 8 bits
     uint64_t off_s, off_partials;
     uint64_t total_bytes;
     int32_t n_mat, n_tail;
     int32_t n_gram, n_poly, n_upd;
     int32_t n_upd_tail;                      // 128-tiles run after the 256-tile update list (see the planner)
     int32_t n_k1_blocks, n_tail_chunks;
+    int32_t n_tail8, n_tail8_chunks;
     int32_t tile_gram, tile_poly, tile_upd;  // tile edge of each contraction phase
 };
 
 inline uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
+
+// One moment of a tensor in 8 bits: a byte an element, then from the next
+// multiple of 256 bytes on an fp32 scale a group of kGroup elements.
+struct Codes {
+    static uint64_t scales(uint64_t numel) { return align_up(numel, kAlign); }  // offset of the scales
+    static uint64_t bytes(uint64_t numel) { return scales(numel) + (numel + kGroup - 1) / kGroup * 4; }
+};
 
 }  // namespace mfsdp

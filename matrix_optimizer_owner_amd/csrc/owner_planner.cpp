@@ -66,7 +66,8 @@ extern "C" mfsdp_status mfsdp_owner_partition(const mfsdp_tensor* tensors, int64
                 return fail(MFSDP_ERR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": negative dimension");
             if (t.dtype != kF32 && t.dtype != kBF16)
                 return fail(MFSDP_ERR_UNSUPPORTED, "tensor " + std::to_string(i) + ": unsupported dtype");
-            if (t.role != MFSDP_ROLE_AUTO && t.role != MFSDP_ROLE_MUON && t.role != MFSDP_ROLE_ADAMW)
+            if (t.role != MFSDP_ROLE_AUTO && t.role != MFSDP_ROLE_MUON && t.role != MFSDP_ROLE_ADAMW &&
+                t.role != MFSDP_ROLE_ADAMW8)
                 return fail(MFSDP_ERR_UNSUPPORTED, "tensor " + std::to_string(i) + ": unknown role");
             if (t.rows > kMaxDim || t.cols > kMaxDim)
                 return fail(MFSDP_ERR_UNSUPPORTED, "tensor " + std::to_string(i) + ": dimension above 2^22");
@@ -89,6 +90,9 @@ extern "C" mfsdp_status mfsdp_owner_partition(const mfsdp_tensor* tensors, int64
                           double(numel) * double(3 * es + 2 * es_mom + uint64_t(es_ns)) / pp->byte_rate;
                 it.mem = 2 * region(numel * es) + region(numel * es_mom) + 2 * region(ld * np * uint64_t(es_ns)) +
                          2 * region(ld * mp * uint64_t(es_ns));
+            } else if (role == MFSDP_ROLE_ADAMW8) {
+                it.cost = (double(numel) * double(3 * es + 4) + double((numel + kGroup - 1) / kGroup) * 16.0) / pp->byte_rate;
+                it.mem = 2 * region(numel * es) + 2 * region(Codes::bytes(numel));
             } else {
                 it.cost = double(numel) * double(3 * es + 16) / pp->byte_rate;
                 it.mem = 2 * region(numel * es) + 2 * region(numel * 4);

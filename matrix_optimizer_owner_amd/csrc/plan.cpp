@@ -143,7 +143,8 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
                 delete plan;
                 return fail(MFSDP_ERR_UNSUPPORTED, "entry " + std::to_string(i) + ": unsupported dtype");
             }
-            if (e.role != MFSDP_ROLE_AUTO && e.role != MFSDP_ROLE_MUON && e.role != MFSDP_ROLE_ADAMW) {
+            if (e.role != MFSDP_ROLE_AUTO && e.role != MFSDP_ROLE_MUON && e.role != MFSDP_ROLE_ADAMW &&
+                e.role != MFSDP_ROLE_ADAMW8) {
                 delete plan;
                 return fail(MFSDP_ERR_UNSUPPORTED, "entry " + std::to_string(i) + ": unknown role");
             }
@@ -188,7 +189,7 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
                             "entries " + std::to_string(i) + " and " + std::to_string(j) + " overlap");
             }
 
-        // ---- state layout: Muon momentum (momentum_dtype), then AdamW moments (fp32) ----
+        // ---- state layout: Muon momentum (momentum_dtype), then AdamW moments (fp32), then those in 8 bits ----
         // every region is followed by `guard` unused bytes (0 unless the
         // caller asked for guard bands)
         const uint64_t guard = align_up(uint64_t(hp->guard_bytes), kAlign);
@@ -212,6 +213,13 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
             const uint64_t numel = uint64_t(entries[i].rows) * uint64_t(entries[i].cols);
             inf.state_offset = state_region(numel * 4, i);
             inf.state_offset2 = state_region(numel * 4, i);
+        }
+        for (int64_t i = 0; i < n; ++i) {
+            mfsdp_entry_info& inf = plan->info[size_t(i)];
+            if (inf.role != MFSDP_ROLE_ADAMW8) continue;
+            const uint64_t numel = uint64_t(entries[i].rows) * uint64_t(entries[i].cols);
+            inf.state_offset = state_region(Codes::bytes(numel), i);
+            inf.state_offset2 = state_region(Codes::bytes(numel), i);
         }
         plan->state_bytes = soff;
 
@@ -256,22 +264,35 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
         }
         plan->ns_out_elems = ns_off;
 
-        std::vector<TailDesc> tails;
-        std::vector<int32_t> tail_begin(1, 0);
-        for (int64_t i = 0; i < n; ++i) {
-            const mfsdp_entry_info& inf = plan->info[size_t(i)];
-            if (inf.role != MFSDP_ROLE_ADAMW) continue;
-            TailDesc t;
-            std::memset(&t, 0, sizeof(t));
-            t.param_off = entries[i].offset;
-            t.m1_off = inf.state_offset;
-            t.m2_off = inf.state_offset2;
-            t.numel = entries[i].rows * entries[i].cols;
-            t.dtype = entries[i].dtype;
-            tails.push_back(t);
-            const int64_t chunks = (t.numel + kTailChunk - 1) / kTailChunk;
-            tail_begin.push_back(int32_t(tail_begin.back() + chunks));
+        // the tail tensors of one role and the first chunk of each
+        std::vector<TailDesc> tails, tails8;
+        std::vector<int32_t> tail_begin, tail8_begin;
+        auto list_tails = [&](int role, std::vector<TailDesc>& list, std::vector<int32_t>& begin) {
+            int64_t total = 0;
+            begin.push_back(0);
+            for (int64_t i = 0; i < n; ++i) {
+                const mfsdp_entry_info& inf = plan->info[size_t(i)];
+                if (inf.role != role) continue;
+                TailDesc t;
+                std::memset(&t, 0, sizeof(t));
+                t.param_off = entries[i].offset;
+                t.m1_off = inf.state_offset;
+                t.m2_off = inf.state_offset2;
+                t.numel = entries[i].rows * entries[i].cols;
+                t.dtype = entries[i].dtype;
+                t.entry = int32_t(i);
+                list.push_back(t);
+                total += (t.numel + kTailChunk - 1) / kTailChunk;
+                if (total > int64_t(INT32_MAX)) return false;
+                begin.push_back(int32_t(total));
+            }
+            return true;
+        };
+        if (!list_tails(MFSDP_ROLE_ADAMW, tails, tail_begin) || !list_tails(MFSDP_ROLE_ADAMW8, tails8, tail8_begin)) {
+            delete plan;
+            return fail(MFSDP_ERR_UNSUPPORTED, "owner buffer too large for one step");
         }
+        if (tails8.empty()) tail8_begin.clear();  // a table without them keeps its workspace as it was
 
         // ---- grouped tile lists, longest contraction first ----
         const int nm = int(mats.size());
@@ -336,7 +357,7 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
             }
             k1_begin.push_back(int32_t(k1_begin.back() + blocks));
         }
-        if (upd.size() > size_t(INT32_MAX) || tail_begin.back() < 0) {
+        if (upd.size() > size_t(INT32_MAX)) {
             delete plan;
             return fail(MFSDP_ERR_UNSUPPORTED, "owner buffer too large for one step");
         }
@@ -365,6 +386,8 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
         w.off_upd_tail = section(upd_tail.size() * sizeof(Tile));
         w.off_tail = section(tails.size() * sizeof(TailDesc));
         w.off_tail_begin = section(tail_begin.size() * sizeof(int32_t));
+        w.off_tail8 = section(tails8.size() * sizeof(TailDesc));
+        w.off_tail8_begin = section(tail8_begin.size() * sizeof(int32_t));
         w.desc_bytes = off;
         // the descriptor blob is uploaded by one copy, so it is one region
         plan->regions.push_back(mfsdp_region{0, off, MFSDP_BUFFER_WORKSPACE, -1});
@@ -389,6 +412,8 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
         w.n_upd_tail = int32_t(upd_tail.size());
         w.n_k1_blocks = k1_begin.back();
         w.n_tail_chunks = tail_begin.back();
+        w.n_tail8 = int32_t(tails8.size());
+        w.n_tail8_chunks = tails8.empty() ? 0 : tail8_begin.back();
         w.tile_gram = tg;
         w.tile_poly = tp;
         w.tile_upd = tu;
@@ -405,6 +430,8 @@ extern "C" mfsdp_status mfsdp_plan_create(const mfsdp_entry* entries, int64_t n,
         put(w.off_upd_tail, upd_tail.data(), upd_tail.size() * sizeof(Tile));
         put(w.off_tail, tails.data(), tails.size() * sizeof(TailDesc));
         put(w.off_tail_begin, tail_begin.data(), tail_begin.size() * sizeof(int32_t));
+        put(w.off_tail8, tails8.data(), tails8.size() * sizeof(TailDesc));
+        put(w.off_tail8_begin, tail8_begin.data(), tail8_begin.size() * sizeof(int32_t));
     } catch (const std::bad_alloc&) {
         delete plan;
         return fail(MFSDP_ERR_INTERNAL, "out of host memory");

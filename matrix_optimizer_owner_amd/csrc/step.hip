@@ -32,7 +32,7 @@ mfsdp_status check_args(mfsdp_plan_t plan, const mfsdp_step_args* args) {
     if (reinterpret_cast<uintptr_t>(args->params) % 16 != 0 || reinterpret_cast<uintptr_t>(args->grads) % 16 != 0 ||
         (args->state && reinterpret_cast<uintptr_t>(args->state) % kAlign != 0))
         return fail(MFSDP_ERR_INVALID_ARGUMENT, "params/grads must be 16-byte aligned and state 256-byte aligned");
-    if (map.n_tail > 0 && args->step < 1)
+    if (map.n_tail + map.n_tail8 > 0 && args->step < 1)
         return fail(MFSDP_ERR_INVALID_ARGUMENT, "step must be >= 1 (AdamW bias correction is 1-based)");
     if (args->ns_out && reinterpret_cast<uintptr_t>(args->ns_out) % 16 != 0)
         return fail(MFSDP_ERR_INVALID_ARGUMENT, "ns_out must be 16-byte aligned");
@@ -68,6 +68,10 @@ mfsdp_status enqueue_step(mfsdp_plan_t plan, const mfsdp_step_args* args, uint8_
     if (map.n_tail > 0) {
         e = launch_adamw(map, plan->hp, args->step, b, stream);
         if (e != hipSuccess) return hip_fail(e, "AdamW launch");
+    }
+    if (map.n_tail8 > 0) {
+        e = launch_adamw8(map, plan->hp, args->step, b, stream);
+        if (e != hipSuccess) return hip_fail(e, "AdamW launch (moments in 8 bits)");
     }
     if ((e = mark(1)) != hipSuccess) return hip_fail(e, "event record");
     const int prec = plan->hp.ns_precision;
@@ -112,7 +116,7 @@ uint64_t g_static_last_plan[kMaxDevices] = {};  // plan whose descriptors the ar
 // The step on the caller's workspace, for both entry points.
 mfsdp_status step_on_caller_workspace(mfsdp_plan_t plan, const mfsdp_step_args* args, const float* grad_scale) {
     const WorkspaceMap& map = plan->map;
-    if (map.n_mat == 0 && map.n_tail == 0) return MFSDP_OK;  // nothing but empty shards
+    if (map.n_mat == 0 && map.n_tail == 0 && map.n_tail8 == 0) return MFSDP_OK;  // nothing but empty shards
     if (mfsdp_status st = check_args(plan, args); st != MFSDP_OK) return st;
     if (!args->workspace) return fail(MFSDP_ERR_INVALID_ARGUMENT, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(args->workspace) % kAlign != 0)
@@ -146,7 +150,7 @@ extern "C" mfsdp_status mfsdp_owner_step_static(mfsdp_plan_t plan, const mfsdp_s
     clear_error();
     if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
     const WorkspaceMap& map = plan->map;
-    if (map.n_mat == 0 && map.n_tail == 0) return MFSDP_OK;
+    if (map.n_mat == 0 && map.n_tail == 0 && map.n_tail8 == 0) return MFSDP_OK;
     if (mfsdp_status st = check_args(plan, args); st != MFSDP_OK) return st;
     if (args->workspace || args->workspace_bytes)
         return fail(MFSDP_ERR_INVALID_ARGUMENT,
