@@ -385,10 +385,11 @@ def _own_logp(s, stream):
                           s["space"].data_ptr(), s["space"].numel(), ids=s["ids"].data_ptr(), first_id=first,
                           logp=s["logp"].data_ptr() if alone else 0, entropy=s["entropy"].data_ptr() if alone else 0,
                           top_k=k, top_ids=s["top_ids"][i].data_ptr() if k else 0,
-                          top_logp=s["top_logp"][i].data_ptr() if k else 0, stream=stream, **s["call"])
+                          top_logp=s["top_logp"][i].data_ptr() if k and alone else 0,
+                          top_logits=s["top_logp"][i].data_ptr() if k and not alone else 0, stream=stream, **s["call"])
     if not alone:
         s["total"](records, len(parts), n, records, logp=s["logp"].data_ptr(), entropy=s["entropy"].data_ptr(), top_k=k,
-                   part_top_ids=s["top_ids"].data_ptr() if k else 0, part_top_logp=s["top_logp"].data_ptr() if k else 0,
+                   part_top_ids=s["top_ids"].data_ptr() if k else 0, part_top_logits=s["top_logp"].data_ptr() if k else 0,
                    top_ids=s["all_ids"].data_ptr() if k else 0, top_logp=s["all_logp"].data_ptr() if k else 0, stream=stream)
     return [s["logp"], s["entropy"]] + ([s["all_ids"], s["all_logp"]] if k else [])
 
