@@ -489,6 +489,150 @@ typedef struct mfsdp_embed_grad_args {
  * UNSUPPORTED (id_type, dout_type), WORKSPACE_TOO_SMALL, HIP. */
 mfsdp_status mfsdp_embed_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_embed_grad_args* args);
 
+/* ---- The output head over a table of the owner buffer ----
+ *
+ * A table as above read the other way: logits of a row x_i of activations
+ * over the table's rows, z_ij = scale * x_i . W_j, and from them
+ *
+ *   logp_i    = z_it - log sum_j e^z_ij, t = id_i - first_id;
+ *   entropy_i = -sum_j p_ij ln p_ij,  p_ij = e^z_ij / sum_k e^z_ik;
+ *   the top_k rows with the largest z_ij, largest first, ties to the lower id.
+ *
+ * The table may be any 2D entry of up to 2^20 columns, bf16 or fp32, tied to
+ * the embedding or not.  Logits are sums in fp32 of products of the values
+ * given, bf16 or fp32 (exact, but for at most 2^-22 of a product of two fp32
+ * values); the sums over them are fp32 in an order that sizes alone fix
+ * (bitwise the same from run to run, no atomics).
+ *
+ * A negative id marks padding: log probability and entropy 0, no
+ * alternatives, no gradient, and whatever x holds there (NaN too) is not read
+ * into a result.  An id of 0 or more outside the table has no target here:
+ * its log probability is 0 and has no gradient, its entropy and alternatives
+ * are the table's.  ids may be NULL: every row counts and none has a target.
+ * Non-finite logits propagate by the formulas: a NaN or +Inf makes the row's
+ * log probability and entropy NaN; a NaN is never among the alternatives.  An
+ * infinite value of an fp32 x or table may make a logit NaN where the formula
+ * has an infinite one.
+ *
+ * A vocabulary cut into several entries: mfsdp_head_logprob on each with its
+ * own first_id, then mfsdp_head_total joins the records (and alternatives),
+ * and mfsdp_head_grad of each entry takes the joined ones; dx is then the sum
+ * of the entries' dx.
+ *
+ * The calls only enqueue launches on the stream, so they can be captured; the
+ * current device must be the stream's and the buffers'.  What a call writes
+ * must not overlap what it reads or anything else it writes, but for
+ * mfsdp_head_total's records. */
+
+/* What a row's distribution is known by, in base 2 (y = log2(e) * z). */
+typedef struct mfsdp_head_record {
+    float max;                /* largest y */
+    float sum;                /* sum of 2^(y - max) */
+    float wsum;               /* sum of 2^(y - max) * (y - max) */
+    float target;             /* y of the target, 0 without one */
+    int32_t found;            /* 1: the target is among the rows summed */
+    int32_t active;           /* 0: padding (all other fields are 0 then) */
+} mfsdp_head_record;
+
+/* Device workspace of mfsdp_head_logprob on up to n rows with up to top_k
+ * alternatives, and with grad = 1 of mfsdp_head_grad on as many too (about
+ * n * rows elements more).  It never falls as n grows, so one for the largest
+ * batch serves every smaller one.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (as mfsdp_head_logprob). */
+mfsdp_status mfsdp_plan_head_workspace_bytes(mfsdp_plan_t plan, int64_t entry, int64_t n, int32_t x_type,
+                                             int32_t top_k, int32_t grad, uint64_t* bytes);
+
+typedef struct mfsdp_head_logprob_args {
+    const void* params;       /* device, the owner's params buffer; 16-byte aligned */
+    const void* x;            /* device, n rows of cols elements, aligned to the element size */
+    int64_t n;                /* 0 .. 2^22; 0: nothing is done */
+    int64_t x_stride;         /* elements from one row of x to the next, >= cols; 0 = cols */
+    int32_t x_type;           /* mfsdp_dtype of x */
+    int32_t id_type;          /* mfsdp_id_type */
+    const void* ids;          /* NULL, or device, n of id_type, aligned to their size */
+    int64_t first_id;         /* id of the table's row 0, 0 .. 2^62 */
+    float scale;              /* finite */
+    int32_t top_k;            /* 0 .. 64; the lists below have as many entries a row */
+    mfsdp_head_record* records; /* device, n, written; 8-byte aligned */
+    float* logp;              /* NULL, or device fp32 [n] */
+    float* entropy;           /* NULL, or device fp32 [n] */
+    int64_t* top_ids;         /* device [n][top_k] (first_id + row; -1 where the table has no more rows); may be
+                                 NULL when top_k is 0 */
+    float* top_logp;          /* NULL, or device fp32 [n][top_k]: their log probabilities (-inf with id -1) */
+    float* top_logits;        /* NULL, or device fp32 [n][top_k]: their y, for mfsdp_head_total */
+    void* workspace;          /* device, mfsdp_plan_head_workspace_bytes, 256-byte aligned; written before it
+                                 is read, so it needs no clearing and may be shared by calls that do not
+                                 overlap */
+    uint64_t workspace_bytes;
+    void* stream;
+} mfsdp_head_logprob_args;
+
+/* Enqueue the log probabilities over entry `entry` of the plan (any role).
+ * An empty entry gives records without sum or target, log probabilities and
+ * entropies 0 and no alternatives.
+ * Errors: INVALID_ARGUMENT (null pointer, entry out of range, n, first_id,
+ * x_stride, scale or top_k out of range, misaligned buffer), UNSUPPORTED
+ * (id_type, x_type, more than 2^20 columns, more than 2^24 - 1 tiles of 128 x
+ * 128 logits), WORKSPACE_TOO_SMALL, HIP. */
+mfsdp_status mfsdp_head_logprob(mfsdp_plan_t plan, int64_t entry, const mfsdp_head_logprob_args* args);
+
+typedef struct mfsdp_head_total_args {
+    const mfsdp_head_record* parts; /* device, [count][n]; 8-byte aligned */
+    int64_t count;            /* 1 .. 65536 */
+    int64_t n;                /* 0 .. 2^22 */
+    mfsdp_head_record* records; /* device, [n], written; may be one of parts */
+    float* logp;              /* NULL, or device fp32 [n] */
+    float* entropy;           /* NULL, or device fp32 [n] */
+    const int64_t* part_top_ids;   /* device [count][n][top_k], of the parts' mfsdp_head_logprob */
+    const float* part_top_logits;  /* device [count][n][top_k], likewise */
+    int64_t* top_ids;         /* as in mfsdp_head_logprob_args */
+    float* top_logp;
+    float* top_logits;
+    int32_t top_k;            /* 0 .. 64; 0: the five arrays above are not used */
+    void* stream;
+} mfsdp_head_total_args;
+
+/* Join the records of several entries or owners in their order: the same
+ * bits wherever the same records are joined.  Parts are the tables in the
+ * order of their ids, for ties among alternatives; a target is in at most one
+ * of them.
+ * Errors: INVALID_ARGUMENT (null or misaligned pointer, count, n or top_k out
+ * of range), HIP. */
+mfsdp_status mfsdp_head_total(const mfsdp_head_total_args* args);
+
+typedef struct mfsdp_head_grad_args {
+    const void* params;       /* as in mfsdp_head_logprob_args, down to scale */
+    const void* x;
+    int64_t n;
+    int64_t x_stride;
+    int32_t x_type;
+    int32_t id_type;
+    const void* ids;
+    int64_t first_id;
+    float scale;
+    int32_t accumulate;       /* 0: the entry's gradient is written; 1: added to what is there */
+    const mfsdp_head_record* records; /* device, n: of mfsdp_head_logprob with the same arguments, or joined */
+    const float* dlogp;       /* device fp32 [n]: gradient of the log probabilities */
+    const float* dentropy;    /* NULL (zeros), or device fp32 [n]: gradient of the entropies */
+    void* dx;                 /* NULL, or device, n rows of cols elements of x_type: written, zeros for padding */
+    int64_t dx_stride;        /* elements from one row of dx to the next, >= cols; 0 = cols */
+    void* grads;              /* NULL, or device, the owner's grads buffer; 16-byte aligned */
+    void* workspace;          /* device, mfsdp_plan_head_workspace_bytes with grad = 1; as in
+                                 mfsdp_head_logprob_args */
+    uint64_t workspace_bytes;
+    void* stream;
+} mfsdp_head_grad_args;
+
+/* Enqueue the gradients of x and of the table:
+ *   dz_ij = scale * (dlogp_i ([j = t] - p_ij) - dentropy_i p_ij (ln p_ij + entropy_i)),
+ *   dx = dz W,  G (+)= dz^T x.
+ * Logits are formed again.  dz is rounded once, to bf16 where x and the table
+ * are bf16; the sums are fp32, rounded once to x_type and to the entry's type
+ * (after what was there is added).  No rows and accumulate = 0 writes zeros.
+ * Errors: as mfsdp_head_logprob, and INVALID_ARGUMENT (records or dlogp NULL
+ * or misaligned, accumulate or dx_stride out of range). */
+mfsdp_status mfsdp_head_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_head_grad_args* args);
+
 /* ---- Owner planner (host only) ----
  *
  * "MatrixFSDP" (arXiv 2607.05895), Abstract: a balance-aware owner planner

@@ -130,6 +130,41 @@ class MomentsArgs(ctypes.Structure):
                 ("type", ctypes.c_int32), ("stream", ctypes.c_void_p)]
 
 
+class HeadRecord(ctypes.Structure):
+    """mfsdp_head_record (24 bytes of device memory a row)."""
+    _fields_ = [("max", ctypes.c_float), ("sum", ctypes.c_float), ("wsum", ctypes.c_float), ("target", ctypes.c_float),
+                ("found", ctypes.c_int32), ("active", ctypes.c_int32)]
+
+
+HEAD_RECORD_BYTES = ctypes.sizeof(HeadRecord)
+
+
+class HeadLogprobArgs(ctypes.Structure):
+    _fields_ = [("params", ctypes.c_void_p), ("x", ctypes.c_void_p), ("n", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("x_type", ctypes.c_int32), ("id_type", ctypes.c_int32), ("ids", ctypes.c_void_p),
+                ("first_id", ctypes.c_int64), ("scale", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("records", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("top_ids", ctypes.c_void_p), ("top_logp", ctypes.c_void_p), ("top_logits", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p)]
+
+
+class HeadTotalArgs(ctypes.Structure):
+    _fields_ = [("parts", ctypes.c_void_p), ("count", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("records", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("part_top_ids", ctypes.c_void_p), ("part_top_logits", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+                ("top_logp", ctypes.c_void_p), ("top_logits", ctypes.c_void_p), ("top_k", ctypes.c_int32),
+                ("stream", ctypes.c_void_p)]
+
+
+class HeadGradArgs(ctypes.Structure):
+    _fields_ = [("params", ctypes.c_void_p), ("x", ctypes.c_void_p), ("n", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("x_type", ctypes.c_int32), ("id_type", ctypes.c_int32), ("ids", ctypes.c_void_p),
+                ("first_id", ctypes.c_int64), ("scale", ctypes.c_float), ("accumulate", ctypes.c_int32),
+                ("records", ctypes.c_void_p), ("dlogp", ctypes.c_void_p), ("dentropy", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_int64), ("grads", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p)]
+
+
 _PACK = {ctypes.c_void_p: "P", ctypes.c_uint64: "Q", ctypes.c_int64: "q", ctypes.c_uint32: "I", ctypes.c_int32: "i",
          ctypes.c_double: "d", ctypes.c_float: "f"}
 
@@ -146,7 +181,8 @@ def _packer(mirror):
 
 _pack_norm, _pack_clip = _packer(GradNormArgs), _packer(GradClipArgs)
 _pack_lookup, _pack_embed, _pack_step = _packer(EmbedLookupArgs), _packer(EmbedGradArgs), _packer(StepArgs)
-_pack_moments = _packer(MomentsArgs)
+_pack_moments, _pack_logprob = _packer(MomentsArgs), _packer(HeadLogprobArgs)
+_pack_total, _pack_head_grad = _packer(HeadTotalArgs), _packer(HeadGradArgs)
 
 EXPORTS = (
     "mfsdp_plan_create", "mfsdp_plan_state_bytes", "mfsdp_plan_workspace_bytes", "mfsdp_plan_ns_out_elems",
@@ -155,6 +191,7 @@ EXPORTS = (
     "mfsdp_plan_grad_workspace_bytes", "mfsdp_grad_norm", "mfsdp_grad_total", "mfsdp_grad_clip",
     "mfsdp_plan_embed_workspace_bytes", "mfsdp_embed_lookup", "mfsdp_embed_grad",
     "mfsdp_moments_read", "mfsdp_moments_write",
+    "mfsdp_plan_head_workspace_bytes", "mfsdp_head_logprob", "mfsdp_head_total", "mfsdp_head_grad",
     "mfsdp_owner_partition", "mfsdp_owner_gather", "mfsdp_owner_scatter", "mfsdp_status_string",
     "mfsdp_last_error_message", "mfsdp_probe_mfma_bf16", "mfsdp_probe_hbm",
 )
@@ -193,6 +230,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mfsdp_embed_grad.argtypes = [P, ctypes.c_int64, P]
     lib.mfsdp_moments_read.argtypes = [P, ctypes.c_int64, P]
     lib.mfsdp_moments_write.argtypes = [P, ctypes.c_int64, P]
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    lib.mfsdp_plan_head_workspace_bytes.argtypes = [P, i64, i64, i32, i32, i32, u64p]
+    lib.mfsdp_head_logprob.argtypes = [P, i64, P]
+    lib.mfsdp_head_total.argtypes = [P]
+    lib.mfsdp_head_grad.argtypes = [P, i64, P]
     lib.mfsdp_plan_destroy.argtypes = [P]
     lib.mfsdp_owner_partition.argtypes = [ctypes.POINTER(Tensor), ctypes.c_int64, ctypes.POINTER(PartitionParams),
                                           ctypes.POINTER(TensorPlace), ctypes.POINTER(ctypes.c_double), u64p, u64p]
@@ -407,6 +449,40 @@ class OwnerPlan:
         if status:
             _check(status)
 
+    def head_workspace_bytes(self, entry: int, n: int, x_type: int = BF16, top_k: int = 0, grad: bool = False) -> int:
+        v = ctypes.c_uint64()
+        _check(self._lib.mfsdp_plan_head_workspace_bytes(self._h, entry, n, x_type, top_k, 1 if grad else 0,
+                                                         ctypes.byref(v)))
+        return v.value
+
+    def head_logprob(self, entry: int, params: int, x: int, n: int, records: int, workspace: int, workspace_bytes: int,
+                     ids: int = 0, id_type: int = I64, x_type: int = BF16, x_stride: int = 0, first_id: int = 0,
+                     scale: float = 1.0, logp: int = 0, entropy: int = 0, top_k: int = 0, top_ids: int = 0,
+                     top_logp: int = 0, top_logits: int = 0, stream: int = 0) -> None:
+        """mfsdp_head_logprob: per row of x the record of its distribution
+        over the entry's rows, the log probability of its id, the entropy and
+        the top_k likeliest ids with their log probabilities."""
+        status = self._lib.mfsdp_head_logprob(
+            self._h, entry, _pack_logprob(params or 0, x or 0, n, x_stride, x_type, id_type, ids or 0, first_id, scale,
+                                          top_k, records or 0, logp or 0, entropy or 0, top_ids or 0, top_logp or 0,
+                                          top_logits or 0, workspace or 0, workspace_bytes, stream or 0))
+        if status:
+            _check(status)
+
+    def head_grad(self, entry: int, params: int, grads: int, x: int, n: int, records: int, dlogp: int, workspace: int,
+                  workspace_bytes: int, dentropy: int = 0, dx: int = 0, ids: int = 0, id_type: int = I64,
+                  x_type: int = BF16, x_stride: int = 0, dx_stride: int = 0, first_id: int = 0, scale: float = 1.0,
+                  accumulate: bool = False, stream: int = 0) -> None:
+        """mfsdp_head_grad: gradients of x (dx, 0 for none) and of the entry
+        (in grads, 0 for none) from those of the log probabilities and
+        entropies."""
+        status = self._lib.mfsdp_head_grad(
+            self._h, entry, _pack_head_grad(params or 0, x or 0, n, x_stride, x_type, id_type, ids or 0, first_id, scale,
+                                            1 if accumulate else 0, records or 0, dlogp or 0, dentropy or 0, dx or 0,
+                                            dx_stride, grads or 0, workspace or 0, workspace_bytes, stream or 0))
+        if status:
+            _check(status)
+
     def _ptrs(self, addrs):
         if addrs is None:
             return None
@@ -444,6 +520,16 @@ def grad_total(parts: int, count: int, stats: int, max_norm: float = float("inf"
     """mfsdp_grad_total: the norm and scale over `count` owners' GradStats
     (device array at parts), summed in order, into the GradStats at stats."""
     _check(load().mfsdp_grad_total(parts, count, max_norm, eps, stats, stream or None))
+
+
+def head_total(parts: int, count: int, n: int, records: int, logp: int = 0, entropy: int = 0, top_k: int = 0,
+               part_top_ids: int = 0, part_top_logits: int = 0, top_ids: int = 0, top_logp: int = 0,
+               top_logits: int = 0, stream: int = 0) -> None:
+    """mfsdp_head_total: join `count` tables' records of n rows (and their
+    alternatives) in order."""
+    _check(load().mfsdp_head_total(_pack_total(parts or 0, count, n, records or 0, logp or 0, entropy or 0,
+                                               part_top_ids or 0, part_top_logits or 0, top_ids or 0, top_logp or 0,
+                                               top_logits or 0, top_k, stream or 0)))
 
 
 @dataclass(frozen=True)

@@ -9,6 +9,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -16,7 +17,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libmfsdp.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["plan.cpp", "grad_plan.cpp", "owner_planner.cpp", "checkpoint.cpp", "step.hip", "elementwise.hip",
-           "adam8.hip", "grad.hip", "embed.hip", "ns_gemm.hip", "probe.hip"]
+           "adam8.hip", "grad.hip", "embed.hip", "head.hip", "ns_gemm.hip", "probe.hip"]
 ARCH = "gfx950"
 
 
@@ -40,8 +41,7 @@ def build(verbose: bool = False) -> str:
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall", "-Wno-unused-function",
     ]
-    objs = []
-    for src in SOURCES:
+    def compile_one(src: str) -> str:
         path = os.path.join(CSRC, src)
         obj = os.path.join(obj_dir, src + ".o")
         lang = ["-x", "c++"] if src.endswith(".cpp") else ["-x", "hip"]
@@ -52,7 +52,10 @@ def build(verbose: bool = False) -> str:
         if res.returncode != 0:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError(f"hipcc failed on {src}")
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(4) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     tmp = LIB_PATH + ".tmp"
     cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,1487 @@
+// head.hip - the output head over a table of the owner buffer: log
+// probabilities of given tokens under softmax(scale * x W^T), entropy, likely
+// alternatives, and the gradients of x and W.
+//
+// Logits are formed in fp32 by MFMA, from bf16 operands or the bf16 planes of
+// fp32 ones (tile_loop.h), and used in base 2, y = log2(e) scale x.W, which is
+// what the exponential instruction takes.  They are never stored
+// whole for the sums: the block that forms a tile of them reduces it, per
+// token and part of the vocabulary, to
+//
+//   M = max y,  S = sum 2^(y-M),  W = sum 2^(y-M) (y-M),
+//
+// and parts join by M = max(Ma, Mb), S = Sa 2^(Ma-M) + Sb 2^(Mb-M),
+// W = 2^(Ma-M) (Wa + (Ma-M) Sa) + the same of b.  Then
+//   logp = ln2 (y_t - M - log2 S),  entropy = ln2 (log2 S - W/S).
+// The k likeliest tokens of a row lie in the k parts with the largest M (ties
+// to the lower part): where they are asked for, logits go to the workspace too
+// and only those parts of them are read.
+//
+// Backward, with p = 2^(y-M)/S:
+//   dz_j = scale (dlogp ([j = t] - p_j) - dH p_j (ln p_j + H)),
+//   dx = dz W,  dW = dz^T x,
+// dz from the logits formed again, stored once, then two more products.  With
+// fp32 among the operands dz is three planes, else one, rounded to bf16: errors
+// of half a step that are independent from element to element and average out
+// in the sums over the vocabulary and the batch, but for a row's target, which
+// alone can outweigh the rest; what rounding takes from it is kept in fp32 and
+// added where dx and dW are written.
+#include <algorithm>
+#include <cmath>
+
+#include "kernels.h"
+#include "plan_internal.h"
+#include "tile_loop.h"
+
+namespace mfsdp {
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kMaxTop = 64;             // a list of alternatives is one lane an entry
+constexpr int kPackThreads = 256;
+constexpr int kPadTokens = 256;         // rows of the packed batch: a multiple of both tile edges
+constexpr int64_t kFewTokens = 64;      // batches up to this are read straight from x and the table
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- token ids ----
+
+struct Ids {
+    const void* ids;   // NULL: every row counts and none has a target
+    int64_t first;
+    int type;          // mfsdp_id_type
+};
+struct Token {
+    int target;        // row of the table, -1: not here
+    bool live;         // not padding (a negative id)
+};
+__device__ __forceinline__ Token token_of(const Ids& a, int64_t i, int rows) {
+    if (!a.ids) return Token{-1, true};
+    const int64_t id = a.type == MFSDP_I64 ? static_cast<const int64_t*>(a.ids)[i] : static_cast<const int32_t*>(a.ids)[i];
+    const int64_t t = id - a.first;
+    return Token{id >= 0 && t >= 0 && t < rows ? int(t) : -1, id >= 0};
+}
+
+// ---- packing ----
+
+struct PackArgs {
+    const uint8_t* src;
+    uint8_t* dst;
+    int64_t stride;     // elements of src from row to row
+    int64_t rows;       // of src
+    int64_t pitch;      // bytes of dst from row to row, a multiple of 128
+    int64_t plane;      // bytes of dst from plane to plane
+    int64_t words;      // 16-byte words of a plane of dst from the first on, over all its rows
+    int cols;
+    int vector;         // src rows are 16-byte aligned
+    Ids ids;            // rows with a negative id become zeros
+    int table_rows;
+    int* targets;       // NULL, or a row's target in the table, -1 without one ...
+    float* rest;        // ... and a zero
+};
+
+// An fp32 value as three bf16 ones that add up to it, each the nearest to what
+// the ones before it leave (the first towards zero where the nearest is not
+// finite).  A value that is not finite is the first alone.
+struct Planes {
+    uint16_t part[3];
+};
+__device__ __forceinline__ Planes planes_of(float v) {
+    Planes p;
+    p.part[0] = f32_to_bf16(v);
+    const bool fine = fabsf(v) < INFINITY;
+    if (fine && (p.part[0] & 0x7f80) == 0x7f80) p.part[0] = uint16_t(__float_as_uint(v) >> 16);
+    const float r = fine ? v - bf16_to_f32(p.part[0]) : 0.f;
+    p.part[1] = f32_to_bf16(r);
+    p.part[2] = f32_to_bf16(r - bf16_to_f32(p.part[1]));
+    return p;
+}
+
+// Rows of a matrix in the layout the tile loop takes, one plane of a bf16
+// matrix or three of an fp32 one: zeros behind each row's end, for rows past
+// the last and for padding tokens.
+template <int D>
+__global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a) {
+    const int64_t w = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
+    if (w >= a.words) return;
+    const int per_row = int(a.pitch / 16);
+    const int64_t row = w / per_row;
+    const int c = int(w % per_row) * 8;
+    const Token t = row < a.rows ? token_of(a.ids, row, a.table_rows) : Token{-1, false};
+    if (a.targets && c == 0) {
+        a.targets[row] = t.target;
+        a.rest[row] = 0.f;
+    }
+    const bool in = t.live && c < a.cols;
+    const uint8_t* src = a.src + row * a.stride * (D == kBF16 ? 2 : 4);
+    uint8_t* dst = a.dst + w * 16;
+    if constexpr (D == kBF16) {
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (in && a.vector && c + 8 <= a.cols) {
+            v = *reinterpret_cast<const u32x4_t*>(src + c * 2);
+        } else if (in) {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < a.cols) v[k >> 1] |= uint32_t(e[c + k]) << (16 * (k & 1));
+        }
+        *reinterpret_cast<u32x4_t*>(dst) = v;
+    } else {
+        float v[8] = {};
+        if (in && a.vector && c + 8 <= a.cols) {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + c * 4);
+            const f32x4_t y = *reinterpret_cast<const f32x4_t*>(src + c * 4 + 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[k] = x[k];
+                v[4 + k] = y[k];
+            }
+        } else if (in) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < a.cols) v[k] = reinterpret_cast<const float*>(src)[c + k];
+        }
+        u32x4_t o[3] = {};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const Planes p = planes_of(v[k]);
+#pragma unroll
+            for (int j = 0; j < 3; ++j) o[j][k >> 1] |= uint32_t(p.part[j]) << (16 * (k & 1));
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j) *reinterpret_cast<u32x4_t*>(dst + j * a.plane) = o[j];
+    }
+}
+
+// ---- tiles ----
+
+// Tile (ti, tj) of a block: tiles run in strips 8 wide along the dimension
+// with fewer of them, and blocks of one XCD (block index mod 8) take 32
+// consecutive ones, 4 x 8 where the strip is 8 wide, whose operands share its
+// L2.  What is left over a multiple of 256 blocks keeps the plain order.
+__device__ __forceinline__ void tile_of(int b, int total, int tp, int tq, int& ti, int& tj) {
+    int at = b;
+    if (b < total / 256 * 256) at = (b / 256 * 8 + (b & 7)) * 32 + ((b & 255) >> 3);
+    const int few = min(tp, tq), many = max(tp, tq);
+    const int strip = at / (8 * many), in = at - strip * 8 * many;
+    const int width = min(8, few - 8 * strip);
+    const int across = 8 * strip + in % width, along = in / width;
+    ti = tp <= tq ? across : along;
+    tj = tp <= tq ? along : across;
+}
+
+struct LogitArgs {
+    Operand table, x;
+    int rows;            // of the table
+    int64_t n;
+    int stages;          // of the contraction
+    int tp, tq;          // tiles along the vocabulary and the batch
+    float c2;            // scale * log2(e)
+    Ids ids;
+    float4* parts;       // [part][n]: M, S, W of a token over BT/2 rows of the table
+    float* targets;      // [n]: y of the target, written where it is here
+    float* logits;       // NULL, or [n][ldl]: y
+    int64_t ldl;
+};
+
+// f(MFMA row tile, accumulator, row) for the rows of a wave's block that a
+// lane holds of one column.
+template <int MM, typename F>
+__device__ __forceinline__ void each_row(int fhalf, F&& f) {
+#pragma unroll
+    for (int mi = 0; mi < MM; ++mi)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f(mi, q * 4 + e, mi * 32 + q * 8 + fhalf * 4 + e);
+}
+
+// One column of a wave's logits, MM x 32 rows of the table from row0 on of
+// which the lane and lane ^ 32 hold half each, `held` of them in the table:
+// their sums (in both lanes), the target and, where asked for, the logits
+// themselves.  RAGGED: held may be less than MM * 32.
+template <int MM, bool RAGGED, typename A>
+__device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_t token, int row0, int held, int64_t part,
+                                              int fhalf) {
+    const bool in = token < a.n;
+    float most = -INFINITY, sum[2] = {0.f, 0.f}, wsum[2] = {0.f, 0.f};
+    each_row<MM>(fhalf, [&](int mi, int e, int r) {
+        acc[mi][e] *= a.c2;
+        if (!RAGGED || r < held) most = fmaxf(most, acc[mi][e]);
+    });
+    most = fmaxf(most, __shfl_xor(most, 32, 64));
+    each_row<MM>(fhalf, [&](int mi, int e, int r) {
+        const float d = acc[mi][e] - most, p = exp2_fast(d);
+        if (!RAGGED || r < held) {
+            sum[e & 1] += p;
+            wsum[e & 1] = __builtin_fmaf(p, d, wsum[e & 1]);
+        }
+    });
+    float s = sum[0] + sum[1], w = wsum[0] + wsum[1];
+    s += __shfl_xor(s, 32, 64);
+    w += __shfl_xor(w, 32, 64);
+    if (in && fhalf == 0) a.parts[part * a.n + token] = make_float4(most, s, w, 0.f);
+    if (a.ids.ids) {
+        const int t = in ? token_of(a.ids, token, a.rows).target - row0 : -1;
+        if (__ballot(t >= 0 && t < MM * 32))
+            each_row<MM>(fhalf, [&](int mi, int e, int r) {
+                if (r == t) a.targets[token] = acc[mi][e];
+            });
+    }
+    if (a.logits && in) {
+        float* to = a.logits + token * a.ldl + row0;
+#pragma unroll
+        for (int mi = 0; mi < MM; ++mi)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = mi * 32 + q * 8 + fhalf * 4;
+                if (!RAGGED || r < held)  // up to three values past the table's end, inside ldl
+                    *reinterpret_cast<float4*>(to + r) =
+                        make_float4(acc[mi][q * 4], acc[mi][q * 4 + 1], acc[mi][q * 4 + 2], acc[mi][q * 4 + 3]);
+            }
+    }
+}
+
+// Column ni of the accumulators, as reduce_column indexes it.
+template <int MM, int MN> struct Column {
+    f32x16_t (&acc)[MM][MN];
+    int ni;
+    __device__ __forceinline__ f32x16_t& operator[](int mi) { return acc[mi][ni]; }
+};
+
+// A tile of logits, BT rows of the table by BT tokens, reduced over each
+// wave's BT/2 rows.
+template <int BT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_logits(LogitArgs a) {
+    using S = Shape<BT, 4>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
+    int ti, tj;
+    tile_of(int(blockIdx.x), a.tp * a.tq, a.tp, a.tq, ti, tj);
+    f32x16_t acc[S::MM][S::MN];
+    tile_loop<false, false, BT>(acc, a.table, a.x, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
+
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    const int wm = wave >> 1, wn = wave & 1, frow = lane & 31, fhalf = lane >> 5;
+    const int row0 = ti * BT + wm * S::WTM, held = a.rows - row0;
+    const int64_t part = int64_t(ti) * 2 + wm;
+#pragma unroll
+    for (int ni = 0; ni < S::MN; ++ni) {
+        const int64_t token = int64_t(tj) * BT + wn * S::WTN + ni * 32 + frow;
+        Column<S::MM, S::MN> col{acc, ni};
+        if (held >= S::WTM)
+            reduce_column<S::MM, false>(a, col, token, row0, held, part, fhalf);
+        else
+            reduce_column<S::MM, true>(a, col, token, row0, held, part, fhalf);
+    }
+}
+
+// ---- few tokens: the table read once, straight into MFMA fragments ----
+
+struct FewArgs {
+    LogitArgs l;         // without operands
+    const uint8_t* table;
+    const uint8_t* x;
+    int64_t x_pitch;     // bytes
+    int64_t pitch;       // bytes of a row of the table
+    int cols;
+};
+
+// Eight consecutive elements of a row as they lie (unaligned words), zeros
+// past the last column.
+template <int D> struct Eight;
+template <> struct Eight<kBF16> {
+    u32x4_t v;
+    __device__ __forceinline__ void load(const uint8_t* row, int k, int cols) {
+        typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(2)));
+        if (k + 8 <= cols) {
+            v = *reinterpret_cast<const word_t*>(row + 2 * k);
+        } else {
+            v = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < cols) v[e >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[k + e]) << (16 * (e & 1));
+        }
+    }
+    // four of them (half 0 or 1) as fp32
+    __device__ __forceinline__ u32x4_t wide(int half) const {
+        const uint32_t a = v[2 * half], b = v[2 * half + 1];
+        return u32x4_t{a << 16, a & 0xffff0000u, b << 16, b & 0xffff0000u};
+    }
+};
+template <> struct Eight<kF32> {
+    u32x4_t v[2];
+    __device__ __forceinline__ void load(const uint8_t* row, int k, int cols) {
+        typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(4)));
+        if (k + 8 <= cols) {
+            v[0] = *reinterpret_cast<const word_t*>(row + 4 * k);
+            v[1] = *reinterpret_cast<const word_t*>(row + 4 * k + 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = k + e < cols ? reinterpret_cast<const uint32_t*>(row)[k + e] : 0u;
+        }
+    }
+    __device__ __forceinline__ u32x4_t wide(int half) const { return v[half]; }
+};
+
+// 32 rows of the table by NB * 32 tokens a block.  Its four waves share the
+// contraction, 64 elements in turn; a lane holds half of those of one row, so
+// that a row is read in whole lines, and the contraction's order inside a line
+// is the same permutation for both operands.  Every column of the product is
+// one token's alone, so that what padding or a row past the last holds goes
+// nowhere.
+template <int WD, int XD, int NB>
+__global__ __launch_bounds__(256) void k_head_few(FewArgs f) {
+    const LogitArgs& a = f.l;
+    __shared__ float sums[4][NB * 16][64];
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    const int frow = lane & 31, fhalf = lane >> 5;
+    const int row0 = int(blockIdx.x) * 32;
+    const uint8_t* w = f.table + int64_t(min(row0 + frow, a.rows - 1)) * f.pitch;
+    const uint8_t* x[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x[b] = f.x + min(int64_t(b * 32 + frow), a.n - 1) * f.x_pitch;
+    f32x16_t acc[NB] = {};
+    const int lines = (f.cols + 63) / 64;
+    auto body = [&](int line, auto COUNT) {
+        constexpr int L = decltype(COUNT)::value;
+        Eight<WD> ew[L][4];
+        Eight<XD> ex[L][NB][4];
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int k = (line + 4 * l) * 64 + fhalf * 32 + g * 8;
+                ew[l][g].load(w, k, f.cols);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) ex[l][b][g].load(x[b], k, f.cols);
+            }
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    if constexpr (WD == kBF16 && XD == kBF16) {
+                        Mfma<uint16_t>::step(acc[b], ew[l][g].v, ex[l][b][g].v);
+                    } else {
+                        Mfma<float>::step(acc[b], ew[l][g].wide(0), ex[l][b][g].wide(0));
+                        Mfma<float>::step(acc[b], ew[l][g].wide(1), ex[l][b][g].wide(1));
+                    }
+                }
+    };
+    // lines of whole elements in batches, the rest one by one
+    const int whole = f.cols / 64;
+    constexpr int BATCH = WD == kBF16 && XD == kBF16 ? (NB == 1 ? 4 : 2) : (NB == 1 ? 2 : 1);
+    int line = wave;
+    for (; line + 4 * (BATCH - 1) < whole; line += 4 * BATCH) body(line, std::integral_constant<int, BATCH>{});
+    for (; line < lines; line += 4) body(line, std::integral_constant<int, 1>{});
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sums[wave][b * 16 + e][lane] = acc[b][e];
+    __syncthreads();
+    const int held = a.rows - row0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (b % 4 != wave) continue;
+        f32x16_t col[1];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            col[0][e] = (sums[0][b * 16 + e][lane] + sums[1][b * 16 + e][lane]) +
+                        (sums[2][b * 16 + e][lane] + sums[3][b * 16 + e][lane]);
+        reduce_column<1, true>(a, col, b * 32 + frow, row0, held, blockIdx.x, fhalf);
+    }
+}
+
+// ---- rows: parts joined, alternatives ----
+
+struct Sums {
+    float m, s, w;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+    if (b.s == 0.f) return a;  // no part: NaN sums are not equal to 0
+    if (a.s == 0.f) return b;
+    const float m = fmaxf(a.m, b.m), da = a.m - m, db = b.m - m;
+    const float fa = exp2_fast(da), fb = exp2_fast(db);
+    return Sums{m, __builtin_fmaf(a.s, fa, b.s * fb),
+                __builtin_fmaf(fa, __builtin_fmaf(da, a.s, a.w), fb * __builtin_fmaf(db, b.s, b.w))};
+}
+__device__ __forceinline__ Sums shuffled(const Sums& a, int off) {
+    return Sums{__shfl_xor(a.m, off, 64), __shfl_xor(a.s, off, 64), __shfl_xor(a.w, off, 64)};
+}
+
+// A wave's list of the k largest values, largest first, ties to the lower
+// index: lane i holds entry i.  An empty entry is (-inf, INT_MAX).
+struct TopList {
+    float v;
+    int id;
+    int k, lane;
+    __device__ __forceinline__ TopList(int k_, int lane_) : v(-INFINITY), id(INT32_MAX), k(k_), lane(lane_) {}
+    static __device__ __forceinline__ bool before(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+    // every lane offers one value (or none); NaN is never before anything
+    __device__ __forceinline__ void offer(float x, int ix, bool valid) {
+        float last = __shfl(v, k - 1, 64);
+        int ilast = __shfl(id, k - 1, 64);
+        uint64_t mask = __ballot(valid && before(x, ix, last, ilast));
+        while (mask) {
+            const int src = __ffsll(static_cast<unsigned long long>(mask)) - 1;
+            mask &= mask - 1;
+            const float c = __shfl(x, src, 64);
+            const int ic = __shfl(ix, src, 64);
+            if (!before(c, ic, last, ilast)) continue;  // the list has grown since (the same in every lane)
+            const int pos = __popcll(__ballot(before(v, id, c, ic)));
+            const float pv = __shfl_up(v, 1, 64);
+            const int pi = __shfl_up(id, 1, 64);
+            if (lane > pos) {
+                v = pv;
+                id = pi;
+            } else if (lane == pos) {
+                v = c;
+                id = ic;
+            }
+            last = __shfl(v, k - 1, 64);
+            ilast = __shfl(id, k - 1, 64);
+        }
+    }
+};
+
+struct RowArgs {
+    const float4* parts;
+    const float* targets;
+    const float* logits;
+    int64_t ldl;
+    int64_t n;
+    int n_parts, part_rows, rows;
+    Ids ids;
+    int64_t first_id;    // id of the table's row 0
+    mfsdp_head_record* records;
+    float *logp, *entropy;
+    int top_k;
+    int64_t* top_ids;
+    float *top_logp, *top_logits;
+};
+
+__device__ __forceinline__ float nat(float y2) { return y2 * kLn2; }
+
+// One token a group of WAVES waves.  Lanes join the parts they stride over in
+// order, then lanes by a butterfly, then waves in order: the same order for
+// the same sizes.
+template <int WAVES>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_head_rows(RowArgs a) {
+    constexpr int TOKENS = WAVES == 1 ? 4 : 1;
+    __shared__ Sums sums[WAVES];
+    __shared__ float best_v[WAVES == 1 ? 1 : WAVES * kMaxTop];
+    __shared__ int best_id[WAVES == 1 ? 1 : WAVES * kMaxTop];
+    const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
+    const int64_t token = int64_t(blockIdx.x) * TOKENS + (WAVES == 1 ? wave : 0);
+    if (token >= a.n) return;  // whole waves; with WAVES > 1 never
+    const int first = WAVES == 1 ? lane : int(threadIdx.x), stride = 64 * WAVES;
+    const Token t = token_of(a.ids, token, a.rows);
+    Sums mine = {-INFINITY, 0.f, 0.f};
+    TopList parts(a.top_k ? a.top_k : 1, lane);
+    const int turns = (a.n_parts + stride - 1) / stride;
+    for (int u = 0; u < turns; ++u) {
+        const int p = u * stride + first;
+        float4 v = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        if (p < a.n_parts) v = a.parts[int64_t(p) * a.n + token];
+        mine = join(mine, Sums{v.x, v.y, v.z});
+        if (a.top_k) parts.offer(v.x, p, p < a.n_parts);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const Sums other = shuffled(mine, off);
+        mine = (lane & off) ? join(other, mine) : join(mine, other);
+    }
+    if constexpr (WAVES > 1) {
+        if (lane == 0) sums[wave] = mine;
+        if (a.top_k) {
+            best_v[wave * kMaxTop + lane] = parts.v;
+            best_id[wave * kMaxTop + lane] = parts.id;
+        }
+        __syncthreads();
+        if (wave > 0) return;
+        mine = sums[0];
+        for (int k = 1; k < WAVES; ++k) {
+            mine = join(mine, sums[k]);
+            if (a.top_k) parts.offer(best_v[k * kMaxTop + lane], best_id[k * kMaxTop + lane], lane < a.top_k);
+        }
+    }
+    const float y = t.target >= 0 && a.rows > 0 ? a.targets[token] : 0.f;
+    const float ls = mine.s == 0.f ? 0.f : log2f(mine.s);
+    if (lane == 0) {
+        mfsdp_head_record r;
+        r.max = t.live ? mine.m : 0.f;
+        r.sum = t.live ? mine.s : 0.f;
+        r.wsum = t.live ? mine.w : 0.f;
+        r.target = y;
+        r.found = t.target >= 0;
+        r.active = t.live;
+        a.records[token] = r;
+        if (a.logp) a.logp[token] = t.target >= 0 ? nat((y - mine.m) - ls) : 0.f;
+        if (a.entropy) a.entropy[token] = t.live && mine.s != 0.f ? nat(ls - mine.w / mine.s) : 0.f;
+    }
+    if (!a.top_k) return;
+    TopList top(a.top_k, lane);
+    if (t.live)
+        for (int k = 0; k < a.top_k; ++k) {
+            const int p = __shfl(parts.id, k, 64);
+            if (p == INT32_MAX) break;  // fewer parts than that
+            for (int r0 = 0; r0 < a.part_rows; r0 += 64) {
+                const int64_t row = int64_t(p) * a.part_rows + r0 + lane;
+                const bool in = r0 + lane < a.part_rows && row < a.rows;
+                top.offer(in ? a.logits[token * a.ldl + row] : 0.f, int(row), in);
+            }
+        }
+    if (lane < a.top_k) {
+        const int64_t at = token * a.top_k + lane;
+        const bool some = top.id != INT32_MAX;
+        a.top_ids[at] = some ? a.first_id + top.id : -1;
+        if (a.top_logits) a.top_logits[at] = top.v;
+        if (a.top_logp) a.top_logp[at] = some ? nat((top.v - mine.m) - ls) : -INFINITY;
+    }
+}
+
+struct TotalArgs {
+    const mfsdp_head_record* parts;
+    int count;
+    int64_t n;
+    mfsdp_head_record* records;
+    float *logp, *entropy;
+    int top_k;
+    const int64_t* part_ids;
+    const float* part_logits;
+    int64_t* top_ids;
+    float *top_logp, *top_logits;
+};
+
+// Records of several tables joined in their order, a wave a token.
+// Alternatives: an entry's place in the parts' lists stands for its id, so
+// that equal logits keep the parts' order.
+__global__ __launch_bounds__(256) void k_head_total(TotalArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t token = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (token >= a.n) return;
+    Sums all = {-INFINITY, 0.f, 0.f};
+    float target = 0.f;
+    int found = 0, active = 0;
+    for (int c = 0; c < a.count; ++c) {
+        const mfsdp_head_record r = a.parts[c * a.n + token];
+        all = join(all, Sums{r.max, r.sum, r.wsum});
+        if (r.found) target = r.target;
+        found |= r.found;
+        active |= r.active;
+    }
+    const float ls = all.s == 0.f ? 0.f : log2f(all.s);
+    TopList top(a.top_k ? a.top_k : 1, lane);
+    for (int c = 0; a.top_k && c < a.count; ++c) {
+        const int64_t at = (c * a.n + token) * a.top_k + lane;
+        const bool in = lane < a.top_k && a.part_ids[at] >= 0;
+        top.offer(in ? a.part_logits[at] : 0.f, c * a.top_k + lane, in);
+    }
+    // every record of the token has been read before one is written
+    if (lane == 0) {
+        a.records[token] = mfsdp_head_record{active ? all.m : 0.f, all.s, all.w, target, found, active};
+        if (a.logp) a.logp[token] = found ? nat((target - all.m) - ls) : 0.f;
+        if (a.entropy) a.entropy[token] = active && all.s != 0.f ? nat(ls - all.w / all.s) : 0.f;
+    }
+    if (lane < a.top_k) {
+        const int64_t at = token * a.top_k + lane;
+        const bool some = top.id != INT32_MAX;
+        const int64_t from = some ? (int64_t(top.id / a.top_k) * a.n + token) * a.top_k + top.id % a.top_k : 0;
+        a.top_ids[at] = some ? a.part_ids[from] : -1;
+        if (a.top_logits) a.top_logits[at] = top.v;
+        if (a.top_logp) a.top_logp[at] = some ? nat((top.v - all.m) - ls) : -INFINITY;
+    }
+}
+
+// Records of an empty table: nothing in the sums, no target.
+__global__ __launch_bounds__(256) void k_head_empty(RowArgs a) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= a.n) return;
+    const bool live = token_of(a.ids, i, 0).live;
+    a.records[i] = mfsdp_head_record{live ? -INFINITY : 0.f, 0.f, 0.f, 0.f, 0, live};
+    if (a.logp) a.logp[i] = 0.f;
+    if (a.entropy) a.entropy[i] = 0.f;
+    for (int k = 0; k < a.top_k; ++k) {
+        a.top_ids[i * a.top_k + k] = -1;
+        if (a.top_logits) a.top_logits[i * a.top_k + k] = -INFINITY;
+        if (a.top_logp) a.top_logp[i * a.top_k + k] = -INFINITY;
+    }
+}
+
+// ---- backward ----
+
+struct DzArgs {
+    LogitArgs l;
+    const mfsdp_head_record* records;
+    const float *dlogp, *dentropy;
+    float scale;
+    uint8_t* dz;       // [plane][tokens, whole tiles][rows, whole tiles] bf16
+    int64_t pitch;     // bytes from token to token
+    int planes;
+    int64_t plane;
+    float* rest;       // [n]: what rounding took from the target's dz (one plane)
+};
+
+// dz of a tile: formed in the accumulators, staged in LDS as [token][row of
+// the table] in bf16, a plane at a time, and written in whole 16-byte words.
+// Zeros for tokens and rows past the last, and for padding.
+template <int BT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
+    using S = Shape<BT, 4>;
+    const LogitArgs& a = d.l;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
+    int ti, tj;
+    tile_of(int(blockIdx.x), a.tp * a.tq, a.tp, a.tq, ti, tj);
+    f32x16_t acc[S::MM][S::MN];
+    tile_loop<false, false, BT>(acc, a.table, a.x, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
+
+    constexpr int RB = BT * 2, GPR = RB / 16;  // bytes and 16-byte words of a staged row
+    static_assert(BT * RB <= Pipe<BT, 4>::BYTES, "staging area");
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    const int wm = wave >> 1, wn = wave & 1, frow = lane & 31, fhalf = lane >> 5;
+    const int row0 = ti * BT + wm * S::WTM, held = a.rows - row0;
+#pragma unroll
+    for (int ni = 0; ni < S::MN; ++ni) {
+        const int64_t token = int64_t(tj) * BT + wn * S::WTN + ni * 32 + frow;
+        float m = 0.f, ls = 0.f, b = 0.f, c = 0.f, hit = 0.f;
+        int t = -1;
+        bool live = false;
+        if (token < a.n) {
+            const Token tok = token_of(a.ids, token, a.rows);
+            const mfsdp_head_record r = d.records[token];
+            live = tok.live && r.active;
+            const float up = r.found ? d.dlogp[token] : 0.f, dh = d.dentropy ? d.dentropy[token] : 0.f;
+            m = r.max;
+            ls = log2f(r.sum);
+            // dz = hit - p (b + c lp), lp = log2 p
+            b = d.scale * __builtin_fmaf(dh, nat(ls - r.wsum / r.sum), up);
+            c = d.scale * dh * kLn2;
+            if (tok.target >= 0 && r.found && live) {
+                t = tok.target - row0;
+                hit = d.scale * up;
+            }
+        }
+        each_row<S::MM>(fhalf, [&](int mi, int e, int) {
+            const float lp = (acc[mi][ni][e] * a.c2 - m) - ls;
+            const float v = -exp2_fast(lp) * __builtin_fmaf(c, lp, b);
+            acc[mi][ni][e] = live ? v : 0.f;
+        });
+        if (held < S::WTM)
+            each_row<S::MM>(fhalf, [&](int mi, int e, int r) {
+                if (r >= held) acc[mi][ni][e] = 0.f;
+            });
+        if (__ballot(t >= 0 && t < S::WTM))
+            each_row<S::MM>(fhalf, [&](int mi, int e, int r) {
+                if (r == t) {
+                    const float v = acc[mi][ni][e] + hit;
+                    acc[mi][ni][e] = v;
+                    if (d.planes == 1) d.rest[token] = fabsf(v) < INFINITY ? v - bf16_to_f32(f32_to_bf16(v)) : 0.f;
+                }
+            });
+    }
+    for (int plane = 0; plane < d.planes; ++plane) {
+        __syncthreads();  // the operands' stages, or the plane before, have been read
+#pragma unroll
+        for (int ni = 0; ni < S::MN; ++ni) {
+            const int cl = wn * S::WTN + ni * 32 + frow;
+#pragma unroll
+            for (int mi = 0; mi < S::MM; ++mi)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int rl = wm * S::WTM + mi * 32 + q * 8 + fhalf * 4;
+                    const uint2 w = make_uint2(pack_bf16x2(acc[mi][ni][q * 4], acc[mi][ni][q * 4 + 1]),
+                                               pack_bf16x2(acc[mi][ni][q * 4 + 2], acc[mi][ni][q * 4 + 3]));
+                    if (d.planes > 1) {
+                        acc[mi][ni][q * 4] -= __uint_as_float(w.x << 16);
+                        acc[mi][ni][q * 4 + 1] -= __uint_as_float(w.x & 0xffff0000u);
+                        acc[mi][ni][q * 4 + 2] -= __uint_as_float(w.y << 16);
+                        acc[mi][ni][q * 4 + 3] -= __uint_as_float(w.y & 0xffff0000u);
+                    }
+                    *reinterpret_cast<uint2*>(lds + cl * RB + ((rl >> 3) ^ (cl & (GPR - 1))) * 16 + ((rl >> 2) & 1) * 8) = w;
+                }
+        }
+        __syncthreads();
+        uint8_t* to = d.dz + plane * d.plane + int64_t(tj) * BT * d.pitch + int64_t(ti) * RB;
+#pragma unroll 8
+        for (int i = 0; i < BT * GPR / 256; ++i) {
+            const int k = int(threadIdx.x) + i * 256, r = k / GPR, j = k % GPR;
+            *reinterpret_cast<u32x4_t*>(to + r * d.pitch + j * 16) =
+                *reinterpret_cast<const u32x4_t*>(lds + r * RB + (j ^ (r & (GPR - 1))) * 16);
+        }
+    }
+}
+
+// A tile of fp32 accumulators, handed on in the order of its columns: through
+// LDS in passes of BT*BT*4 / 128 KB, where row c of the staging area is tile
+// column c of the pass, its 16-byte words j at j ^ (c % 32).  fix(pass,
+// staging area) may change it (the block is in step before and after), then
+// before(c, r) and out(c, r, what before gave, four values) see the values of
+// tile rows r .. r+3 of tile column c, `before` some words ahead.
+template <int BT> struct Staging {
+    static constexpr int PASSES = BT == 256 ? 2 : 1, COLS = BT / PASSES, BYTES = COLS * BT * 4;
+    static_assert(BYTES <= Pipe<BT, 4>::BYTES, "staging area");
+    float* at;
+    __device__ __forceinline__ float4& word(int c, int j) const {  // c in the pass
+        return *reinterpret_cast<float4*>(at + c * BT + ((j ^ (c & 31)) * 4));
+    }
+};
+template <int BT, typename FIX, typename BEFORE, typename OUT>
+__device__ __forceinline__ void walk_columns(const f32x16_t (&acc)[BT / 64][BT / 64], uint8_t* lds, FIX&& fix,
+                                             BEFORE&& before, OUT&& out) {
+    using S = Shape<BT, 4>;
+    using G = Staging<BT>;
+    constexpr int NCH = BT / 4, TURNS = G::COLS * NCH / 256, AHEAD = 8;
+    static_assert(TURNS % AHEAD == 0, "walk");
+    const G st = {reinterpret_cast<float*>(lds)};
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    const int wm = wave >> 1, wn = wave & 1, frow = lane & 31, fhalf = lane >> 5;
+    __syncthreads();  // every wave is done with the operands' stages
+#pragma unroll
+    for (int h = 0; h < G::PASSES; ++h) {
+        if (G::PASSES == 1 || wn == h) {
+#pragma unroll
+            for (int mi = 0; mi < S::MM; ++mi)
+#pragma unroll
+                for (int ni = 0; ni < S::MN; ++ni)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int rl = wm * S::WTM + mi * 32 + q * 8 + fhalf * 4;
+                        const int cl = wn * S::WTN + ni * 32 + frow - h * G::COLS;
+                        const f32x16_t& v = acc[mi][ni];
+                        st.word(cl, rl >> 2) = make_float4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
+                    }
+        }
+        __syncthreads();
+        fix(h, st);
+        for (int i0 = 0; i0 < TURNS; i0 += AHEAD) {
+            decltype(before(0, 0)) early[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int k = int(threadIdx.x) + (i0 + i) * 256;
+                early[i] = before(h * G::COLS + k / NCH, k % NCH * 4);
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int k = int(threadIdx.x) + (i0 + i) * 256;
+                out(h * G::COLS + k / NCH, k % NCH * 4, early[i], st.word(k / NCH, k % NCH));
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Four consecutive elements of a row from column c on, n of them inside; as
+// one vector where `vector` says that rows are aligned for it.
+template <int D> __device__ __forceinline__ float4 get4(const uint8_t* row, int c, int n, bool vector) {
+    if (n >= 4 && vector) {
+        if constexpr (D == kBF16) {
+            const uint2 r = *reinterpret_cast<const uint2*>(row + c * 2);
+            return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                               __uint_as_float(r.y & 0xffff0000u));
+        } else {
+            return *reinterpret_cast<const float4*>(row + c * 4);
+        }
+    }
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k < n) v[k] = load_elem(row, D, c + k);
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+template <int D> __device__ __forceinline__ void put4(uint8_t* row, int c, int n, bool vector, const float4& v) {
+    if (n >= 4 && vector) {
+        if constexpr (D == kBF16)
+            *reinterpret_cast<uint2*>(row + c * 2) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        else
+            *reinterpret_cast<float4*>(row + c * 4) = v;
+    } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < n) store_elem(row, D, c + k, e[k]);
+    }
+}
+__device__ __forceinline__ float4 fma4(float f, const float4& a, const float4& b) {
+    return make_float4(__builtin_fmaf(f, a.x, b.x), __builtin_fmaf(f, a.y, b.y), __builtin_fmaf(f, a.z, b.z),
+                       __builtin_fmaf(f, a.w, b.w));
+}
+
+struct DxArgs {
+    Operand table, dz;
+    int64_t n;
+    int cols, rows;
+    int tp, tq;           // tiles along the columns and the batch
+    int stages, splits;   // of the contraction over the vocabulary, and the parts it is cut into
+    Ids ids;
+    const int* targets;
+    const float* rest;    // NULL, or the rests of the targets' dz (the table then has one plane)
+    uint8_t* dx;
+    int64_t stride;
+    int vector;
+    float* sums;          // splits > 1: [split][n][ld]
+    int64_t ld;
+};
+
+// dx = dz W: P is W, read K-major (its rows are the contraction).
+template <int D, int BT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
+    using S = Shape<BT, 4>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
+    const int tiles = a.tp * a.tq, split = int(blockIdx.x) / tiles;
+    int ti, tj;
+    tile_of(int(blockIdx.x) - split * tiles, tiles, a.tp, a.tq, ti, tj);
+    const int k0 = int(int64_t(a.stages) * split / a.splits), k1 = int(int64_t(a.stages) * (split + 1) / a.splits);
+    f32x16_t acc[S::MM][S::MN];
+    tile_loop<true, false, BT>(acc, a.table, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, k0, k1, lds);
+    struct Extra {
+        float rest;
+        float4 w;
+    };
+    walk_columns<BT>(
+        acc, lds, [](int, const Staging<BT>&) {},
+        [&](int c, int r) {
+            const int64_t token = int64_t(tj) * BT + c;
+            const int col = ti * BT + r;
+            Extra x = {0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            if (a.rest && split == 0 && token < a.n && col < a.cols) {
+                x.rest = a.rest[token];
+                const int t = a.targets[token];  // columns past the last are inside the row's pitch
+                if (t >= 0) x.w = get4<kBF16>(a.table.base + t * a.table.pitch, col, 4, true);
+            }
+            return x;
+        },
+        [&](int c, int r, const Extra& x, float4 v) {
+            const int64_t token = int64_t(tj) * BT + c;
+            const int col = ti * BT + r;
+            if (token >= a.n || col >= a.cols) return;
+            if (x.rest != 0.f) v = fma4(x.rest, x.w, v);
+            if (a.splits > 1) {
+                *reinterpret_cast<float4*>(a.sums + (split * a.n + token) * a.ld + col) = v;  // ld is a multiple of 4
+            } else {
+                if (!token_of(a.ids, token, a.rows).live) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                put4<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
+            }
+        });
+}
+
+// The parts of dx added in their order.
+template <int D>
+__global__ __launch_bounds__(256) void k_head_dx_sum(DxArgs a) {
+    const int64_t w = int64_t(blockIdx.x) * 256 + threadIdx.x, per = a.ld / 4;
+    const int64_t token = w / per;
+    const int col = int(w % per) * 4;
+    if (token >= a.n || col >= a.cols) return;
+    f32x4_t v = {};
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(a.sums + (s * a.n + token) * a.ld + col);
+    if (!token_of(a.ids, token, a.rows).live) v = f32x4_t{};
+    put4<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, make_float4(v[0], v[1], v[2], v[3]));
+}
+
+struct DwArgs {
+    Operand x, dz;
+    int64_t n;
+    int rows, cols;
+    int tp, tq;          // tiles along the columns and the vocabulary
+    int stages;          // of the contraction over the batch
+    const int* targets;
+    const float* rest;   // NULL, or the rests of the targets' dz (x then has one plane)
+    uint8_t* grad;
+    int vector;
+    int add;
+};
+
+// What rounding took from the targets' dz, times x, added to the staged rows
+// of the table's gradient.  The block looks through the targets 2048 at a time
+// for rows of its pass, each wave through a quarter of them, and lists them in
+// order; then the wave that a row falls to (row mod 4) adds its entries in the
+// lists' order, so sums do not depend on timing.
+constexpr int kListTokens = 2048;
+template <int BT>
+__device__ __forceinline__ void add_rests(const DwArgs& a, uint8_t* lds, const Staging<BT>& st, int first_row, int first_col) {
+    constexpr int PART = kListTokens / 4;
+    static_assert(Staging<BT>::BYTES + kListTokens * 4 + 16 <= Pipe<BT, 4>::BYTES, "list area");
+    uint32_t* list = reinterpret_cast<uint32_t*>(lds + Staging<BT>::BYTES);
+    uint32_t* counts = list + kListTokens;
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    for (int64_t at = 0; at < a.n; at += kListTokens) {
+        const int64_t mine = at + wave * PART;
+        int target[PART / 64];
+#pragma unroll
+        for (int i = 0; i < PART / 64; ++i) {
+            const int64_t token = mine + i * 64 + lane;
+            target[i] = token < a.n ? a.targets[token] : -1;
+        }
+        int found = 0;
+#pragma unroll
+        for (int i = 0; i < PART / 64; ++i) {
+            const int c = target[i] - first_row;
+            const bool hit = target[i] >= 0 && c >= 0 && c < Staging<BT>::COLS;
+            const uint64_t mask = __ballot(hit);
+            if (hit)
+                list[wave * PART + found + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
+                    uint32_t(c) << 12 | uint32_t(wave * PART + i * 64 + lane);
+            found += __popcll(mask);
+        }
+        if (lane == 0) counts[wave] = uint32_t(found);
+        __syncthreads();
+        const int col = first_col + lane * 4;
+        for (int w = 0; w < 4; ++w) {
+            const int count = int(counts[w]);
+            for (int e = 0; e < count; ++e) {
+                const uint32_t entry = list[w * PART + e];
+                const int c = int(entry >> 12);
+                if ((c & 3) != wave || lane * 4 >= BT || col >= a.cols) continue;
+                const int64_t token = at + int(entry & 4095);
+                const float4 x = get4<kBF16>(a.x.base + token * a.x.pitch, col, 4, true);
+                float4& v = st.word(c, lane);
+                v = fma4(a.rest[token], x, v);
+            }
+        }
+        __syncthreads();  // the list and the counts are free again, the staged rows whole
+    }
+}
+
+// dW = dz^T x: both operands K-major (their rows are the contraction).
+template <int D, int BT>
+__global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
+    using S = Shape<BT, 4>;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
+    int ti, tj;
+    tile_of(int(blockIdx.x), a.tp * a.tq, a.tp, a.tq, ti, tj);
+    f32x16_t acc[S::MM][S::MN];
+    tile_loop<true, true, BT>(acc, a.x, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
+    auto row_of = [&](int c) { return a.grad + (int64_t(tj) * BT + c) * a.cols * (D == kBF16 ? 2 : 4); };
+    walk_columns<BT>(
+        acc, lds,
+        [&](int h, const Staging<BT>& st) {
+            if (a.rest) add_rests<BT>(a, lds, st, tj * BT + h * Staging<BT>::COLS, ti * BT);
+        },
+        [&](int c, int r) {
+            const int n = a.cols - (ti * BT + r);
+            return a.add && tj * BT + c < a.rows && n > 0 ? get4<D>(row_of(c), ti * BT + r, n, a.vector)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        },
+        [&](int c, int r, const float4& old, const float4& v) {
+            const int n = a.cols - (ti * BT + r);
+            if (tj * BT + c < a.rows && n > 0) put4<D>(row_of(c), ti * BT + r, n, a.vector, a.add ? fma4(1.f, old, v) : v);
+        });
+}
+
+// Zeros in rows of `cols` elements of es bytes, `stride` elements apart: what
+// an empty batch or an empty table gives.
+__global__ __launch_bounds__(256) void k_head_zero(uint8_t* to, int64_t rows, int64_t cols, int64_t stride, int es) {
+    const int64_t all = rows * cols;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+        uint8_t* p = to + (i / cols * stride + i % cols) * es;
+        if (es == 2)
+            *reinterpret_cast<uint16_t*>(p) = 0;
+        else
+            *reinterpret_cast<uint32_t*>(p) = 0;
+    }
+}
+
+// ---- host side ----
+
+hipError_t fill_zeros(uint8_t* to, int64_t rows, int64_t cols, int64_t stride, int32_t type, hipStream_t stream) {
+    if (rows * cols == 0) return hipSuccess;
+    const int64_t blocks = std::min<int64_t>((rows * cols + 255) / 256, 1 << 16);
+    k_head_zero<<<dim3(uint32_t(blocks)), dim3(256), 0, stream>>>(to, rows, cols, stride, type == kBF16 ? 2 : 4);
+    return hipGetLastError();
+}
+
+mfsdp_status hip_fail(hipError_t e, const char* what) {
+    return fail(MFSDP_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxFirst = int64_t(1) << 62, kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxCols = int64_t(1) << 20;         // byte offsets inside a stage stay below 2^31
+constexpr int64_t kMaxTiles = (int64_t(1) << 32) / 256 - 1;  // a launch has fewer than 2^32 threads
+constexpr int kCusHead = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile edge of a product with p x q results: the time of its rounds, one block
+// a CU with 256-tiles, two with 128, in units of a 128-tile on a whole CU,
+// which does its work 15% slower than a 256-tile.
+int pick_tile(int64_t p, int64_t q) {
+    const int64_t large = ceil_div(p, 256) * ceil_div(q, 256), small = ceil_div(p, 128) * ceil_div(q, 128);
+    const double tl = 4.0 * double(ceil_div(large, kCusHead)), ts = 2.0 * 1.15 * double(ceil_div(small, 2 * kCusHead));
+    return tl <= ts ? 256 : 128;
+}
+
+// Tile edge of dx, and the parts its contraction over the vocabulary is cut
+// into until the blocks fill the chip, each of at least 16 stages.
+int dx_tile(const mfsdp_entry& e, int64_t n) { return n <= 128 || e.cols <= 128 ? 128 : 256; }
+int dx_splits(const mfsdp_entry& e, int64_t n) {
+    const int t = dx_tile(e, n);
+    const int64_t tiles = ceil_div(e.cols, t) * ceil_div(n, t), slots = t == 256 ? kCusHead : 2 * kCusHead;
+    return int(std::clamp<int64_t>(slots / tiles, 1, std::max<int64_t>(1, ceil_div(e.rows, 64) / 16)));
+}
+
+// How a batch of n tokens is laid out and cut over one entry.
+struct HeadShape {
+    int x_planes, table_planes, dz_planes;
+    int64_t pitch;            // bytes of a packed row, in whole stages
+    int stages;
+    bool direct;              // the table is read where it lies
+    int64_t np, vp;           // padded tokens and rows of the table
+    bool few;
+    int tile;                 // edge of the logits' tiles
+    int part_rows;
+    int64_t n_parts;
+    int tile_dw, splits;
+    uint64_t x, table, parts, targets, logits, dz, rest, sums, total;
+    uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane
+};
+
+HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, bool grad) {
+    HeadShape s = {};
+    if (n == 0 || e.rows == 0 || e.cols == 0) return s;
+    s.x_planes = x_type == kBF16 ? 1 : 3;
+    s.table_planes = e.dtype == kBF16 ? 1 : 3;
+    s.dz_planes = s.x_planes + s.table_planes > 2 ? 3 : 1;
+    const int64_t kp = int64_t(align_up(uint64_t(e.cols), 64));
+    s.pitch = kp * 2;
+    s.stages = int(kp / 64);
+    s.direct = s.table_planes == 1 && kp == e.cols;
+    s.np = int64_t(align_up(uint64_t(n), kPadTokens));
+    s.vp = int64_t(align_up(uint64_t(e.rows), 256));
+    s.few = !grad && n <= kFewTokens;
+    s.tile = pick_tile(e.rows, n);
+    s.part_rows = s.few ? 32 : s.tile / 2;
+    s.n_parts = s.few ? ceil_div(e.rows, 32) : 2 * ceil_div(e.rows, s.tile);
+    uint64_t off = 0;
+    auto region = [&](uint64_t bytes) {
+        const uint64_t at = off;
+        off = align_up(off + bytes, kAlign);
+        return at;
+    };
+    s.x_plane = uint64_t(s.np) * uint64_t(s.pitch);
+    s.table_plane = uint64_t(e.rows) * uint64_t(s.pitch);
+    s.x = region(uint64_t(s.x_planes) * s.x_plane);
+    s.table = region(s.direct ? 0 : uint64_t(s.table_planes) * s.table_plane);
+    s.targets = region(uint64_t(s.np) * 4);
+    if (grad) {
+        s.rest = region(uint64_t(s.np) * 4);
+        s.dz_plane = uint64_t(s.np) * uint64_t(s.vp) * 2;
+        s.dz = region(uint64_t(s.dz_planes) * s.dz_plane);
+        s.splits = dx_splits(e, n);
+        s.tile_dw = pick_tile(e.rows, e.cols);
+        // a workspace for n tokens serves fewer of them, which may be cut into more parts
+        int64_t most = 0;
+        for (int64_t m = std::min<int64_t>(n, 2 * kCusHead * 256); m > 0; m = (m - 1) / 128 * 128) {
+            const int64_t splits = dx_splits(e, m);
+            if (splits > 1) most = std::max(most, splits * m);
+        }
+        s.sums = region(uint64_t(most) * align_up(uint64_t(e.cols), 4) * 4);
+    } else {
+        // the most that either edge, or a smaller batch in another form, needs
+        s.parts = region(16 * std::max(uint64_t(2 * ceil_div(e.rows, 128)) * uint64_t(n),
+                                       uint64_t(ceil_div(e.rows, 32)) * uint64_t(std::min(n, kFewTokens))));
+        s.logits = region(top_k > 0 ? uint64_t(n) * uint64_t(s.vp) * 4 : 0);
+    }
+    s.total = off;
+    return s;
+}
+
+mfsdp_status check_common(mfsdp_plan_t plan, int64_t entry, int64_t n, int32_t x_type, int32_t top_k) {
+    if (entry < 0 || entry >= int64_t(plan->entries.size()))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "entry index out of range");
+    if (x_type != MFSDP_F32 && x_type != MFSDP_BF16)
+        return fail(MFSDP_ERR_UNSUPPORTED, "x must be MFSDP_F32 or MFSDP_BF16");
+    if (n < 0 || n > kMaxTokens) return fail(MFSDP_ERR_INVALID_ARGUMENT, "n must be in 0..2^22");
+    if (top_k < 0 || top_k > kMaxTop) return fail(MFSDP_ERR_INVALID_ARGUMENT, "top_k must be in 0..64");
+    const mfsdp_entry& e = plan->entries[size_t(entry)];
+    if (e.cols > kMaxCols) return fail(MFSDP_ERR_UNSUPPORTED, "a table of more than 2^20 columns");
+    if (ceil_div(e.rows, 128) * ceil_div(n, 128) > kMaxTiles || ceil_div(e.rows, 128) * ceil_div(e.cols, 128) > kMaxTiles)
+        return fail(MFSDP_ERR_UNSUPPORTED, "more than 2^24 tiles of 128 x 128 logits: cut the batch");
+    return MFSDP_OK;
+}
+
+mfsdp_status check_batch(const mfsdp_entry& e, const void* params, const void* x, int64_t n, int32_t x_type,
+                         int64_t* stride, const void* ids, int32_t id_type, int64_t first_id, float scale) {
+    if (id_type != MFSDP_I32 && id_type != MFSDP_I64)
+        return fail(MFSDP_ERR_UNSUPPORTED, "id_type must be MFSDP_I32 or MFSDP_I64");
+    if (first_id < 0 || first_id > kMaxFirst) return fail(MFSDP_ERR_INVALID_ARGUMENT, "first_id must be in 0..2^62");
+    if (!std::isfinite(scale)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "scale is not finite");
+    if (*stride == 0) *stride = e.cols;
+    if (*stride < e.cols || *stride > kMaxStride) return fail(MFSDP_ERR_INVALID_ARGUMENT, "row stride below cols or above 2^40");
+    if (!params || misaligned(params, 16)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "params is NULL or not 16-byte aligned");
+    if (n > 0) {
+        if (!x || misaligned(x, x_type == MFSDP_BF16 ? 2 : 4)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "x is NULL or misaligned");
+        if (ids && misaligned(ids, id_type == MFSDP_I64 ? 8 : 4)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "ids is misaligned");
+    }
+    return MFSDP_OK;
+}
+
+mfsdp_status check_space(const void* workspace, uint64_t have, uint64_t need) {
+    if (need == 0) return MFSDP_OK;
+    if (!workspace || misaligned(workspace, kAlign))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "workspace is NULL or not 256-byte aligned");
+    if (have < need)
+        return fail(MFSDP_ERR_WORKSPACE_TOO_SMALL,
+                    "workspace has " + std::to_string(have) + " bytes, the call needs " + std::to_string(need));
+    return MFSDP_OK;
+}
+
+void launch_pack(const PackArgs& a, int src_type, hipStream_t stream) {
+    // a launch has fewer than 2^32 threads: whole rows each
+    constexpr int64_t kMost = ((int64_t(1) << 32) / kPackThreads - 1) * kPackThreads;
+    const int64_t per_row = a.pitch / 16, chunk = kMost / per_row * per_row;
+    for (int64_t w = 0; w < a.words; w += chunk) {
+        PackArgs b = a;
+        const int64_t row = w / per_row;
+        b.words = std::min(chunk, a.words - w);
+        b.src = a.src + row * a.stride * (src_type == kBF16 ? 2 : 4);
+        b.dst = a.dst + w * 16;
+        b.rows = std::max<int64_t>(0, a.rows - row);
+        if (a.ids.ids) b.ids.ids = static_cast<const uint8_t*>(a.ids.ids) + row * (a.ids.type == MFSDP_I64 ? 8 : 4);
+        if (a.targets) {
+            b.targets = a.targets + row;
+            b.rest = a.rest + row;
+        }
+        const dim3 grid(uint32_t(ceil_div(b.words, kPackThreads)));
+        if (src_type == kBF16)
+            k_head_pack<kBF16><<<grid, dim3(kPackThreads), 0, stream>>>(b);
+        else
+            k_head_pack<kF32><<<grid, dim3(kPackThreads), 0, stream>>>(b);
+    }
+}
+
+struct Batch {
+    const uint8_t* table;   // the entry's first element
+    const void* x;
+    int64_t n, stride;
+    int x_type;
+    Ids ids;
+    float scale;
+    uint8_t* ws;
+    hipStream_t stream;
+};
+
+LogitArgs logit_args(const mfsdp_entry& e, const HeadShape& s, const Batch& b) {
+    LogitArgs a = {};
+    a.rows = int(e.rows);
+    a.n = b.n;
+    a.stages = s.stages;
+    a.tp = int(ceil_div(e.rows, s.tile));
+    a.tq = int(ceil_div(b.n, s.tile));
+    a.c2 = float(double(b.scale) * 1.44269504088896340736);
+    a.ids = b.ids;
+    return a;
+}
+
+// The batch, and a table that cannot be read in place, in the tile loop's
+// layout.  rest: also the targets' rows, and zeros there.
+void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, bool rest, LogitArgs& a) {
+    PackArgs p = {};
+    p.src = static_cast<const uint8_t*>(b.x);
+    p.dst = b.ws + s.x;
+    p.stride = b.stride;
+    p.rows = b.n;
+    p.pitch = s.pitch;
+    p.plane = int64_t(s.x_plane);
+    p.words = s.np * (s.pitch / 16);
+    p.cols = int(e.cols);
+    p.vector = !misaligned(b.x, 16) && b.stride * (b.x_type == kBF16 ? 2 : 4) % 16 == 0;
+    p.ids = b.ids;
+    p.table_rows = int(e.rows);
+    if (rest) {
+        p.targets = reinterpret_cast<int*>(b.ws + s.targets);
+        p.rest = reinterpret_cast<float*>(b.ws + s.rest);
+    }
+    launch_pack(p, b.x_type, b.stream);
+    const int blocks = int(s.pitch / kBlockBytes);
+    a.x = Operand{p.dst, s.pitch, s.np, blocks, s.x_planes, p.plane};
+    a.table = Operand{b.table, s.pitch, e.rows, blocks, 1, 0};
+    if (s.direct) return;
+    p.src = b.table;
+    p.dst = b.ws + s.table;
+    p.stride = e.cols;
+    p.rows = e.rows;
+    p.plane = int64_t(s.table_plane);
+    p.words = e.rows * (s.pitch / 16);
+    p.vector = e.cols * (e.dtype == kBF16 ? 2 : 4) % 16 == 0;
+    p.ids = Ids{};
+    p.targets = nullptr;
+    launch_pack(p, e.dtype, b.stream);
+    a.table = Operand{p.dst, s.pitch, e.rows, blocks, s.table_planes, p.plane};
+}
+
+template <int WD, int XD> void launch_few(const FewArgs& f, hipStream_t stream) {
+    const dim3 grid(uint32_t(ceil_div(f.l.rows, 32)));
+    if (f.l.n <= 32)
+        k_head_few<WD, XD, 1><<<grid, dim3(256), 0, stream>>>(f);
+    else
+        k_head_few<WD, XD, 2><<<grid, dim3(256), 0, stream>>>(f);
+}
+
+hipError_t launch_logprob(const mfsdp_entry& e, const HeadShape& s, const Batch& b, RowArgs r) {
+    LogitArgs a = logit_args(e, s, b);
+    a.parts = reinterpret_cast<float4*>(b.ws + s.parts);
+    a.targets = reinterpret_cast<float*>(b.ws + s.targets);
+    a.logits = r.top_k > 0 ? reinterpret_cast<float*>(b.ws + s.logits) : nullptr;
+    a.ldl = s.vp;
+    if (s.few) {
+        const int xs = b.x_type == kBF16 ? 2 : 4, es = e.dtype == kBF16 ? 2 : 4;
+        const FewArgs f = {a, b.table, static_cast<const uint8_t*>(b.x), b.stride * xs, e.cols * es, int(e.cols)};
+        if (e.dtype == kBF16)
+            b.x_type == kBF16 ? launch_few<kBF16, kBF16>(f, b.stream) : launch_few<kBF16, kF32>(f, b.stream);
+        else
+            b.x_type == kBF16 ? launch_few<kF32, kBF16>(f, b.stream) : launch_few<kF32, kF32>(f, b.stream);
+    } else {
+        pack_operands(e, s, b, false, a);
+        const dim3 grid(uint32_t(a.tp) * uint32_t(a.tq));
+        if (s.tile == 256)
+            k_head_logits<256><<<grid, dim3(256), 0, b.stream>>>(a);
+        else
+            k_head_logits<128><<<grid, dim3(256), 0, b.stream>>>(a);
+    }
+    r.parts = a.parts;
+    r.targets = a.targets;
+    r.logits = a.logits;
+    r.ldl = a.ldl;
+    r.n_parts = int(s.n_parts);
+    r.part_rows = s.part_rows;
+    if (s.few)
+        k_head_rows<16><<<dim3(uint32_t(b.n)), dim3(1024), 0, b.stream>>>(r);
+    else
+        k_head_rows<1><<<dim3(uint32_t(ceil_div(b.n, 4))), dim3(256), 0, b.stream>>>(r);
+    return hipGetLastError();
+}
+
+struct GradOut {
+    const mfsdp_head_record* records;
+    const float *dlogp, *dentropy;
+    uint8_t* dx;
+    int64_t dx_stride;
+    uint8_t* grad;      // the entry's gradient
+    int add;
+};
+
+template <int D> void launch_dx(const DxArgs& a, int tile, hipStream_t stream) {
+    const dim3 grid(uint32_t(a.tp) * uint32_t(a.tq) * uint32_t(a.splits));
+    if (tile == 256)
+        k_head_dx<D, 256><<<grid, dim3(256), 0, stream>>>(a);
+    else
+        k_head_dx<D, 128><<<grid, dim3(256), 0, stream>>>(a);
+    if (a.splits > 1) k_head_dx_sum<D><<<dim3(uint32_t(ceil_div(a.n * (a.ld / 4), 256))), dim3(256), 0, stream>>>(a);
+}
+
+template <int D> void launch_dw(const DwArgs& a, int tile, hipStream_t stream) {
+    const dim3 grid(uint32_t(a.tp) * uint32_t(a.tq));
+    if (tile == 256)
+        k_head_dw<D, 256><<<grid, dim3(256), 0, stream>>>(a);
+    else
+        k_head_dw<D, 128><<<grid, dim3(256), 0, stream>>>(a);
+}
+
+hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b, const GradOut& g) {
+    DzArgs d = {};
+    d.l = logit_args(e, s, b);
+    pack_operands(e, s, b, true, d.l);
+    d.records = g.records;
+    d.dlogp = g.dlogp;
+    d.dentropy = g.dentropy;
+    d.scale = b.scale;
+    d.dz = b.ws + s.dz;
+    d.pitch = s.vp * 2;
+    d.planes = s.dz_planes;
+    d.plane = int64_t(s.dz_plane);
+    d.rest = reinterpret_cast<float*>(b.ws + s.rest);
+    const dim3 grid(uint32_t(d.l.tp) * uint32_t(d.l.tq));
+    if (s.tile == 256)
+        k_head_dz<256><<<grid, dim3(256), 0, b.stream>>>(d);
+    else
+        k_head_dz<128><<<grid, dim3(256), 0, b.stream>>>(d);
+    // tokens and vocabulary rows that dz was written for
+    const Operand dz = {d.dz, d.pitch, int64_t(d.l.tq) * s.tile, int(int64_t(d.l.tp) * s.tile * 2 / kBlockBytes), s.dz_planes,
+                        d.plane};
+    const int* targets = reinterpret_cast<const int*>(b.ws + s.targets);
+    const float* rest = s.dz_planes == 1 ? d.rest : nullptr;
+    if (g.dx) {
+        DxArgs a = {};
+        const int tile = dx_tile(e, b.n), xs = b.x_type == kBF16 ? 2 : 4;
+        a.table = d.l.table;
+        a.dz = dz;
+        a.n = b.n;
+        a.cols = int(e.cols);
+        a.rows = int(e.rows);
+        a.tp = int(ceil_div(e.cols, tile));
+        a.tq = int(ceil_div(b.n, tile));
+        a.stages = int(ceil_div(e.rows, 64));
+        a.splits = s.splits;
+        a.ids = b.ids;
+        a.targets = targets;
+        a.rest = rest;
+        a.dx = g.dx;
+        a.stride = g.dx_stride;
+        a.vector = !misaligned(g.dx, uintptr_t(4 * xs)) && g.dx_stride % 4 == 0;
+        a.sums = reinterpret_cast<float*>(b.ws + s.sums);
+        a.ld = int64_t(align_up(uint64_t(e.cols), 4));
+        b.x_type == kBF16 ? launch_dx<kBF16>(a, tile, b.stream) : launch_dx<kF32>(a, tile, b.stream);
+    }
+    if (g.grad) {
+        DwArgs a = {};
+        a.x = d.l.x;
+        a.dz = dz;
+        a.n = b.n;
+        a.rows = int(e.rows);
+        a.cols = int(e.cols);
+        a.tp = int(ceil_div(e.cols, s.tile_dw));
+        a.tq = int(ceil_div(e.rows, s.tile_dw));
+        a.stages = int(ceil_div(b.n, 64));
+        a.targets = targets;
+        a.rest = rest;
+        a.grad = g.grad;
+        a.vector = e.cols % 4 == 0;  // the entry is 16-byte aligned
+        a.add = g.add;
+        e.dtype == kBF16 ? launch_dw<kBF16>(a, s.tile_dw, b.stream) : launch_dw<kF32>(a, s.tile_dw, b.stream);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace mfsdp
+
+using namespace mfsdp;
+
+extern "C" mfsdp_status mfsdp_plan_head_workspace_bytes(mfsdp_plan_t plan, int64_t entry, int64_t n, int32_t x_type,
+                                                        int32_t top_k, int32_t grad, uint64_t* bytes) {
+    clear_error();
+    if (!plan || !bytes) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL argument");
+    if (mfsdp_status st = check_common(plan, entry, n, x_type, top_k); st != MFSDP_OK) return st;
+    if (grad != 0 && grad != 1) return fail(MFSDP_ERR_INVALID_ARGUMENT, "grad must be 0 or 1");
+    const mfsdp_entry& e = plan->entries[size_t(entry)];
+    // one workspace serves the call forward too
+    uint64_t most = head_shape(e, n, x_type, top_k, false).total;
+    if (grad) most = std::max(most, head_shape(e, n, x_type, 0, true).total);
+    *bytes = most;
+    return MFSDP_OK;
+}
+
+extern "C" mfsdp_status mfsdp_head_logprob(mfsdp_plan_t plan, int64_t entry, const mfsdp_head_logprob_args* args) {
+    clear_error();
+    if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
+    if (mfsdp_status st = check_common(plan, entry, args->n, args->x_type, args->top_k); st != MFSDP_OK) return st;
+    const mfsdp_entry& e = plan->entries[size_t(entry)];
+    int64_t stride = args->x_stride;
+    if (mfsdp_status st = check_batch(e, args->params, args->x, args->n, args->x_type, &stride, args->ids, args->id_type,
+                                      args->first_id, args->scale);
+        st != MFSDP_OK)
+        return st;
+    if (args->n == 0) return MFSDP_OK;
+    if (!args->records || misaligned(args->records, 8))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "records is NULL or not 8-byte aligned");
+    if (misaligned(args->logp, 4) || misaligned(args->entropy, 4) || misaligned(args->top_logp, 4) ||
+        misaligned(args->top_logits, 4) || misaligned(args->top_ids, 8))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "an output is misaligned");
+    if (args->top_k > 0 && !args->top_ids) return fail(MFSDP_ERR_INVALID_ARGUMENT, "top_ids is NULL");
+    const HeadShape s = head_shape(e, args->n, args->x_type, args->top_k, false);
+    if (mfsdp_status st = check_space(args->workspace, args->workspace_bytes, s.total); st != MFSDP_OK) return st;
+    RowArgs r = {};
+    r.n = args->n;
+    r.rows = int(e.rows);
+    r.ids = Ids{args->ids, args->first_id, args->id_type};
+    r.first_id = args->first_id;
+    r.records = args->records;
+    r.logp = args->logp;
+    r.entropy = args->entropy;
+    r.top_k = args->top_k;
+    r.top_ids = args->top_ids;
+    r.top_logp = args->top_logp;
+    r.top_logits = args->top_logits;
+    hipStream_t stream = static_cast<hipStream_t>(args->stream);
+    hipError_t err;
+    if (e.rows == 0 || e.cols == 0) {
+        k_head_empty<<<dim3(uint32_t(ceil_div(args->n, 256))), dim3(256), 0, stream>>>(r);
+        err = hipGetLastError();
+    } else {
+        const Batch b = {static_cast<const uint8_t*>(args->params) + e.offset, args->x, args->n, stride, args->x_type, r.ids,
+                         args->scale, static_cast<uint8_t*>(args->workspace), stream};
+        err = launch_logprob(e, s, b, r);
+    }
+    if (err != hipSuccess) return hip_fail(err, "log probability launch");
+    return MFSDP_OK;
+}
+
+extern "C" mfsdp_status mfsdp_head_total(const mfsdp_head_total_args* args) {
+    clear_error();
+    if (!args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL args");
+    if (args->count < 1 || args->count > 65536) return fail(MFSDP_ERR_INVALID_ARGUMENT, "count must be in 1..65536");
+    if (args->n < 0 || args->n > kMaxTokens) return fail(MFSDP_ERR_INVALID_ARGUMENT, "n must be in 0..2^22");
+    if (args->top_k < 0 || args->top_k > kMaxTop) return fail(MFSDP_ERR_INVALID_ARGUMENT, "top_k must be in 0..64");
+    if (args->n == 0) return MFSDP_OK;
+    if (!args->parts || misaligned(args->parts, 8) || !args->records || misaligned(args->records, 8))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "parts or records is NULL or not 8-byte aligned");
+    if (misaligned(args->logp, 4) || misaligned(args->entropy, 4) || misaligned(args->top_logp, 4) ||
+        misaligned(args->top_logits, 4) || misaligned(args->top_ids, 8) || misaligned(args->part_top_ids, 8) ||
+        misaligned(args->part_top_logits, 4))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "a buffer is misaligned");
+    if (args->top_k > 0 && (!args->top_ids || !args->part_top_ids || !args->part_top_logits))
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "top_ids, part_top_ids or part_top_logits is NULL");
+    TotalArgs a = {};
+    a.parts = args->parts;
+    a.count = int(args->count);
+    a.n = args->n;
+    a.records = args->records;
+    a.logp = args->logp;
+    a.entropy = args->entropy;
+    a.top_k = args->top_k;
+    a.part_ids = args->part_top_ids;
+    a.part_logits = args->part_top_logits;
+    a.top_ids = args->top_ids;
+    a.top_logp = args->top_logp;
+    a.top_logits = args->top_logits;
+    k_head_total<<<dim3(uint32_t(ceil_div(a.n, 4))), dim3(256), 0, static_cast<hipStream_t>(args->stream)>>>(a);
+    if (hipError_t err = hipGetLastError(); err != hipSuccess) return hip_fail(err, "head total launch");
+    return MFSDP_OK;
+}
+
+extern "C" mfsdp_status mfsdp_head_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_head_grad_args* args) {
+    clear_error();
+    if (!plan || !args) return fail(MFSDP_ERR_INVALID_ARGUMENT, "NULL plan or args");
+    if (mfsdp_status st = check_common(plan, entry, args->n, args->x_type, 0); st != MFSDP_OK) return st;
+    const mfsdp_entry& e = plan->entries[size_t(entry)];
+    int64_t stride = args->x_stride, dx_stride = args->dx_stride == 0 ? e.cols : args->dx_stride;
+    if (mfsdp_status st = check_batch(e, args->params, args->x, args->n, args->x_type, &stride, args->ids, args->id_type,
+                                      args->first_id, args->scale);
+        st != MFSDP_OK)
+        return st;
+    if (args->accumulate != 0 && args->accumulate != 1)
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "accumulate must be 0 or 1");
+    if (dx_stride < e.cols || dx_stride > kMaxStride)
+        return fail(MFSDP_ERR_INVALID_ARGUMENT, "dx row stride below cols or above 2^40");
+    if (misaligned(args->grads, 16)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "grads is not 16-byte aligned");
+    if (misaligned(args->dx, args->x_type == MFSDP_BF16 ? 2 : 4)) return fail(MFSDP_ERR_INVALID_ARGUMENT, "dx is misaligned");
+    if (args->n > 0) {
+        if (!args->records || misaligned(args->records, 8))
+            return fail(MFSDP_ERR_INVALID_ARGUMENT, "records is NULL or not 8-byte aligned");
+        if (!args->dlogp || misaligned(args->dlogp, 4) || misaligned(args->dentropy, 4))
+            return fail(MFSDP_ERR_INVALID_ARGUMENT, "dlogp is NULL, or dlogp or dentropy misaligned");
+    }
+    hipStream_t stream = static_cast<hipStream_t>(args->stream);
+    uint8_t* grad = args->grads ? static_cast<uint8_t*>(args->grads) + e.offset : nullptr;
+    const HeadShape s = head_shape(e, args->n, args->x_type, 0, true);
+    if (mfsdp_status st = check_space(args->workspace, args->workspace_bytes, s.total); st != MFSDP_OK) return st;
+    hipError_t err = hipSuccess;
+    if (e.cols == 0 || (args->n == 0 && (e.rows == 0 || args->accumulate || !grad))) return MFSDP_OK;
+    if (args->n == 0) {
+        err = fill_zeros(grad, e.rows, e.cols, e.cols, e.dtype, stream);
+    } else if (e.rows == 0) {
+        if (args->dx) err = fill_zeros(static_cast<uint8_t*>(args->dx), args->n, e.cols, dx_stride, args->x_type, stream);
+    } else {
+        const Batch b = {static_cast<const uint8_t*>(args->params) + e.offset, args->x, args->n, stride, args->x_type,
+                         Ids{args->ids, args->first_id, args->id_type}, args->scale, static_cast<uint8_t*>(args->workspace),
+                         stream};
+        const GradOut g = {args->records, args->dlogp, args->dentropy, static_cast<uint8_t*>(args->dx), dx_stride, grad,
+                           args->accumulate};
+        err = launch_grad(e, s, b, g);
+    }
+    if (err != hipSuccess) return hip_fail(err, "head gradient launch");
+    return MFSDP_OK;
+}
