@@ -286,110 +286,137 @@ struct FewArgs {
     int cols;
 };
 
-// Eight consecutive elements of a row as they lie (unaligned words), zeros
-// past the last column.
-template <int D> struct Eight;
-template <> struct Eight<kBF16> {
-    u32x4_t v;
-    __device__ __forceinline__ void load(const uint8_t* row, int k, int cols) {
-        typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(2)));
-        if (k + 8 <= cols) {
+// The 16 bytes of T (bf16 or fp32) that elements k .. of a row make, the row in
+// type D and at any address; zeros past the last column.  INSIDE: there are none.
+template <typename T, int D, bool INSIDE> __device__ __forceinline__ u32x4_t granule(const uint8_t* row, int k, int cols) {
+    constexpr int N = 16 / int(sizeof(T));
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (INSIDE || k + N <= cols) {
+        if constexpr (D == kF32) {
+            typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(4)));
+            v = *reinterpret_cast<const word_t*>(row + 4 * k);
+        } else if constexpr (sizeof(T) == 2) {
+            typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(2)));
             v = *reinterpret_cast<const word_t*>(row + 2 * k);
         } else {
-            v = u32x4_t{0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e < cols) v[e >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[k + e]) << (16 * (e & 1));
+            typedef unsigned int word_t __attribute__((ext_vector_type(2), aligned(2)));
+            const word_t r = *reinterpret_cast<const word_t*>(row + 2 * k);
+            v = u32x4_t{r[0] << 16, r[0] & 0xffff0000u, r[1] << 16, r[1] & 0xffff0000u};
         }
-    }
-    // four of them (half 0 or 1) as fp32
-    __device__ __forceinline__ u32x4_t wide(int half) const {
-        const uint32_t a = v[2 * half], b = v[2 * half + 1];
-        return u32x4_t{a << 16, a & 0xffff0000u, b << 16, b & 0xffff0000u};
-    }
-};
-template <> struct Eight<kF32> {
-    u32x4_t v[2];
-    __device__ __forceinline__ void load(const uint8_t* row, int k, int cols) {
-        typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(4)));
-        if (k + 8 <= cols) {
-            v[0] = *reinterpret_cast<const word_t*>(row + 4 * k);
-            v[1] = *reinterpret_cast<const word_t*>(row + 4 * k + 16);
-        } else {
+    } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = k + e < cols ? reinterpret_cast<const uint32_t*>(row)[k + e] : 0u;
-        }
+        for (int e = 0; e < N; ++e)
+            if (k + e < cols) {
+                if constexpr (D == kF32)
+                    v[e] = reinterpret_cast<const uint32_t*>(row)[k + e];
+                else if constexpr (sizeof(T) == 2)
+                    v[e >> 1] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[k + e]) << (16 * (e & 1));
+                else
+                    v[e] = uint32_t(reinterpret_cast<const uint16_t*>(row)[k + e]) << 16;
+            }
     }
-    __device__ __forceinline__ u32x4_t wide(int half) const { return v[half]; }
-};
+    return v;
+}
 
-// 32 rows of the table by NB * 32 tokens a block.  Its four waves share the
-// contraction, 64 elements in turn; a lane holds half of those of one row, so
-// that a row is read in whole lines, and the contraction's order inside a line
-// is the same permutation for both operands.  Every column of the product is
-// one token's alone, so that what padding or a row past the last holds goes
-// nowhere.
-template <int WD, int XD, int NB>
+// Orders a wave's LDS writes before its reads and the other way round: lanes
+// exchange values through a part of LDS that no other wave touches.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// RB * 32 rows of the table by NB * 32 tokens a block.  Its four waves share
+// the contraction, 128 bytes of T in turn.  A wave loads its lines of both
+// operands with 8 lanes a row, so that a load instruction takes whole lines (a
+// load straight into the fragment's layout touches 64 of them for 16 bytes
+// each: 410 us where this takes 185, 32 tokens over 128256 x 4096), several
+// lines ahead, and turns them to fragments in an LDS tile of its own: no
+// barrier until the end.  Every column of the product is one token's alone, so
+// what padding or a row past the last holds goes nowhere.
+template <int WD, int XD, int RB, int NB>
 __global__ __launch_bounds__(256) void k_head_few(FewArgs f) {
+    using T = std::conditional_t<WD == kBF16 && XD == kBF16, uint16_t, float>;
+    constexpr int LINE = 128 / int(sizeof(T)), GE = 16 / int(sizeof(T));  // elements of a line and a granule
+    constexpr int ROWS = (RB + NB) * 32;                                   // LDS rows of a wave's tile
+    constexpr int AHEAD = RB + NB == 2 ? 4 : 2;                            // lines loaded at once
+    constexpr int TILE = 4 * ROWS * 128, SUMS = 4 * RB * NB * 16 * 64 * 4;
     const LogitArgs& a = f.l;
-    __shared__ float sums[4][NB * 16][64];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[TILE > SUMS ? TILE : SUMS];
     const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
     const int frow = lane & 31, fhalf = lane >> 5;
-    const int row0 = int(blockIdx.x) * 32;
-    const uint8_t* w = f.table + int64_t(min(row0 + frow, a.rows - 1)) * f.pitch;
-    const uint8_t* x[NB];
+    const int row0 = int(blockIdx.x) * RB * 32;
+    uint8_t* tile = lds + wave * ROWS * 128;
+    const uint8_t *w[RB * 4], *x[NB * 4];  // the rows whose granules the lane loads
 #pragma unroll
-    for (int b = 0; b < NB; ++b) x[b] = f.x + min(int64_t(b * 32 + frow), a.n - 1) * f.x_pitch;
-    f32x16_t acc[NB] = {};
-    const int lines = (f.cols + 63) / 64;
-    auto body = [&](int line, auto COUNT) {
+    for (int i = 0; i < RB * 4; ++i) w[i] = f.table + int64_t(min(row0 + i * 8 + (lane >> 3), a.rows - 1)) * f.pitch;
+#pragma unroll
+    for (int i = 0; i < NB * 4; ++i) x[i] = f.x + min(int64_t(i * 8 + (lane >> 3)), a.n - 1) * f.x_pitch;
+    f32x16_t acc[RB][NB] = {};
+    const int lines = (f.cols + LINE - 1) / LINE, mine = (lane & 7) * GE;
+    // L lines from `line` on, four apart
+    auto run = [&](int line, auto COUNT, auto INSIDE) {
         constexpr int L = decltype(COUNT)::value;
-        Eight<WD> ew[L][4];
-        Eight<XD> ex[L][NB][4];
+        u32x4_t ew[L][RB * 4], ex[L][NB * 4];
 #pragma unroll
-        for (int l = 0; l < L; ++l)
+        for (int l = 0; l < L; ++l) {
+            const int k = (line + 4 * l) * LINE + mine;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int k = (line + 4 * l) * 64 + fhalf * 32 + g * 8;
-                ew[l][g].load(w, k, f.cols);
+            for (int i = 0; i < RB * 4; ++i) ew[l][i] = granule<T, WD, decltype(INSIDE)::value>(w[i], k, f.cols);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) ex[l][b][g].load(x[b], k, f.cols);
+            for (int i = 0; i < NB * 4; ++i) ex[l][i] = granule<T, XD, decltype(INSIDE)::value>(x[i], k, f.cols);
+        }
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+#pragma unroll
+            for (int i = 0; i < (RB + NB) * 4; ++i) {
+                const int r = i * 8 + (lane >> 3);
+                *reinterpret_cast<u32x4_t*>(tile + r * 128 + swz_r<8>(r, lane & 7) * 16) = i < RB * 4 ? ew[l][i] : ex[l][i - RB * 4];
             }
+            wave_exchange();
 #pragma unroll
-        for (int l = 0; l < L; ++l)
+            for (int kk = 0; kk < 4; ++kk) {
+                u32x4_t fr[RB + NB];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if constexpr (WD == kBF16 && XD == kBF16) {
-                        Mfma<uint16_t>::step(acc[b], ew[l][g].v, ex[l][b][g].v);
-                    } else {
-                        Mfma<float>::step(acc[b], ew[l][g].wide(0), ex[l][b][g].wide(0));
-                        Mfma<float>::step(acc[b], ew[l][g].wide(1), ex[l][b][g].wide(1));
-                    }
+                for (int j = 0; j < RB + NB; ++j) {
+                    const int r = j * 32 + frow;
+                    fr[j] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + swz_r<8>(r, 2 * kk + fhalf) * 16);
                 }
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) Mfma<T>::step(acc[i][j], fr[i], fr[RB + j]);
+            }
+            wave_exchange();
+        }
     };
-    // lines of whole elements in batches, the rest one by one
-    const int whole = f.cols / 64;
-    constexpr int BATCH = WD == kBF16 && XD == kBF16 ? (NB == 1 ? 4 : 2) : (NB == 1 ? 2 : 1);
+    using One = std::integral_constant<int, 1>;
+    const int whole = f.cols / LINE;  // lines without zeros
     int line = wave;
-    for (; line + 4 * (BATCH - 1) < whole; line += 4 * BATCH) body(line, std::integral_constant<int, BATCH>{});
-    for (; line < lines; line += 4) body(line, std::integral_constant<int, 1>{});
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sums[wave][b * 16 + e][lane] = acc[b][e];
+    for (; line + 4 * (AHEAD - 1) < whole; line += 4 * AHEAD) run(line, std::integral_constant<int, AHEAD>{}, std::true_type{});
+    for (; line < whole; line += 4) run(line, One{}, std::true_type{});
+    if (line < lines) run(line, One{}, std::false_type{});
     __syncthreads();
-    const int held = a.rows - row0;
+    float* sums = reinterpret_cast<float*>(lds);  // [wave][i, j, accumulator][lane]
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        if (b % 4 != wave) continue;
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sums[((wave * RB * NB + i * NB + j) * 16 + e) * 64 + lane] = acc[i][j][e];
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < RB * NB; ++q) {
+        if (q % 4 != wave) continue;
         f32x16_t col[1];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            col[0][e] = (sums[0][b * 16 + e][lane] + sums[1][b * 16 + e][lane]) +
-                        (sums[2][b * 16 + e][lane] + sums[3][b * 16 + e][lane]);
-        reduce_column<1, true>(a, col, b * 32 + frow, row0, held, blockIdx.x, fhalf);
+        for (int e = 0; e < 16; ++e) {
+            auto of = [&](int v) { return sums[((v * RB * NB + q) * 16 + e) * 64 + lane]; };
+            col[0][e] = (of(0) + of(1)) + (of(2) + of(3));
+        }
+        const int first = row0 + q / NB * 32;
+        if (first < a.rows)
+            reduce_column<1, true>(a, col, q % NB * 32 + frow, first, a.rows - first, int64_t(blockIdx.x) * RB + q / NB, fhalf);
     }
 }
 
@@ -418,20 +445,24 @@ struct TopList {
     int k, lane;
     __device__ __forceinline__ TopList(int k_, int lane_) : v(-INFINITY), id(INT32_MAX), k(k_), lane(lane_) {}
     static __device__ __forceinline__ bool before(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+    // the value in a lane (the same lane for all), and each lane's neighbour's
+    static __device__ __forceinline__ int read(int x, int from) { return __builtin_amdgcn_readlane(x, from); }
+    static __device__ __forceinline__ float read(float x, int from) { return __int_as_float(read(__float_as_int(x), from)); }
+    static __device__ __forceinline__ int shifted(int x) { return __builtin_amdgcn_mov_dpp(x, 0x138, 0xf, 0xf, false); }
     // every lane offers one value (or none); NaN is never before anything
     __device__ __forceinline__ void offer(float x, int ix, bool valid) {
-        float last = __shfl(v, k - 1, 64);
-        int ilast = __shfl(id, k - 1, 64);
+        float last = read(v, k - 1);
+        int ilast = read(id, k - 1);
         uint64_t mask = __ballot(valid && before(x, ix, last, ilast));
         while (mask) {
             const int src = __ffsll(static_cast<unsigned long long>(mask)) - 1;
             mask &= mask - 1;
-            const float c = __shfl(x, src, 64);
-            const int ic = __shfl(ix, src, 64);
+            const float c = read(x, src);
+            const int ic = read(ix, src);
             if (!before(c, ic, last, ilast)) continue;  // the list has grown since (the same in every lane)
             const int pos = __popcll(__ballot(before(v, id, c, ic)));
-            const float pv = __shfl_up(v, 1, 64);
-            const int pi = __shfl_up(id, 1, 64);
+            const float pv = __int_as_float(shifted(__float_as_int(v)));  // of lane - 1
+            const int pi = shifted(id);
             if (lane > pos) {
                 v = pv;
                 id = pi;
@@ -439,8 +470,8 @@ struct TopList {
                 v = c;
                 id = ic;
             }
-            last = __shfl(v, k - 1, 64);
-            ilast = __shfl(id, k - 1, 64);
+            last = read(v, k - 1);
+            ilast = read(id, k - 1);
         }
     }
 };
@@ -463,82 +494,161 @@ struct RowArgs {
 
 __device__ __forceinline__ float nat(float y2) { return y2 * kLn2; }
 
-// One token a group of WAVES waves.  Lanes join the parts they stride over in
-// order, then lanes by a butterfly, then waves in order: the same order for
-// the same sizes.
-template <int WAVES>
-__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void k_head_rows(RowArgs a) {
-    constexpr int TOKENS = WAVES == 1 ? 4 : 1;
-    __shared__ Sums sums[WAVES];
-    __shared__ float best_v[WAVES == 1 ? 1 : WAVES * kMaxTop];
-    __shared__ int best_id[WAVES == 1 ? 1 : WAVES * kMaxTop];
-    const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
-    const int64_t token = int64_t(blockIdx.x) * TOKENS + (WAVES == 1 ? wave : 0);
-    if (token >= a.n) return;  // whole waves; with WAVES > 1 never
-    const int first = WAVES == 1 ? lane : int(threadIdx.x), stride = 64 * WAVES;
-    const Token t = token_of(a.ids, token, a.rows);
-    Sums mine = {-INFINITY, 0.f, 0.f};
-    TopList parts(a.top_k ? a.top_k : 1, lane);
-    const int turns = (a.n_parts + stride - 1) / stride;
-    for (int u = 0; u < turns; ++u) {
-        const int p = u * stride + first;
-        float4 v = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        if (p < a.n_parts) v = a.parts[int64_t(p) * a.n + token];
-        mine = join(mine, Sums{v.x, v.y, v.z});
-        if (a.top_k) parts.offer(v.x, p, p < a.n_parts);
+// A token's sums, known to a whole wave, and what follows from them.
+struct Row {
+    Token t;
+    Sums sum;
+    float ls;   // log2 of the sum
+    __device__ __forceinline__ float logp(float y) const { return nat((y - sum.m) - ls); }
+};
+__device__ __forceinline__ Row finish_row(const RowArgs& a, int64_t token, const Token& t, const Sums& sum, bool writes) {
+    const Row r = {t, sum, sum.s == 0.f ? 0.f : log2f(sum.s)};
+    if (writes) {
+        const float y = t.target >= 0 ? a.targets[token] : 0.f;
+        a.records[token] = mfsdp_head_record{t.live ? sum.m : 0.f, t.live ? sum.s : 0.f, t.live ? sum.w : 0.f, y, t.target >= 0, t.live};
+        if (a.logp) a.logp[token] = t.target >= 0 ? r.logp(y) : 0.f;
+        if (a.entropy) a.entropy[token] = t.live && sum.s != 0.f ? nat(r.ls - sum.w / sum.s) : 0.f;
     }
+    return r;
+}
+__device__ __forceinline__ void put_top(const RowArgs& a, int64_t token, const Row& r, int place, float y, int id) {
+    const int64_t at = token * a.top_k + place;
+    const bool some = id != INT32_MAX;
+    a.top_ids[at] = some ? a.first_id + id : -1;
+    if (a.top_logits) a.top_logits[at] = some ? y : -INFINITY;
+    if (a.top_logp) a.top_logp[at] = some ? r.logp(y) : -INFINITY;
+}
+__device__ __forceinline__ Sums wave_join(Sums mine, int lane) {
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const Sums other = shuffled(mine, off);
         mine = (lane & off) ? join(other, mine) : join(mine, other);
     }
-    if constexpr (WAVES > 1) {
-        if (lane == 0) sums[wave] = mine;
-        if (a.top_k) {
-            best_v[wave * kMaxTop + lane] = parts.v;
-            best_id[wave * kMaxTop + lane] = parts.id;
+    return mine;
+}
+
+// A token's alternatives by one wave: the parts with the largest M in a list,
+// then those parts' rows in another.
+__device__ __forceinline__ void top_by_lists(const RowArgs& a, int64_t token, const Row& r, int lane) {
+    TopList parts(a.top_k, lane), top(a.top_k, lane);
+    if (r.t.live)
+        for (int p0 = 0; p0 < a.n_parts; p0 += 64) {
+            const int p = p0 + lane;
+            parts.offer(p < a.n_parts ? a.parts[int64_t(p) * a.n + token].x : 0.f, p, p < a.n_parts);
         }
-        __syncthreads();
-        if (wave > 0) return;
-        mine = sums[0];
-        for (int k = 1; k < WAVES; ++k) {
-            mine = join(mine, sums[k]);
-            if (a.top_k) parts.offer(best_v[k * kMaxTop + lane], best_id[k * kMaxTop + lane], lane < a.top_k);
+    // the rows of the chosen parts, 64 at a time over all of them, four loads on their way
+    const int total = r.t.live ? a.top_k * a.part_rows : 0;
+    for (int at = 0; at < total; at += 256) {
+        float y4[4];
+        int row4[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = at + u * 64 + lane, k = i / a.part_rows;
+            const int p = __shfl(parts.id, min(k, 63), 64);
+            const int64_t row = int64_t(p) * a.part_rows + i % a.part_rows;
+            row4[u] = i < total && p != INT32_MAX && row < a.rows ? int(row) : -1;  // fewer parts, the table's end
+            y4[u] = row4[u] >= 0 ? a.logits[token * a.ldl + row] : 0.f;
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) top.offer(y4[u], row4[u], row4[u] >= 0);
     }
-    const float y = t.target >= 0 && a.rows > 0 ? a.targets[token] : 0.f;
-    const float ls = mine.s == 0.f ? 0.f : log2f(mine.s);
-    if (lane == 0) {
-        mfsdp_head_record r;
-        r.max = t.live ? mine.m : 0.f;
-        r.sum = t.live ? mine.s : 0.f;
-        r.wsum = t.live ? mine.w : 0.f;
-        r.target = y;
-        r.found = t.target >= 0;
-        r.active = t.live;
-        a.records[token] = r;
-        if (a.logp) a.logp[token] = t.target >= 0 ? nat((y - mine.m) - ls) : 0.f;
-        if (a.entropy) a.entropy[token] = t.live && mine.s != 0.f ? nat(ls - mine.w / mine.s) : 0.f;
+    if (lane < a.top_k) put_top(a, token, r, lane, top.v, top.id);
+}
+
+// Rows of a batch, a wave each: lanes join the parts they stride over in
+// order, then by a butterfly, the same order for the same sizes.
+__global__ __launch_bounds__(256) void k_head_rows(RowArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t token = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (token >= a.n) return;
+    Sums mine = {-INFINITY, 0.f, 0.f};
+    for (int p = lane; p < a.n_parts; p += 64) {
+        const float4 v = a.parts[int64_t(p) * a.n + token];
+        mine = join(mine, Sums{v.x, v.y, v.z});
     }
+    mine = wave_join(mine, lane);
+    const Row r = finish_row(a, token, token_of(a.ids, token, a.rows), mine, lane == 0);
+    if (a.top_k) top_by_lists(a, token, r, lane);
+}
+
+// Rows of a few tokens, a block of 16 waves each.  Alternatives without a
+// serial list: the k-th largest of 64 groups' largest M is at most the k-th
+// largest logit, so the parts whose M reaches it hold all alternatives, and so
+// do their logits that reach it; each of those finds its place by counting the
+// ones before it.  (Lists take 29 us for one token where this takes 13.)  More
+// parts or logits than there is room for, as where most logits are equal, go
+// through the lists.
+constexpr int kRowWaves = 16, kRoomParts = 512, kRoomRows = 1024;
+__global__ __launch_bounds__(64 * kRowWaves) void k_head_few_rows(RowArgs a) {
+    __shared__ Sums sums[kRowWaves];
+    __shared__ float group_most[64];
+    __shared__ int parts[kRoomParts], row_id[kRoomRows];
+    __shared__ float row_y[kRoomRows];
+    __shared__ int n_parts, n_rows;
+    const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
+    const int64_t token = blockIdx.x;
+    Sums mine = {-INFINITY, 0.f, 0.f};
+    float most = -INFINITY;
+    for (int p = threadIdx.x; p < a.n_parts; p += 64 * kRowWaves) {
+        const float4 v = a.parts[int64_t(p) * a.n + token];
+        mine = join(mine, Sums{v.x, v.y, v.z});
+        most = fmaxf(most, v.x);
+    }
+    mine = wave_join(mine, lane);
+    if (lane == 0) sums[wave] = mine;
+    if (a.top_k) {
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+        if ((lane & 15) == 0) group_most[wave * 4 + lane / 16] = most;
+        if (threadIdx.x == 0) n_parts = n_rows = 0;
+    }
+    __syncthreads();
+    mine = sums[0];
+    for (int k = 1; k < kRowWaves; ++k) mine = join(mine, sums[k]);
+    const Row r = finish_row(a, token, token_of(a.ids, token, a.rows), mine, threadIdx.x == 0);
     if (!a.top_k) return;
-    TopList top(a.top_k, lane);
-    if (t.live)
-        for (int k = 0; k < a.top_k; ++k) {
-            const int p = __shfl(parts.id, k, 64);
-            if (p == INT32_MAX) break;  // fewer parts than that
-            for (int r0 = 0; r0 < a.part_rows; r0 += 64) {
-                const int64_t row = int64_t(p) * a.part_rows + r0 + lane;
-                const bool in = r0 + lane < a.part_rows && row < a.rows;
-                top.offer(in ? a.logits[token * a.ldl + row] : 0.f, int(row), in);
+    if (!r.t.live) {
+        if (int(threadIdx.x) < a.top_k) put_top(a, token, r, threadIdx.x, 0.f, INT32_MAX);
+        return;
+    }
+    // the k-th largest of the groups' values, by each one's place among them
+    const float g = group_most[lane];
+    int place = 0;
+#pragma unroll 8
+    for (int k = 0; k < 64; ++k) place += TopList::before(TopList::read(g, k), k, g, lane);
+    const float least = TopList::read(g, __ffsll(static_cast<unsigned long long>(__ballot(place == a.top_k - 1))) - 1);
+    for (int p = threadIdx.x; p < a.n_parts; p += 64 * kRowWaves)
+        if (a.parts[int64_t(p) * a.n + token].x >= least) {
+            const int at = atomicAdd(&n_parts, 1);  // their order does not matter
+            if (at < kRoomParts) parts[at] = p;
+        }
+    __syncthreads();
+    const int total = n_parts * a.part_rows;
+    if (n_parts <= kRoomParts)
+        for (int i = threadIdx.x; i < total; i += 64 * kRowWaves) {
+            const int64_t row = int64_t(parts[i / a.part_rows]) * a.part_rows + i % a.part_rows;
+            const float y = row < a.rows ? a.logits[token * a.ldl + row] : 0.f;
+            if (row < a.rows && y >= least) {
+                const int at = atomicAdd(&n_rows, 1);
+                if (at < kRoomRows) {
+                    row_y[at] = y;
+                    row_id[at] = int(row);
+                }
             }
         }
-    if (lane < a.top_k) {
-        const int64_t at = token * a.top_k + lane;
-        const bool some = top.id != INT32_MAX;
-        a.top_ids[at] = some ? a.first_id + top.id : -1;
-        if (a.top_logits) a.top_logits[at] = top.v;
-        if (a.top_logp) a.top_logp[at] = some ? nat((top.v - mine.m) - ls) : -INFINITY;
+    __syncthreads();
+    if (n_parts > kRoomParts || n_rows > kRoomRows) {
+        if (wave == 0) top_by_lists(a, token, r, lane);
+        return;
     }
+    if (int(threadIdx.x) < n_rows) {
+        const float y = row_y[threadIdx.x];
+        const int id = row_id[threadIdx.x];
+        int before = 0;
+        for (int k = 0; k < n_rows; ++k) before += TopList::before(row_y[k], row_id[k], y, id);
+        if (before < a.top_k) put_top(a, token, r, before, y, id);
+    }
+    if (int(threadIdx.x) >= n_rows && int(threadIdx.x) < a.top_k) put_top(a, token, r, threadIdx.x, 0.f, INT32_MAX);
 }
 
 struct TotalArgs {
@@ -828,9 +938,19 @@ template <int D, int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
     using S = Shape<BT, 4>;
     __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
-    const int tiles = a.tp * a.tq, split = int(blockIdx.x) / tiles;
-    int ti, tj;
-    tile_of(int(blockIdx.x) - split * tiles, tiles, a.tp, a.tq, ti, tj);
+    // parts one after another on an XCD (block index mod 8), whose L2 the tiles of a part share
+    const int tiles = a.tp * a.tq;
+    int split = 0, ti, tj;
+    if (a.splits > 1) {
+        const int all = tiles * a.splits, per = (all + 7) / 8;
+        const int at = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
+        if (int(blockIdx.x >> 3) >= per || at >= all) return;
+        split = at / tiles;
+        ti = (at - split * tiles) % a.tp;
+        tj = (at - split * tiles) / a.tp;
+    } else {
+        tile_of(int(blockIdx.x), tiles, a.tp, a.tq, ti, tj);
+    }
     const int k0 = int(int64_t(a.stages) * split / a.splits), k1 = int(int64_t(a.stages) * (split + 1) / a.splits);
     f32x16_t acc[S::MM][S::MN];
     tile_loop<true, false, BT>(acc, a.table, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, k0, k1, lds);
@@ -1014,18 +1134,28 @@ int pick_tile(int64_t p, int64_t q) {
 }
 
 // Tile edge of dx, and the parts its contraction over the vocabulary is cut
-// into until the blocks fill the chip, each of at least 16 stages.
-int dx_tile(const mfsdp_entry& e, int64_t n) { return n <= 128 || e.cols <= 128 ? 128 : 256; }
+// into until the blocks fill the chip, each of at least 4 stages.  The larger
+// tile where it does not pad the result by more than a tenth over the smaller.
+int dx_tile(const mfsdp_entry& e, int64_t n) {
+    auto area = [&](int64_t t) { return double(ceil_div(e.cols, t) * t) * double(ceil_div(n, t) * t); };
+    return area(256) <= 1.1 * area(128) ? 256 : 128;
+}
 int dx_splits(const mfsdp_entry& e, int64_t n) {
     const int t = dx_tile(e, n);
     const int64_t tiles = ceil_div(e.cols, t) * ceil_div(n, t), slots = t == 256 ? kCusHead : 2 * kCusHead;
-    return int(std::clamp<int64_t>(slots / tiles, 1, std::max<int64_t>(1, ceil_div(e.rows, 64) / 16)));
+    return int(std::clamp<int64_t>(slots / tiles, 1, std::max<int64_t>(1, ceil_div(e.rows, 64) / 4)));
 }
+
+// Bytes from row to row of `cols` bf16 elements (a multiple of 64): an odd
+// number of 128-byte pieces, so that a stage's piece of 256 rows spreads over
+// the channels of the L2.
+int64_t odd_pitch(int64_t cols) { return (cols / 64 | 1) * kBlockBytes; }
 
 // How a batch of n tokens is laid out and cut over one entry.
 struct HeadShape {
     int x_planes, table_planes, dz_planes;
-    int64_t pitch;            // bytes of a packed row, in whole stages
+    int64_t pitch;            // bytes of a packed row, in whole stages and an odd number of 128-byte pieces
+    int64_t dz_pitch;         // likewise
     int stages;
     bool direct;              // the table is read where it lies
     int64_t np, vp;           // padded tokens and rows of the table
@@ -1045,7 +1175,7 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     s.table_planes = e.dtype == kBF16 ? 1 : 3;
     s.dz_planes = s.x_planes + s.table_planes > 2 ? 3 : 1;
     const int64_t kp = int64_t(align_up(uint64_t(e.cols), 64));
-    s.pitch = kp * 2;
+    s.pitch = odd_pitch(kp);
     s.stages = int(kp / 64);
     s.direct = s.table_planes == 1 && kp == e.cols;
     s.np = int64_t(align_up(uint64_t(n), kPadTokens));
@@ -1067,7 +1197,8 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     s.targets = region(uint64_t(s.np) * 4);
     if (grad) {
         s.rest = region(uint64_t(s.np) * 4);
-        s.dz_plane = uint64_t(s.np) * uint64_t(s.vp) * 2;
+        s.dz_pitch = odd_pitch(s.vp);
+        s.dz_plane = uint64_t(s.np) * uint64_t(s.dz_pitch);
         s.dz = region(uint64_t(s.dz_planes) * s.dz_plane);
         s.splits = dx_splits(e, n);
         s.tile_dw = pick_tile(e.rows, e.cols);
@@ -1195,9 +1326,9 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
         p.rest = reinterpret_cast<float*>(b.ws + s.rest);
     }
     launch_pack(p, b.x_type, b.stream);
-    const int blocks = int(s.pitch / kBlockBytes);
+    const int blocks = s.stages;  // of 128 bytes that hold columns
     a.x = Operand{p.dst, s.pitch, s.np, blocks, s.x_planes, p.plane};
-    a.table = Operand{b.table, s.pitch, e.rows, blocks, 1, 0};
+    a.table = Operand{b.table, e.cols * 2, e.rows, blocks, 1, 0};
     if (s.direct) return;
     p.src = b.table;
     p.dst = b.ws + s.table;
@@ -1213,11 +1344,15 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
 }
 
 template <int WD, int XD> void launch_few(const FewArgs& f, hipStream_t stream) {
-    const dim3 grid(uint32_t(ceil_div(f.l.rows, 32)));
+    // 64 rows a block where that leaves two blocks a CU: x is read half as often
+    const bool two = f.l.rows >= 64 * 2 * kCusHead;
+    const dim3 grid(uint32_t(ceil_div(f.l.rows, two ? 64 : 32)));
     if (f.l.n <= 32)
-        k_head_few<WD, XD, 1><<<grid, dim3(256), 0, stream>>>(f);
+        two ? k_head_few<WD, XD, 2, 1><<<grid, dim3(256), 0, stream>>>(f)
+            : k_head_few<WD, XD, 1, 1><<<grid, dim3(256), 0, stream>>>(f);
     else
-        k_head_few<WD, XD, 2><<<grid, dim3(256), 0, stream>>>(f);
+        two ? k_head_few<WD, XD, 2, 2><<<grid, dim3(256), 0, stream>>>(f)
+            : k_head_few<WD, XD, 1, 2><<<grid, dim3(256), 0, stream>>>(f);
 }
 
 hipError_t launch_logprob(const mfsdp_entry& e, const HeadShape& s, const Batch& b, RowArgs r) {
@@ -1248,9 +1383,9 @@ hipError_t launch_logprob(const mfsdp_entry& e, const HeadShape& s, const Batch&
     r.n_parts = int(s.n_parts);
     r.part_rows = s.part_rows;
     if (s.few)
-        k_head_rows<16><<<dim3(uint32_t(b.n)), dim3(1024), 0, b.stream>>>(r);
+        k_head_few_rows<<<dim3(uint32_t(b.n)), dim3(64 * kRowWaves), 0, b.stream>>>(r);
     else
-        k_head_rows<1><<<dim3(uint32_t(ceil_div(b.n, 4))), dim3(256), 0, b.stream>>>(r);
+        k_head_rows<<<dim3(uint32_t(ceil_div(b.n, 4))), dim3(256), 0, b.stream>>>(r);
     return hipGetLastError();
 }
 
@@ -1264,7 +1399,8 @@ struct GradOut {
 };
 
 template <int D> void launch_dx(const DxArgs& a, int tile, hipStream_t stream) {
-    const dim3 grid(uint32_t(a.tp) * uint32_t(a.tq) * uint32_t(a.splits));
+    const uint32_t blocks = uint32_t(a.tp) * uint32_t(a.tq) * uint32_t(a.splits);
+    const dim3 grid(a.splits > 1 ? uint32_t(align_up(blocks, 8)) : blocks);
     if (tile == 256)
         k_head_dx<D, 256><<<grid, dim3(256), 0, stream>>>(a);
     else
@@ -1289,7 +1425,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     d.dentropy = g.dentropy;
     d.scale = b.scale;
     d.dz = b.ws + s.dz;
-    d.pitch = s.vp * 2;
+    d.pitch = s.dz_pitch;
     d.planes = s.dz_planes;
     d.plane = int64_t(s.dz_plane);
     d.rest = reinterpret_cast<float*>(b.ws + s.rest);
