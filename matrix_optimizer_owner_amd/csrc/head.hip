@@ -827,7 +827,8 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
 // column c of the pass, its 16-byte words j at j ^ (c % 32).  fix(pass,
 // staging area) may change it (the block is in step before and after), then
 // before(c, r) and out(c, r, what before gave, four values) see the values of
-// tile rows r .. r+3 of tile column c, `before` some words ahead.
+// tile rows r .. r+3 of tile column c, `before` half a pass ahead, so that
+// what it loads is on its way together.
 template <int BT> struct Staging {
     static constexpr int PASSES = BT == 256 ? 2 : 1, COLS = BT / PASSES, BYTES = COLS * BT * 4;
     static_assert(BYTES <= Pipe<BT, 4>::BYTES, "staging area");
@@ -841,7 +842,7 @@ __device__ __forceinline__ void walk_columns(const f32x16_t (&acc)[BT / 64][BT /
                                              BEFORE&& before, OUT&& out) {
     using S = Shape<BT, 4>;
     using G = Staging<BT>;
-    constexpr int NCH = BT / 4, TURNS = G::COLS * NCH / 256, AHEAD = 8;
+    constexpr int NCH = BT / 4, TURNS = G::COLS * NCH / 256, AHEAD = TURNS / 2;
     static_assert(TURNS % AHEAD == 0, "walk");
     const G st = {reinterpret_cast<float*>(lds)};
     const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
@@ -881,24 +882,37 @@ __device__ __forceinline__ void walk_columns(const f32x16_t (&acc)[BT / 64][BT /
     }
 }
 
-// Four consecutive elements of a row from column c on, n of them inside; as
-// one vector where `vector` says that rows are aligned for it.
-template <int D> __device__ __forceinline__ float4 get4(const uint8_t* row, int c, int n, bool vector) {
-    if (n >= 4 && vector) {
-        if constexpr (D == kBF16) {
-            const uint2 r = *reinterpret_cast<const uint2*>(row + c * 2);
-            return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                               __uint_as_float(r.y & 0xffff0000u));
-        } else {
-            return *reinterpret_cast<const float4*>(row + c * 4);
+// Four consecutive elements of a row as they lie, from column c on, n of them
+// inside (the others 0); as one vector where `vector` says that rows are
+// aligned for it.
+template <int D> struct Four;
+template <> struct Four<kBF16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const uint8_t* row, int c, int n, bool vector) {
+        if (n >= 4 && vector) {
+            v = *reinterpret_cast<const uint2*>(row + c * 2);
+            return;
         }
+        const uint16_t* e = reinterpret_cast<const uint16_t*>(row) + c;
+        v = make_uint2((n > 0 ? e[0] : 0u) | (n > 1 ? uint32_t(e[1]) << 16 : 0u), (n > 2 ? e[2] : 0u) | (n > 3 ? uint32_t(e[3]) << 16 : 0u));
     }
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (k < n) v[k] = load_elem(row, D, c + k);
-    return make_float4(v[0], v[1], v[2], v[3]);
-}
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
+};
+template <> struct Four<kF32> {
+    float4 v;
+    __device__ __forceinline__ void load(const uint8_t* row, int c, int n, bool vector) {
+        if (n >= 4 && vector) {
+            v = *reinterpret_cast<const float4*>(row + c * 4);
+            return;
+        }
+        const float* e = reinterpret_cast<const float*>(row) + c;
+        v = make_float4(n > 0 ? e[0] : 0.f, n > 1 ? e[1] : 0.f, n > 2 ? e[2] : 0.f, n > 3 ? e[3] : 0.f);
+    }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
 template <int D> __device__ __forceinline__ void put4(uint8_t* row, int c, int n, bool vector, const float4& v) {
     if (n >= 4 && vector) {
         if constexpr (D == kBF16)
@@ -956,18 +970,18 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
     tile_loop<true, false, BT>(acc, a.table, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, k0, k1, lds);
     struct Extra {
         float rest;
-        float4 w;
+        Four<kBF16> w;
     };
     walk_columns<BT>(
         acc, lds, [](int, const Staging<BT>&) {},
         [&](int c, int r) {
             const int64_t token = int64_t(tj) * BT + c;
             const int col = ti * BT + r;
-            Extra x = {0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            Extra x = {};
             if (a.rest && split == 0 && token < a.n && col < a.cols) {
                 x.rest = a.rest[token];
                 const int t = a.targets[token];  // columns past the last are inside the row's pitch
-                if (t >= 0) x.w = get4<kBF16>(a.table.base + t * a.table.pitch, col, 4, true);
+                if (t >= 0) x.w.load(a.table.base + t * a.table.pitch, col, 4, true);
             }
             return x;
         },
@@ -975,7 +989,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
             const int64_t token = int64_t(tj) * BT + c;
             const int col = ti * BT + r;
             if (token >= a.n || col >= a.cols) return;
-            if (x.rest != 0.f) v = fma4(x.rest, x.w, v);
+            if (x.rest != 0.f) v = fma4(x.rest, x.w.get(), v);
             if (a.splits > 1) {
                 *reinterpret_cast<float4*>(a.sums + (split * a.n + token) * a.ld + col) = v;  // ld is a multiple of 4
             } else {
@@ -1047,16 +1061,31 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, uint8_t* lds, const S
         if (lane == 0) counts[wave] = uint32_t(found);
         __syncthreads();
         const int col = first_col + lane * 4;
+        const bool holds = lane * 4 < BT && col < a.cols;
         for (int w = 0; w < 4; ++w) {
-            const int count = int(counts[w]);
-            for (int e = 0; e < count; ++e) {
-                const uint32_t entry = list[w * PART + e];
-                const int c = int(entry >> 12);
-                if ((c & 3) != wave || lane * 4 >= BT || col >= a.cols) continue;
-                const int64_t token = at + int(entry & 4095);
-                const float4 x = get4<kBF16>(a.x.base + token * a.x.pitch, col, 4, true);
-                float4& v = st.word(c, lane);
-                v = fma4(a.rest[token], x, v);
+            const int count = uni(int(counts[w]));
+            for (int e0 = 0; e0 < count; e0 += 4) {  // four loads on their way
+                Four<kBF16> x[4];
+                float rest[4];
+                int c[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t entry = uint32_t(uni(int(list[w * PART + min(e0 + u, count - 1)])));
+                    const int64_t token = at + int(entry & 4095);
+                    c[u] = e0 + u < count && int(entry >> 12 & 3) == wave ? int(entry >> 12) : -1;
+                    x[u] = Four<kBF16>{};
+                    rest[u] = 0.f;
+                    if (c[u] >= 0 && holds) {
+                        x[u].load(a.x.base + token * a.x.pitch, col, 4, true);
+                        rest[u] = a.rest[token];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (c[u] >= 0 && holds) {
+                        float4& v = st.word(c[u], lane);
+                        v = fma4(rest[u], x[u].get(), v);
+                    }
             }
         }
         __syncthreads();  // the list and the counts are free again, the staged rows whole
@@ -1080,12 +1109,13 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
         },
         [&](int c, int r) {
             const int n = a.cols - (ti * BT + r);
-            return a.add && tj * BT + c < a.rows && n > 0 ? get4<D>(row_of(c), ti * BT + r, n, a.vector)
-                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            Four<D> old = {};
+            if (a.add && tj * BT + c < a.rows && n > 0) old.load(row_of(c), ti * BT + r, n, a.vector);
+            return old;
         },
-        [&](int c, int r, const float4& old, const float4& v) {
+        [&](int c, int r, const Four<D>& old, const float4& v) {
             const int n = a.cols - (ti * BT + r);
-            if (tj * BT + c < a.rows && n > 0) put4<D>(row_of(c), ti * BT + r, n, a.vector, a.add ? fma4(1.f, old, v) : v);
+            if (tj * BT + c < a.rows && n > 0) put4<D>(row_of(c), ti * BT + r, n, a.vector, a.add ? fma4(1.f, old.get(), v) : v);
         });
 }
 
@@ -1124,26 +1154,53 @@ constexpr int kCusHead = 256;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile edge of a product with p x q results: the time of its rounds, one block
-// a CU with 256-tiles, two with 128, in units of a 128-tile on a whole CU,
-// which does its work 15% slower than a 256-tile.
-int pick_tile(int64_t p, int64_t q) {
+// Tile edge of a product with p x q results over `stages` of the contraction.
+// Microseconds of a round: 256-tiles, one block a CU, 1.45 a stage and 10 for
+// what comes before and after the loop; 128-tiles, two blocks a CU, 1.03 a
+// stage, the rest hidden by the other block.  (50257 rows, 1024 tokens: 12
+// stages 101 us with 256-tiles, 83 with 128; 128256 rows, 4096 tokens: 64
+// stages 3270 and 4140.)
+int pick_tile(int64_t p, int64_t q, int stages) {
     const int64_t large = ceil_div(p, 256) * ceil_div(q, 256), small = ceil_div(p, 128) * ceil_div(q, 128);
-    const double tl = 4.0 * double(ceil_div(large, kCusHead)), ts = 2.0 * 1.15 * double(ceil_div(small, 2 * kCusHead));
-    return tl <= ts ? 256 : 128;
+    return double(ceil_div(large, kCusHead)) * (1.45 * stages + 10) <= double(ceil_div(small, 2 * kCusHead)) * (1.03 * stages + 2)
+               ? 256
+               : 128;
 }
 
 // Tile edge of dx, and the parts its contraction over the vocabulary is cut
-// into until the blocks fill the chip, each of at least 4 stages.  The larger
-// tile where it does not pad the result by more than a tenth over the smaller.
-int dx_tile(const mfsdp_entry& e, int64_t n) {
-    auto area = [&](int64_t t) { return double(ceil_div(e.cols, t) * t) * double(ceil_div(n, t) * t); };
-    return area(256) <= 1.1 * area(128) ? 256 : 128;
+// into, of at least 4 stages: the least of the rounds, as above, and what the
+// parts' sums cost, written and read at 4 TB/s.
+struct DxCut {
+    int tile, splits;
+};
+DxCut dx_cut(const mfsdp_entry& e, int64_t n, int runs) {
+    const int64_t stages = ceil_div(e.rows, 64);
+    DxCut best = {256, 1};
+    double least = INFINITY;
+    for (int t : {256, 128}) {
+        const int64_t tiles = ceil_div(e.cols, t) * ceil_div(n, t), slots = t == 256 ? kCusHead : 2 * kCusHead;
+        const int64_t most = std::clamp<int64_t>(slots / tiles, 1, std::max<int64_t>(1, stages / 4));
+        for (int64_t s = 1; s <= most; ++s) {
+            const double one = double(ceil_div(stages, s) * runs) * (t == 256 ? 1.45 : 1.03) + (t == 256 ? 25 : 10);
+            const double us = double(ceil_div(tiles * s, slots)) * one + (s > 1 ? 5 + double(s * n * e.cols) * 8 / 4e6 : 0);
+            if (us < least) {
+                least = us;
+                best = {t, int(s)};
+            }
+        }
+    }
+    return best;
 }
-int dx_splits(const mfsdp_entry& e, int64_t n) {
-    const int t = dx_tile(e, n);
-    const int64_t tiles = ceil_div(e.cols, t) * ceil_div(n, t), slots = t == 256 ? kCusHead : 2 * kCusHead;
-    return int(std::clamp<int64_t>(slots / tiles, 1, std::max<int64_t>(1, ceil_div(e.rows, 64) / 4)));
+// Rows of sums that dx_cut may ask for with up to n tokens: never falls as n grows.
+int64_t dx_sum_rows(const mfsdp_entry& e, int64_t n) {
+    const int64_t stages = ceil_div(e.rows, 64);
+    int64_t rows = 0;
+    for (int t : {256, 128}) {
+        const int64_t across = ceil_div(e.cols, t), slots = t == 256 ? kCusHead : 2 * kCusHead;
+        const int64_t most = std::min(slots / across, std::max<int64_t>(1, stages / 4));  // parts of one row of tiles
+        if (most > 1) rows = std::max(rows, std::min(most * n, slots / across * t));
+    }
+    return rows;
 }
 
 // Bytes from row to row of `cols` bf16 elements (a multiple of 64): an odd
@@ -1163,7 +1220,8 @@ struct HeadShape {
     int tile;                 // edge of the logits' tiles
     int part_rows;
     int64_t n_parts;
-    int tile_dw, splits;
+    int tile_dw;
+    DxCut dx;
     uint64_t x, table, parts, targets, logits, dz, rest, sums, total;
     uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane
 };
@@ -1181,7 +1239,8 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     s.np = int64_t(align_up(uint64_t(n), kPadTokens));
     s.vp = int64_t(align_up(uint64_t(e.rows), 256));
     s.few = !grad && n <= kFewTokens;
-    s.tile = pick_tile(e.rows, n);
+    const int pairs = s.x_planes * s.table_planes;
+    s.tile = pick_tile(e.rows, n, s.stages * (pairs == 9 ? 6 : pairs));
     s.part_rows = s.few ? 32 : s.tile / 2;
     s.n_parts = s.few ? ceil_div(e.rows, 32) : 2 * ceil_div(e.rows, s.tile);
     uint64_t off = 0;
@@ -1200,15 +1259,10 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
         s.dz_pitch = odd_pitch(s.vp);
         s.dz_plane = uint64_t(s.np) * uint64_t(s.dz_pitch);
         s.dz = region(uint64_t(s.dz_planes) * s.dz_plane);
-        s.splits = dx_splits(e, n);
-        s.tile_dw = pick_tile(e.rows, e.cols);
-        // a workspace for n tokens serves fewer of them, which may be cut into more parts
-        int64_t most = 0;
-        for (int64_t m = std::min<int64_t>(n, 2 * kCusHead * 256); m > 0; m = (m - 1) / 128 * 128) {
-            const int64_t splits = dx_splits(e, m);
-            if (splits > 1) most = std::max(most, splits * m);
-        }
-        s.sums = region(uint64_t(most) * align_up(uint64_t(e.cols), 4) * 4);
+        const int of_dx = s.dz_planes * s.table_planes, of_dw = s.dz_planes * s.x_planes;
+        s.dx = dx_cut(e, n, of_dx == 9 ? 6 : of_dx);
+        s.tile_dw = pick_tile(e.rows, e.cols, int(ceil_div(n, 64)) * (of_dw == 9 ? 6 : of_dw));
+        s.sums = region(uint64_t(dx_sum_rows(e, n)) * align_up(uint64_t(e.cols), 4) * 4);
     } else {
         // the most that either edge, or a smaller batch in another form, needs
         s.parts = region(16 * std::max(uint64_t(2 * ceil_div(e.rows, 128)) * uint64_t(n),
@@ -1441,7 +1495,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     const float* rest = s.dz_planes == 1 ? d.rest : nullptr;
     if (g.dx) {
         DxArgs a = {};
-        const int tile = dx_tile(e, b.n), xs = b.x_type == kBF16 ? 2 : 4;
+        const int tile = s.dx.tile, xs = b.x_type == kBF16 ? 2 : 4;
         a.table = d.l.table;
         a.dz = dz;
         a.n = b.n;
@@ -1450,7 +1504,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.tp = int(ceil_div(e.cols, tile));
         a.tq = int(ceil_div(b.n, tile));
         a.stages = int(ceil_div(e.rows, 64));
-        a.splits = s.splits;
+        a.splits = s.dx.splits;
         a.ids = b.ids;
         a.targets = targets;
         a.rest = rest;
