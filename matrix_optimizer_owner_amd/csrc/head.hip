@@ -69,9 +69,10 @@ struct PackArgs {
     uint8_t* dst;
     int64_t stride;     // elements of src from row to row
     int64_t rows;       // of src
-    int64_t pitch;      // bytes of dst from row to row, a multiple of 128
+    int64_t block;      // bytes of dst from column block to column block, whose rows are 128 bytes apart
     int64_t plane;      // bytes of dst from plane to plane
-    int64_t words;      // 16-byte words of a plane of dst from the first on, over all its rows
+    int64_t words;      // 16-byte words of a plane of dst, over all its rows
+    int per_row;        // of a row
     int cols;
     int vector;         // src rows are 16-byte aligned
     Ids ids;            // rows with a negative id become zeros
@@ -104,9 +105,8 @@ template <int D>
 __global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a) {
     const int64_t w = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
     if (w >= a.words) return;
-    const int per_row = int(a.pitch / 16);
-    const int64_t row = w / per_row;
-    const int c = int(w % per_row) * 8;
+    const int64_t row = w / a.per_row;
+    const int g = int(w % a.per_row), c = g * 8;
     const Token t = row < a.rows ? token_of(a.ids, row, a.table_rows) : Token{-1, false};
     if (a.targets && c == 0) {
         a.targets[row] = t.target;
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a) {
     }
     const bool in = t.live && c < a.cols;
     const uint8_t* src = a.src + row * a.stride * (D == kBF16 ? 2 : 4);
-    uint8_t* dst = a.dst + w * 16;
+    uint8_t* dst = a.dst + int64_t(g >> 3) * a.block + row * 128 + (g & 7) * 16;
     if constexpr (D == kBF16) {
         u32x4_t v = {0u, 0u, 0u, 0u};
         if (in && a.vector && c + 8 <= a.cols) {
@@ -150,6 +150,35 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < 3; ++j) *reinterpret_cast<u32x4_t*>(dst + j * a.plane) = o[j];
+    }
+}
+
+// The packed batch turned over, a plane's 64 x 64 elements a block: rows are
+// its columns, contiguous along the tokens.
+struct TurnArgs {
+    const uint8_t* src;
+    uint8_t* dst;
+    int64_t src_block, dst_block, src_plane, dst_plane;
+};
+__global__ __launch_bounds__(256) void k_head_turn(TurnArgs a) {
+    __shared__ uint16_t t[64][66];
+    const uint8_t* src = a.src + blockIdx.z * a.src_plane + blockIdx.y * a.src_block + int64_t(blockIdx.x) * 8192;
+    uint8_t* dst = a.dst + blockIdx.z * a.dst_plane + blockIdx.x * a.dst_block + int64_t(blockIdx.y) * 8192;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = int(threadIdx.x) + i * 256, row = k >> 3, g = k & 7;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src + k * 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[g * 8 + e][row] = uint16_t(v[e >> 1] >> (16 * (e & 1)));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = int(threadIdx.x) + i * 256, row = k >> 3, g = k & 7;
+        u32x4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = uint32_t(t[row][g * 8 + 2 * e]) | uint32_t(t[row][g * 8 + 2 * e + 1]) << 16;
+        *reinterpret_cast<u32x4_t*>(dst + k * 16) = v;
     }
 }
 
@@ -726,8 +755,8 @@ struct DzArgs {
     const mfsdp_head_record* records;
     const float *dlogp, *dentropy;
     float scale;
-    uint8_t* dz;       // [plane][tokens, whole tiles][rows, whole tiles] bf16
-    int64_t pitch;     // bytes from token to token
+    uint8_t* dz;       // [plane][64 rows of the table][tokens, whole tiles][64] bf16
+    int64_t block;     // bytes from 64 rows to the next 64
     int planes;
     int64_t plane;
     float* rest;       // [n]: what rounding took from the target's dz (one plane)
@@ -812,11 +841,11 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
                 }
         }
         __syncthreads();
-        uint8_t* to = d.dz + plane * d.plane + int64_t(tj) * BT * d.pitch + int64_t(ti) * RB;
+        uint8_t* to = d.dz + plane * d.plane + int64_t(ti) * (BT / 64) * d.block + int64_t(tj) * BT * 128;
 #pragma unroll 8
         for (int i = 0; i < BT * GPR / 256; ++i) {
-            const int k = int(threadIdx.x) + i * 256, r = k / GPR, j = k % GPR;
-            *reinterpret_cast<u32x4_t*>(to + r * d.pitch + j * 16) =
+            const int k = int(threadIdx.x) + i * 256, b = k / (BT * 8), r = k / 8 % BT, j = b * 8 + k % 8;
+            *reinterpret_cast<u32x4_t*>(to + b * d.block + (k % (BT * 8)) * 16) =
                 *reinterpret_cast<const u32x4_t*>(lds + r * RB + (j ^ (r & (GPR - 1))) * 16);
         }
     }
@@ -980,8 +1009,8 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
             Extra x = {};
             if (a.rest && split == 0 && token < a.n && col < a.cols) {
                 x.rest = a.rest[token];
-                const int t = a.targets[token];  // columns past the last are inside the row's pitch
-                if (t >= 0) x.w.load(a.table.base + t * a.table.pitch, col, 4, true);
+                const int t = a.targets[token];  // columns past the last are inside their block
+                if (t >= 0) x.w.load(a.table.at(t, col), 0, 4, true);
             }
             return x;
         },
@@ -1014,7 +1043,8 @@ __global__ __launch_bounds__(256) void k_head_dx_sum(DxArgs a) {
 }
 
 struct DwArgs {
-    Operand x, dz;
+    Operand turned, dz;  // x with its columns as rows
+    Operand x;
     int64_t n;
     int rows, cols;
     int tp, tq;          // tiles along the columns and the vocabulary
@@ -1076,7 +1106,7 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, uint8_t* lds, const S
                     x[u] = Four<kBF16>{};
                     rest[u] = 0.f;
                     if (c[u] >= 0 && holds) {
-                        x[u].load(a.x.base + token * a.x.pitch, col, 4, true);
+                        x[u].load(a.x.at(token, col), 0, 4, true);
                         rest[u] = a.rest[token];
                     }
                 }
@@ -1092,7 +1122,8 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, uint8_t* lds, const S
     }
 }
 
-// dW = dz^T x: both operands K-major (their rows are the contraction).
+// dW = dz^T x: P is x turned over, Q is dz, read K-major (its rows are the
+// contraction).
 template <int D, int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     using S = Shape<BT, 4>;
@@ -1100,7 +1131,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     int ti, tj;
     tile_of(int(blockIdx.x), a.tp * a.tq, a.tp, a.tq, ti, tj);
     f32x16_t acc[S::MM][S::MN];
-    tile_loop<true, true, BT>(acc, a.x, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
+    tile_loop<false, true, BT>(acc, a.turned, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
     auto row_of = [&](int c) { return a.grad + (int64_t(tj) * BT + c) * a.cols * (D == kBF16 ? 2 : 4); };
     walk_columns<BT>(
         acc, lds,
@@ -1203,17 +1234,10 @@ int64_t dx_sum_rows(const mfsdp_entry& e, int64_t n) {
     return rows;
 }
 
-// Bytes from row to row of `cols` bf16 elements (a multiple of 64): an odd
-// number of 128-byte pieces, so that a stage's piece of 256 rows spreads over
-// the channels of the L2.
-int64_t odd_pitch(int64_t cols) { return (cols / 64 | 1) * kBlockBytes; }
-
 // How a batch of n tokens is laid out and cut over one entry.
 struct HeadShape {
     int x_planes, table_planes, dz_planes;
-    int64_t pitch;            // bytes of a packed row, in whole stages and an odd number of 128-byte pieces
-    int64_t dz_pitch;         // likewise
-    int stages;
+    int stages;               // 128-byte column blocks of a row of x or the table
     bool direct;              // the table is read where it lies
     int64_t np, vp;           // padded tokens and rows of the table
     bool few;
@@ -1222,8 +1246,8 @@ struct HeadShape {
     int64_t n_parts;
     int tile_dw;
     DxCut dx;
-    uint64_t x, table, parts, targets, logits, dz, rest, sums, total;
-    uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane
+    uint64_t x, turned, table, parts, targets, logits, dz, rest, sums, total;
+    uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane (turned over: as x)
 };
 
 HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, bool grad) {
@@ -1233,7 +1257,6 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     s.table_planes = e.dtype == kBF16 ? 1 : 3;
     s.dz_planes = s.x_planes + s.table_planes > 2 ? 3 : 1;
     const int64_t kp = int64_t(align_up(uint64_t(e.cols), 64));
-    s.pitch = odd_pitch(kp);
     s.stages = int(kp / 64);
     s.direct = s.table_planes == 1 && kp == e.cols;
     s.np = int64_t(align_up(uint64_t(n), kPadTokens));
@@ -1249,15 +1272,15 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
         off = align_up(off + bytes, kAlign);
         return at;
     };
-    s.x_plane = uint64_t(s.np) * uint64_t(s.pitch);
-    s.table_plane = uint64_t(e.rows) * uint64_t(s.pitch);
+    s.x_plane = uint64_t(s.np) * uint64_t(kp) * 2;
+    s.table_plane = uint64_t(e.rows) * uint64_t(kp) * 2;
     s.x = region(uint64_t(s.x_planes) * s.x_plane);
     s.table = region(s.direct ? 0 : uint64_t(s.table_planes) * s.table_plane);
     s.targets = region(uint64_t(s.np) * 4);
     if (grad) {
         s.rest = region(uint64_t(s.np) * 4);
-        s.dz_pitch = odd_pitch(s.vp);
-        s.dz_plane = uint64_t(s.np) * uint64_t(s.dz_pitch);
+        s.turned = region(uint64_t(s.x_planes) * s.x_plane);
+        s.dz_plane = uint64_t(s.np) * uint64_t(s.vp) * 2;
         s.dz = region(uint64_t(s.dz_planes) * s.dz_plane);
         const int of_dx = s.dz_planes * s.table_planes, of_dw = s.dz_planes * s.x_planes;
         s.dx = dx_cut(e, n, of_dx == 9 ? 6 : of_dx);
@@ -1316,13 +1339,13 @@ mfsdp_status check_space(const void* workspace, uint64_t have, uint64_t need) {
 void launch_pack(const PackArgs& a, int src_type, hipStream_t stream) {
     // a launch has fewer than 2^32 threads: whole rows each
     constexpr int64_t kMost = ((int64_t(1) << 32) / kPackThreads - 1) * kPackThreads;
-    const int64_t per_row = a.pitch / 16, chunk = kMost / per_row * per_row;
+    const int64_t per_row = a.per_row, chunk = kMost / per_row * per_row;
     for (int64_t w = 0; w < a.words; w += chunk) {
         PackArgs b = a;
         const int64_t row = w / per_row;
         b.words = std::min(chunk, a.words - w);
         b.src = a.src + row * a.stride * (src_type == kBF16 ? 2 : 4);
-        b.dst = a.dst + w * 16;
+        b.dst = a.dst + row * 128;
         b.rows = std::max<int64_t>(0, a.rows - row);
         if (a.ids.ids) b.ids.ids = static_cast<const uint8_t*>(a.ids.ids) + row * (a.ids.type == MFSDP_I64 ? 8 : 4);
         if (a.targets) {
@@ -1368,9 +1391,10 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
     p.dst = b.ws + s.x;
     p.stride = b.stride;
     p.rows = b.n;
-    p.pitch = s.pitch;
+    p.block = s.np * 128;
     p.plane = int64_t(s.x_plane);
-    p.words = s.np * (s.pitch / 16);
+    p.per_row = s.stages * 8;
+    p.words = s.np * p.per_row;
     p.cols = int(e.cols);
     p.vector = !misaligned(b.x, 16) && b.stride * (b.x_type == kBF16 ? 2 : 4) % 16 == 0;
     p.ids = b.ids;
@@ -1380,21 +1404,21 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
         p.rest = reinterpret_cast<float*>(b.ws + s.rest);
     }
     launch_pack(p, b.x_type, b.stream);
-    const int blocks = s.stages;  // of 128 bytes that hold columns
-    a.x = Operand{p.dst, s.pitch, s.np, blocks, s.x_planes, p.plane};
-    a.table = Operand{b.table, e.cols * 2, e.rows, blocks, 1, 0};
+    a.x = Operand{p.dst, 128, p.block, s.np, s.stages, s.x_planes, p.plane};
+    a.table = Operand{b.table, e.cols * 2, 128, e.rows, s.stages, 1, 0};
     if (s.direct) return;
     p.src = b.table;
     p.dst = b.ws + s.table;
     p.stride = e.cols;
     p.rows = e.rows;
+    p.block = e.rows * 128;
     p.plane = int64_t(s.table_plane);
-    p.words = e.rows * (s.pitch / 16);
+    p.words = e.rows * p.per_row;
     p.vector = e.cols * (e.dtype == kBF16 ? 2 : 4) % 16 == 0;
     p.ids = Ids{};
     p.targets = nullptr;
     launch_pack(p, e.dtype, b.stream);
-    a.table = Operand{p.dst, s.pitch, e.rows, blocks, s.table_planes, p.plane};
+    a.table = Operand{p.dst, 128, p.block, e.rows, s.stages, s.table_planes, p.plane};
 }
 
 template <int WD, int XD> void launch_few(const FewArgs& f, hipStream_t stream) {
@@ -1479,7 +1503,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     d.dentropy = g.dentropy;
     d.scale = b.scale;
     d.dz = b.ws + s.dz;
-    d.pitch = s.dz_pitch;
+    d.block = s.np * 128;
     d.planes = s.dz_planes;
     d.plane = int64_t(s.dz_plane);
     d.rest = reinterpret_cast<float*>(b.ws + s.rest);
@@ -1489,8 +1513,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     else
         k_head_dz<128><<<grid, dim3(256), 0, b.stream>>>(d);
     // tokens and vocabulary rows that dz was written for
-    const Operand dz = {d.dz, d.pitch, int64_t(d.l.tq) * s.tile, int(int64_t(d.l.tp) * s.tile * 2 / kBlockBytes), s.dz_planes,
-                        d.plane};
+    const Operand dz = {d.dz, 128, d.block, int64_t(d.l.tq) * s.tile, d.l.tp * (s.tile / 64), s.dz_planes, d.plane};
     const int* targets = reinterpret_cast<const int*>(b.ws + s.targets);
     const float* rest = s.dz_planes == 1 ? d.rest : nullptr;
     if (g.dx) {
@@ -1517,6 +1540,10 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     }
     if (g.grad) {
         DwArgs a = {};
+        const int64_t kp = int64_t(s.stages) * 64;
+        const TurnArgs t = {d.l.x.base, b.ws + s.turned, d.l.x.block, kp * 128, d.l.x.plane, d.l.x.plane};
+        k_head_turn<<<dim3(uint32_t(s.np / 64), uint32_t(s.stages), uint32_t(s.x_planes)), dim3(256), 0, b.stream>>>(t);
+        a.turned = Operand{t.dst, 128, t.dst_block, kp, int(s.np / 64), s.x_planes, t.dst_plane};
         a.x = d.l.x;
         a.dz = dz;
         a.n = b.n;

@@ -8,7 +8,11 @@
 // Both reach LDS by direct global->LDS loads of 16 bytes a lane into rings of
 // stage slots, 3 for P and 2 for Q, whose rows are 128 bytes, swizzled on the
 // global side; K-major is read back with the transposing LDS read.  Rows are
-// 16-byte aligned and their pitch is a multiple of 128 bytes.  Nothing past an
+// 16-byte aligned.  In a plain matrix the 128-byte column blocks of a row follow
+// one another; in one made for this loop each column block is a matrix of its
+// own, its rows 128 bytes apart, so that a stage is one piece of memory (a
+// K-major one 4 or 2), and a tile's stages do not sweep over the pages of the
+// whole matrix.  Nothing past an
 // operand's last row or last 128-byte column block is read: a load that would
 // lie there reads the last one instead, and what it brings has to be
 // multiplied by zeros (contraction) or left out (tile rows).
@@ -31,10 +35,15 @@ namespace {
 struct Operand {
     const uint8_t* base;
     int64_t pitch;    // bytes from one row to the next
+    int64_t block;    // bytes from one 128-byte column block of a row to the next
     int64_t rows;     // rows that may be read
-    int blocks;       // K-major: 128-byte column blocks that may be read
+    int blocks;       // column blocks that may be read
     int planes;       // 1 or 3
     int64_t plane;    // bytes from one plane to the next
+    // element (row, col), inside plane 0
+    __device__ __forceinline__ const uint8_t* at(int64_t row, int col) const {
+        return base + row * pitch + int64_t(col >> 6) * block + (col & 63) * 2;
+    }
 };
 
 // The runs over the contraction: (plane of P, plane of Q) of each, 4 bits.
@@ -79,19 +88,19 @@ struct StageLoads {
     __device__ __forceinline__ void set(const Operand& o, const Runs& runs, int64_t row0, int k0, int lane, int wave) {
         if constexpr (KM) {
             step = int64_t(KST) * o.pitch;
-            base = o.base + k0 * step;
+            const int block0 = int(row0 / 64);
+            base = o.base + k0 * step + block0 * o.block;
             const int last = int(o.rows % KST);
             ragged = last ? int(o.rows / KST) : -1;
-            const int block0 = int(row0 / 64);
 #pragma unroll
             for (int i = 0; i < LP; ++i) {
                 const int r = (i * 4 + wave) * 8 + (lane >> 3), blk = r / KST, k = r % KST;
-                const uint32_t col = uint32_t(min(block0 + blk, o.blocks - 1)) * 128u + uint32_t(swz_k(r, lane & 7)) * 16u;
+                const uint32_t col = uint32_t(min(blk, o.blocks - 1 - block0)) * uint32_t(o.block) + uint32_t(swz_k(r, lane & 7)) * 16u;
                 off[i] = uint32_t(k) * uint32_t(o.pitch) + col;
                 back[i] = last && k >= last ? -int32_t(uint32_t(k - (last - 1)) * uint32_t(o.pitch)) : 0;
             }
         } else {
-            step = PP::KSB;
+            step = o.block;
             base = o.base + row0 * o.pitch + k0 * step;
             ragged = -1;
             const int last = int(min(o.rows - row0, int64_t(BT))) - 1;
