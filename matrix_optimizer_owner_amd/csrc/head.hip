@@ -855,9 +855,12 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
 // LDS in passes of BT*BT*4 / 128 KB, where row c of the staging area is tile
 // column c of the pass, its 16-byte words j at j ^ (c % 32).  fix(pass,
 // staging area) may change it (the block is in step before and after), then
-// before(c, r) and out(c, r, what before gave, four values) see the values of
-// tile rows r .. r+3 of tile column c, `before` half a pass ahead, so that
-// what it loads is on its way together.
+// before(c, r) and out(c, r, what before gave, eight values) see the values of
+// tile rows r .. r+7 of tile column c, `before` of a whole pass ahead of its
+// staging, so that what it loads is on its way meanwhile.
+struct Values {
+    float4 a, b;
+};
 template <int BT> struct Staging {
     static constexpr int PASSES = BT == 256 ? 2 : 1, COLS = BT / PASSES, BYTES = COLS * BT * 4;
     static_assert(BYTES <= Pipe<BT, 4>::BYTES, "staging area");
@@ -866,19 +869,25 @@ template <int BT> struct Staging {
         return *reinterpret_cast<float4*>(at + c * BT + ((j ^ (c & 31)) * 4));
     }
 };
+// (Barriers of LDS accesses alone, so that a pass does not wait for the stores
+// of the one before it.)
 template <int BT, typename FIX, typename BEFORE, typename OUT>
 __device__ __forceinline__ void walk_columns(const f32x16_t (&acc)[BT / 64][BT / 64], uint8_t* lds, FIX&& fix,
                                              BEFORE&& before, OUT&& out) {
     using S = Shape<BT, 4>;
     using G = Staging<BT>;
-    constexpr int NCH = BT / 4, TURNS = G::COLS * NCH / 256, AHEAD = TURNS / 2;
-    static_assert(TURNS % AHEAD == 0, "walk");
+    constexpr int NCH = BT / 8, TURNS = G::COLS * NCH / 256;
+    constexpr int STEP = 256 / NCH;  // columns from turn to turn
+    const int c0 = int(threadIdx.x) / NCH, r = int(threadIdx.x) % NCH * 8;
     const G st = {reinterpret_cast<float*>(lds)};
     const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
     const int wm = wave >> 1, wn = wave & 1, frow = lane & 31, fhalf = lane >> 5;
-    __syncthreads();  // every wave is done with the operands' stages
+    stage_barrier();  // every wave is done with the operands' stages
 #pragma unroll
     for (int h = 0; h < G::PASSES; ++h) {
+        decltype(before(0, 0)) early[TURNS];
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) early[i] = before(h * G::COLS + c0 + i * STEP, r);
         if (G::PASSES == 1 || wn == h) {
 #pragma unroll
             for (int mi = 0; mi < S::MM; ++mi)
@@ -892,72 +901,81 @@ __device__ __forceinline__ void walk_columns(const f32x16_t (&acc)[BT / 64][BT /
                         st.word(cl, rl >> 2) = make_float4(v[q * 4], v[q * 4 + 1], v[q * 4 + 2], v[q * 4 + 3]);
                     }
         }
-        __syncthreads();
+        stage_barrier();
         fix(h, st);
-        for (int i0 = 0; i0 < TURNS; i0 += AHEAD) {
-            decltype(before(0, 0)) early[AHEAD];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int k = int(threadIdx.x) + (i0 + i) * 256;
-                early[i] = before(h * G::COLS + k / NCH, k % NCH * 4);
-            }
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int k = int(threadIdx.x) + (i0 + i) * 256;
-                out(h * G::COLS + k / NCH, k % NCH * 4, early[i], st.word(k / NCH, k % NCH));
-            }
+        for (int i = 0; i < TURNS; ++i) {
+            const int c = c0 + i * STEP;
+            out(h * G::COLS + c, r, early[i], Values{st.word(c, r / 4), st.word(c, r / 4 + 1)});
         }
-        __syncthreads();
+        if (h + 1 < G::PASSES) stage_barrier();
     }
 }
 
-// Four consecutive elements of a row as they lie, from column c on, n of them
-// inside (the others 0); as one vector where `vector` says that rows are
-// aligned for it.
-template <int D> struct Four;
-template <> struct Four<kBF16> {
-    uint2 v;
+// Eight consecutive elements of a row as they lie, from column c on, n of them
+// inside (the others 0); as whole vectors where `vector` says that rows are
+// aligned for it.  Stores go past the caches.
+template <int D> struct Eight;
+template <> struct Eight<kBF16> {
+    u32x4_t v;
     __device__ __forceinline__ void load(const uint8_t* row, int c, int n, bool vector) {
-        if (n >= 4 && vector) {
-            v = *reinterpret_cast<const uint2*>(row + c * 2);
+        if (n >= 8 && vector) {
+            v = *reinterpret_cast<const u32x4_t*>(row + c * 2);
             return;
         }
         const uint16_t* e = reinterpret_cast<const uint16_t*>(row) + c;
-        v = make_uint2((n > 0 ? e[0] : 0u) | (n > 1 ? uint32_t(e[1]) << 16 : 0u), (n > 2 ? e[2] : 0u) | (n > 3 ? uint32_t(e[3]) << 16 : 0u));
+        v = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < n) v[k >> 1] |= uint32_t(e[k]) << (16 * (k & 1));
     }
-    __device__ __forceinline__ float4 get() const {
-        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                           __uint_as_float(v.y & 0xffff0000u));
+    __device__ __forceinline__ Values get() const {
+        auto lo = [&](int k) { return __uint_as_float(v[k] << 16); };
+        auto hi = [&](int k) { return __uint_as_float(v[k] & 0xffff0000u); };
+        return Values{make_float4(lo(0), hi(0), lo(1), hi(1)), make_float4(lo(2), hi(2), lo(3), hi(3))};
+    }
+    static __device__ __forceinline__ void store(uint8_t* row, int c, const Values& x) {
+        __builtin_nontemporal_store(u32x4_t{pack_bf16x2(x.a.x, x.a.y), pack_bf16x2(x.a.z, x.a.w), pack_bf16x2(x.b.x, x.b.y),
+                                            pack_bf16x2(x.b.z, x.b.w)},
+                                    reinterpret_cast<u32x4_t*>(row + c * 2));
     }
 };
-template <> struct Four<kF32> {
-    float4 v;
+template <> struct Eight<kF32> {
+    Values v;
     __device__ __forceinline__ void load(const uint8_t* row, int c, int n, bool vector) {
-        if (n >= 4 && vector) {
-            v = *reinterpret_cast<const float4*>(row + c * 4);
+        const float* e = reinterpret_cast<const float*>(row) + c;
+        if (n >= 8 && vector) {
+            v = Values{reinterpret_cast<const float4*>(e)[0], reinterpret_cast<const float4*>(e)[1]};
             return;
         }
-        const float* e = reinterpret_cast<const float*>(row) + c;
-        v = make_float4(n > 0 ? e[0] : 0.f, n > 1 ? e[1] : 0.f, n > 2 ? e[2] : 0.f, n > 3 ? e[3] : 0.f);
-    }
-    __device__ __forceinline__ float4 get() const { return v; }
-};
-template <int D> __device__ __forceinline__ void put4(uint8_t* row, int c, int n, bool vector, const float4& v) {
-    if (n >= 4 && vector) {
-        if constexpr (D == kBF16)
-            *reinterpret_cast<uint2*>(row + c * 2) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        else
-            *reinterpret_cast<float4*>(row + c * 4) = v;
-    } else {
-        const float e[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k) x[k] = k < n ? e[k] : 0.f;
+        v = Values{make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7])};
+    }
+    __device__ __forceinline__ Values get() const { return v; }
+    static __device__ __forceinline__ void store(uint8_t* row, int c, const Values& x) {
+        f32x4_t* p = reinterpret_cast<f32x4_t*>(row + c * 4);
+        __builtin_nontemporal_store(f32x4_t{x.a.x, x.a.y, x.a.z, x.a.w}, p);
+        __builtin_nontemporal_store(f32x4_t{x.b.x, x.b.y, x.b.z, x.b.w}, p + 1);
+    }
+};
+template <int D> __device__ __forceinline__ void put8(uint8_t* row, int c, int n, bool vector, const Values& v) {
+    if (n >= 8 && vector) {
+        Eight<D>::store(row, c, v);
+    } else {
+        const float e[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
             if (k < n) store_elem(row, D, c + k, e[k]);
     }
 }
 __device__ __forceinline__ float4 fma4(float f, const float4& a, const float4& b) {
     return make_float4(__builtin_fmaf(f, a.x, b.x), __builtin_fmaf(f, a.y, b.y), __builtin_fmaf(f, a.z, b.z),
                        __builtin_fmaf(f, a.w, b.w));
+}
+__device__ __forceinline__ Values fma8(float f, const Values& x, const Values& y) {
+    return Values{fma4(f, x.a, y.a), fma4(f, x.b, y.b)};
 }
 
 struct DxArgs {
@@ -972,7 +990,7 @@ struct DxArgs {
     uint8_t* dx;
     int64_t stride;
     int vector;
-    float* sums;          // splits > 1: [split][n][ld]
+    float* sums;          // splits > 1: [split][n][ld], ld a multiple of 8
     int64_t ld;
 };
 
@@ -999,7 +1017,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
     tile_loop<true, false, BT>(acc, a.table, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, k0, k1, lds);
     struct Extra {
         float rest;
-        Four<kBF16> w;
+        Eight<kBF16> w;
     };
     walk_columns<BT>(
         acc, lds, [](int, const Staging<BT>&) {},
@@ -1010,20 +1028,22 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
             if (a.rest && split == 0 && token < a.n && col < a.cols) {
                 x.rest = a.rest[token];
                 const int t = a.targets[token];  // columns past the last are inside their block
-                if (t >= 0) x.w.load(a.table.at(t, col), 0, 4, true);
+                if (t >= 0) x.w.load(a.table.at(t, col), 0, 8, true);
             }
             return x;
         },
-        [&](int c, int r, const Extra& x, float4 v) {
+        [&](int c, int r, const Extra& x, Values v) {
             const int64_t token = int64_t(tj) * BT + c;
             const int col = ti * BT + r;
             if (token >= a.n || col >= a.cols) return;
-            if (x.rest != 0.f) v = fma4(x.rest, x.w.get(), v);
+            if (x.rest != 0.f) v = fma8(x.rest, x.w.get(), v);
             if (a.splits > 1) {
-                *reinterpret_cast<float4*>(a.sums + (split * a.n + token) * a.ld + col) = v;  // ld is a multiple of 4
+                float4* to = reinterpret_cast<float4*>(a.sums + (split * a.n + token) * a.ld + col);  // ld: of 8
+                to[0] = v.a;
+                to[1] = v.b;
             } else {
-                if (!token_of(a.ids, token, a.rows).live) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                put4<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
+                if (!token_of(a.ids, token, a.rows).live) v = Values{};
+                put8<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
             }
         });
 }
@@ -1031,15 +1051,18 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
 // The parts of dx added in their order.
 template <int D>
 __global__ __launch_bounds__(256) void k_head_dx_sum(DxArgs a) {
-    const int64_t w = int64_t(blockIdx.x) * 256 + threadIdx.x, per = a.ld / 4;
+    const int64_t w = int64_t(blockIdx.x) * 256 + threadIdx.x, per = a.ld / 8;
     const int64_t token = w / per;
-    const int col = int(w % per) * 4;
+    const int col = int(w % per) * 8;
     if (token >= a.n || col >= a.cols) return;
-    f32x4_t v = {};
+    Values v = {};
 #pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) v += *reinterpret_cast<const f32x4_t*>(a.sums + (s * a.n + token) * a.ld + col);
-    if (!token_of(a.ids, token, a.rows).live) v = f32x4_t{};
-    put4<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, make_float4(v[0], v[1], v[2], v[3]));
+    for (int s = 0; s < a.splits; ++s) {
+        const float4* from = reinterpret_cast<const float4*>(a.sums + (s * a.n + token) * a.ld + col);
+        v = fma8(1.f, Values{from[0], from[1]}, v);
+    }
+    if (!token_of(a.ids, token, a.rows).live) v = Values{};
+    put8<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
 }
 
 struct DwArgs {
@@ -1049,77 +1072,95 @@ struct DwArgs {
     int rows, cols;
     int tp, tq;          // tiles along the columns and the vocabulary
     int stages;          // of the contraction over the batch
-    const int* targets;
+    const int* starts;   // of k_head_lists
+    const uint32_t* list;
     const float* rest;   // NULL, or the rests of the targets' dz (x then has one plane)
     uint8_t* grad;
     int vector;
     int add;
 };
 
-// What rounding took from the targets' dz, times x, added to the staged rows
-// of the table's gradient.  The block looks through the targets 2048 at a time
-// for rows of its pass, each wave through a quarter of them, and lists them in
-// order; then the wave that a row falls to (row mod 4) adds its entries in the
-// lists' order, so sums do not depend on timing.
-constexpr int kListTokens = 2048;
-template <int BT>
-__device__ __forceinline__ void add_rests(const DwArgs& a, uint8_t* lds, const Staging<BT>& st, int first_row, int first_col) {
-    constexpr int PART = kListTokens / 4;
-    static_assert(Staging<BT>::BYTES + kListTokens * 4 + 16 <= Pipe<BT, 4>::BYTES, "list area");
-    uint32_t* list = reinterpret_cast<uint32_t*>(lds + Staging<BT>::BYTES);
-    uint32_t* counts = list + kListTokens;
-    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
-    for (int64_t at = 0; at < a.n; at += kListTokens) {
-        const int64_t mine = at + wave * PART;
-        int target[PART / 64];
-#pragma unroll
-        for (int i = 0; i < PART / 64; ++i) {
-            const int64_t token = mine + i * 64 + lane;
-            target[i] = token < a.n ? a.targets[token] : -1;
-        }
-        int found = 0;
-#pragma unroll
-        for (int i = 0; i < PART / 64; ++i) {
-            const int c = target[i] - first_row;
-            const bool hit = target[i] >= 0 && c >= 0 && c < Staging<BT>::COLS;
-            const uint64_t mask = __ballot(hit);
-            if (hit)
-                list[wave * PART + found + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
-                    uint32_t(c) << 12 | uint32_t(wave * PART + i * 64 + lane);
-            found += __popcll(mask);
-        }
-        if (lane == 0) counts[wave] = uint32_t(found);
+// The tokens whose target lies in each group of 128 rows of the table, in
+// order: list[starts[g]] .. list[starts[g + 1] - 1], each the row in its group
+// << 24 | the token (at most 2^22 of them).  A block a group looks through all
+// targets: once for those of the groups before, whose number is the list's
+// start, and once for its own.
+constexpr int kListRows = 128;
+struct ListArgs {
+    const int* targets;
+    int n, rows;
+    int* starts;
+    uint32_t* list;
+};
+__global__ __launch_bounds__(256) void k_head_lists(ListArgs a) {
+    __shared__ int counts[4];
+    const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
+    const int first = int(blockIdx.x) * kListRows;
+    int below = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < a.n; i += 256) below += uint32_t(a.targets[i]) < uint32_t(first);
+    for (int off = 1; off < 64; off <<= 1) below += __shfl_xor(below, off, 64);
+    if (lane == 0) counts[wave] = below;
+    __syncthreads();
+    int at = counts[0] + counts[1] + counts[2] + counts[3];
+    if (threadIdx.x == 0) a.starts[blockIdx.x] = at;
+    if (first >= a.rows) return;  // the block past the last group: its start is the last one's end
+    for (int i0 = 0; i0 < a.n; i0 += 256) {
+        const int i = i0 + int(threadIdx.x);
+        const uint32_t c = i < a.n ? uint32_t(a.targets[i] - first) : ~0u;  // no target: -1 - first
+        const bool hit = c < uint32_t(kListRows);
+        const uint64_t mask = __ballot(hit);
         __syncthreads();
-        const int col = first_col + lane * 4;
-        const bool holds = lane * 4 < BT && col < a.cols;
-        for (int w = 0; w < 4; ++w) {
-            const int count = uni(int(counts[w]));
-            for (int e0 = 0; e0 < count; e0 += 4) {  // four loads on their way
-                Four<kBF16> x[4];
-                float rest[4];
-                int c[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t entry = uint32_t(uni(int(list[w * PART + min(e0 + u, count - 1)])));
-                    const int64_t token = at + int(entry & 4095);
-                    c[u] = e0 + u < count && int(entry >> 12 & 3) == wave ? int(entry >> 12) : -1;
-                    x[u] = Four<kBF16>{};
-                    rest[u] = 0.f;
-                    if (c[u] >= 0 && holds) {
-                        x[u].load(a.x.at(token, col), 0, 4, true);
-                        rest[u] = a.rest[token];
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (c[u] >= 0 && holds) {
-                        float4& v = st.word(c[u], lane);
-                        v = fma4(rest[u], x[u].get(), v);
-                    }
-            }
-        }
-        __syncthreads();  // the list and the counts are free again, the staged rows whole
+        if (lane == 0) counts[wave] = __popcll(mask);
+        __syncthreads();
+        int before = at;
+        for (int w = 0; w < wave; ++w) before += counts[w];
+        if (hit) a.list[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] = c << 24 | uint32_t(i);
+        at += counts[0] + counts[1] + counts[2] + counts[3];
     }
+}
+
+// What rounding took from the targets' dz, times x, added to the staged rows
+// of the table's gradient: the wave that a row falls to (row mod 4) adds its
+// entries in the list's order, so sums do not depend on timing.
+template <int BT>
+__device__ __forceinline__ void add_rests(const DwArgs& a, const Staging<BT>& st, int first, int end, int first_col) {
+    static_assert(Staging<BT>::COLS == kListRows, "a pass is a group");
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    const int col = first_col + lane * 4;
+    const bool holds = lane * 4 < BT && col < a.cols;
+    for (int e0 = first; e0 < end; e0 += 64) {
+        const uint32_t mine = e0 + lane < end ? a.list[e0 + lane] : 0u;
+        uint64_t own = __ballot(e0 + lane < end && int(mine >> 24 & 3) == wave);
+        while (own) {  // eight entries' loads on their way: text has rows with hundreds of tokens
+            constexpr int N = 8;
+            uint2 x[N];
+            float rest[N];
+            int c[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                c[u] = -1;
+                x[u] = make_uint2(0u, 0u);
+                rest[u] = 0.f;
+                if (own) {
+                    const uint32_t entry = __builtin_amdgcn_readlane(mine, __ffsll(static_cast<unsigned long long>(own)) - 1);
+                    own &= own - 1;
+                    const int64_t token = entry & 0xffffff;
+                    c[u] = int(entry >> 24);
+                    if (holds) x[u] = *reinterpret_cast<const uint2*>(a.x.at(token, col));
+                    rest[u] = a.rest[token];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (c[u] >= 0 && holds) {
+                    float4& v = st.word(c[u], lane);
+                    v = fma4(rest[u], make_float4(__uint_as_float(x[u].x << 16), __uint_as_float(x[u].x & 0xffff0000u),
+                                                  __uint_as_float(x[u].y << 16), __uint_as_float(x[u].y & 0xffff0000u)), v);
+                }
+        }
+    }
+    stage_barrier();  // the staged rows are whole
 }
 
 // dW = dz^T x: P is x turned over, Q is dz, read K-major (its rows are the
@@ -1130,23 +1171,28 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
     int ti, tj;
     tile_of(int(blockIdx.x), a.tp * a.tq, a.tp, a.tq, ti, tj);
+    int starts[Staging<BT>::PASSES + 1] = {};
+    if (a.rest)
+#pragma unroll
+        for (int h = 0; h <= Staging<BT>::PASSES; ++h)
+            starts[h] = uni(a.starts[min(tj * Staging<BT>::PASSES + h, (a.rows + kListRows - 1) / kListRows)]);
     f32x16_t acc[S::MM][S::MN];
     tile_loop<false, true, BT>(acc, a.turned, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
-    auto row_of = [&](int c) { return a.grad + (int64_t(tj) * BT + c) * a.cols * (D == kBF16 ? 2 : 4); };
+    const int left = a.cols - ti * BT, under = a.rows - tj * BT;  // columns and rows from the tile's first on
+    const uint32_t pitch = uint32_t(a.cols) * (D == kBF16 ? 2 : 4);  // at most 2^22
+    uint8_t* to = a.grad + int64_t(tj) * BT * pitch + int64_t(ti) * BT * (D == kBF16 ? 2 : 4);
     walk_columns<BT>(
         acc, lds,
         [&](int h, const Staging<BT>& st) {
-            if (a.rest) add_rests<BT>(a, lds, st, tj * BT + h * Staging<BT>::COLS, ti * BT);
+            if (a.rest) add_rests<BT>(a, st, starts[h], starts[h + 1], ti * BT);
         },
         [&](int c, int r) {
-            const int n = a.cols - (ti * BT + r);
-            Four<D> old = {};
-            if (a.add && tj * BT + c < a.rows && n > 0) old.load(row_of(c), ti * BT + r, n, a.vector);
+            Eight<D> old = {};
+            if (a.add && c < under && r < left) old.load(to + uint32_t(c) * pitch, r, left - r, a.vector);
             return old;
         },
-        [&](int c, int r, const Four<D>& old, const float4& v) {
-            const int n = a.cols - (ti * BT + r);
-            if (tj * BT + c < a.rows && n > 0) put4<D>(row_of(c), ti * BT + r, n, a.vector, a.add ? fma4(1.f, old.get(), v) : v);
+        [&](int c, int r, const Eight<D>& old, const Values& v) {
+            if (c < under && r < left) put8<D>(to + uint32_t(c) * pitch, r, left - r, a.vector, a.add ? fma8(1.f, old.get(), v) : v);
         });
 }
 
@@ -1246,7 +1292,7 @@ struct HeadShape {
     int64_t n_parts;
     int tile_dw;
     DxCut dx;
-    uint64_t x, turned, table, parts, targets, logits, dz, rest, sums, total;
+    uint64_t x, turned, table, parts, targets, logits, dz, rest, starts, list, sums, total;
     uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane (turned over: as x)
 };
 
@@ -1279,13 +1325,15 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     s.targets = region(uint64_t(s.np) * 4);
     if (grad) {
         s.rest = region(uint64_t(s.np) * 4);
+        s.starts = region(uint64_t(ceil_div(e.rows, kListRows) + 1) * 4);
+        s.list = region(uint64_t(s.np) * 4);
         s.turned = region(uint64_t(s.x_planes) * s.x_plane);
         s.dz_plane = uint64_t(s.np) * uint64_t(s.vp) * 2;
         s.dz = region(uint64_t(s.dz_planes) * s.dz_plane);
         const int of_dx = s.dz_planes * s.table_planes, of_dw = s.dz_planes * s.x_planes;
         s.dx = dx_cut(e, n, of_dx == 9 ? 6 : of_dx);
         s.tile_dw = pick_tile(e.rows, e.cols, int(ceil_div(n, 64)) * (of_dw == 9 ? 6 : of_dw));
-        s.sums = region(uint64_t(dx_sum_rows(e, n)) * align_up(uint64_t(e.cols), 4) * 4);
+        s.sums = region(uint64_t(dx_sum_rows(e, n)) * align_up(uint64_t(e.cols), 8) * 4);
     } else {
         // the most that either edge, or a smaller batch in another form, needs
         s.parts = region(16 * std::max(uint64_t(2 * ceil_div(e.rows, 128)) * uint64_t(n),
@@ -1483,7 +1531,7 @@ template <int D> void launch_dx(const DxArgs& a, int tile, hipStream_t stream) {
         k_head_dx<D, 256><<<grid, dim3(256), 0, stream>>>(a);
     else
         k_head_dx<D, 128><<<grid, dim3(256), 0, stream>>>(a);
-    if (a.splits > 1) k_head_dx_sum<D><<<dim3(uint32_t(ceil_div(a.n * (a.ld / 4), 256))), dim3(256), 0, stream>>>(a);
+    if (a.splits > 1) k_head_dx_sum<D><<<dim3(uint32_t(ceil_div(a.n * (a.ld / 8), 256))), dim3(256), 0, stream>>>(a);
 }
 
 template <int D> void launch_dw(const DwArgs& a, int tile, hipStream_t stream) {
@@ -1533,9 +1581,9 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.rest = rest;
         a.dx = g.dx;
         a.stride = g.dx_stride;
-        a.vector = !misaligned(g.dx, uintptr_t(4 * xs)) && g.dx_stride % 4 == 0;
+        a.vector = !misaligned(g.dx, 16) && g.dx_stride * xs % 16 == 0;
         a.sums = reinterpret_cast<float*>(b.ws + s.sums);
-        a.ld = int64_t(align_up(uint64_t(e.cols), 4));
+        a.ld = int64_t(align_up(uint64_t(e.cols), 8));
         b.x_type == kBF16 ? launch_dx<kBF16>(a, tile, b.stream) : launch_dx<kF32>(a, tile, b.stream);
     }
     if (g.grad) {
@@ -1552,10 +1600,16 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.tp = int(ceil_div(e.cols, s.tile_dw));
         a.tq = int(ceil_div(e.rows, s.tile_dw));
         a.stages = int(ceil_div(b.n, 64));
-        a.targets = targets;
+        a.starts = reinterpret_cast<int*>(b.ws + s.starts);
+        a.list = reinterpret_cast<uint32_t*>(b.ws + s.list);
         a.rest = rest;
+        if (rest) {
+            const ListArgs l = {targets, int(b.n), int(e.rows), reinterpret_cast<int*>(b.ws + s.starts),
+                                reinterpret_cast<uint32_t*>(b.ws + s.list)};
+            k_head_lists<<<dim3(uint32_t(ceil_div(e.rows, kListRows) + 1)), dim3(256), 0, b.stream>>>(l);
+        }
         a.grad = g.grad;
-        a.vector = e.cols % 4 == 0;  // the entry is 16-byte aligned
+        a.vector = e.cols * (e.dtype == kBF16 ? 2 : 4) % 16 == 0;  // the entry is 16-byte aligned
         a.add = g.add;
         e.dtype == kBF16 ? launch_dw<kBF16>(a, s.tile_dw, b.stream) : launch_dw<kF32>(a, s.tile_dw, b.stream);
     }
