@@ -125,49 +125,69 @@ __device__ __forceinline__ Scale group_scale(const float (&x)[kPer]) {
     most = group_max(most);
     Scale s;
     s.value = most < 0x7f800000u ? __uint_as_float(most) : __uint_as_float(0x7fc00000u);
-    s.pre = s.value > 0x1p100f ? 0x1p-30f : s.value < 0x1p-90f ? 0x1p60f : 1.f;
+    s.pre = s.value > 0x1p100f ? 0x1p-30f : s.value < 0x1p-90f && s.value > 0.f ? 0x1p60f : 1.f;
     const float v = s.value * s.pre;
     s.inv = v > 0.f ? __builtin_amdgcn_rcpf(v) : 0.f;
     return s;
 }
 
-// Code of one magnitude, not yet a whole number; u: what is added before it is
-// rounded down.
-__device__ __forceinline__ float code_of(float x, const Scale& s, float count, float u) {
-    const float share = fabsf(x) * s.pre * s.inv;
-    return fminf(__builtin_fmaf(__builtin_amdgcn_sqrtf(share), count, u), count);
+// Code of a magnitude in bits 8 and up.  DITHER: floor(256 * count * sqrt(|x| /
+// value) + 1/2) + byte, whose 256th part rounded down is the code with the
+// dither (byte + 1/2) / 256; else without the 1/2, so that byte 128 gives the
+// nearest code.  The root is at most 1 + 2^-22: no code exceeds count.
+// PRE: the scale's pre is not 1 somewhere in the wave.
+template <bool DITHER, bool PRE>
+__device__ __forceinline__ uint32_t code_of(float x, const Scale& s, float count, uint32_t byte) {
+    const float share = PRE ? fabsf(x) * s.pre * s.inv : fabsf(x) * s.inv;
+    return uint32_t(__builtin_fmaf(__builtin_amdgcn_sqrtf(share), 256.f * count, DITHER ? 0.5f : 0.f)) + byte;
 }
 
-__device__ __forceinline__ u32x2_t pack_first(const float (&m)[kPer], const Scale& s, const float (&u)[kPer]) {
-    uint32_t w[2] = {0u, 0u};
+// Both moments' codes; word: the dither's 32 bits of elements 2j and 2j + 1.
+struct Packed {
+    u32x2_t first, root;
+};
+template <bool DITHER, bool PRE>
+__device__ __forceinline__ Packed pack_codes(const float (&m)[kPer], const Scale& sm, const float (&r)[kPer], const Scale& sr,
+                                             const uint32_t (&word)[kPer / 2]) {
+    Packed p;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int c = int(code_of(m[k], s, 127.f, u[k]));
-        w[k >> 2] |= (uint32_t(m[k] < 0.f ? -c : c) & 0xffu) << (8 * (k & 3));
-    }
-    return u32x2_t{w[0], w[1]};
-}
-__device__ __forceinline__ u32x2_t pack_root(const float (&r)[kPer], const Scale& s, const float (&u)[kPer]) {
-    uint32_t w[2] = {0u, 0u};
+    for (int h = 0; h < 2; ++h) {
+        uint32_t c[4], d[4];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const uint32_t d = uint32_t(code_of(r[k], s, 255.f, u[k]));
-        w[k >> 2] |= max(d, r[k] > 0.f ? 1u : 0u) << (8 * (k & 3));
+        for (int j = 0; j < 4; ++j) {
+            const int k = h * 4 + j;
+            const uint32_t w = word[k / 2];
+            const int sign = __float_as_int(m[k]) >> 31;
+            const uint32_t v = code_of<DITHER, PRE>(m[k], sm, 127.f, (w >> (16 * (k & 1))) & 0xff);
+            c[j] = uint32_t((int(v >> 8 & 0xff) ^ sign) - sign);
+            d[j] = max(code_of<DITHER, PRE>(r[k], sr, 255.f, (w >> (16 * (k & 1) + 8)) & 0xff), r[k] > 0.f ? 256u : 0u);
+        }
+        p.first[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400), __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400), 0x05040100);
+        p.root[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(d[3], d[2], 0x0c0c0501), __builtin_amdgcn_perm(d[1], d[0], 0x0c0c0501), 0x05040100);
     }
-    return u32x2_t{w[0], w[1]};
+    return p;
 }
-__device__ __forceinline__ void unpack_first(u32x2_t w, float scale, float (&m)[kPer]) {
+template <bool DITHER>
+__device__ __forceinline__ Packed pack(const float (&m)[kPer], const Scale& sm, const float (&r)[kPer], const Scale& sr,
+                                       const uint32_t (&word)[kPer / 2]) {
+    if (__any(sm.pre != 1.f || sr.pre != 1.f)) return pack_codes<DITHER, true>(m, sm, r, sr, word);
+    return pack_codes<DITHER, false>(m, sm, r, sr, word);
+}
+// EXACT: the group's largest value is its scale, bit for bit; else within half a step of fp32
+template <bool EXACT> __device__ __forceinline__ void unpack_first(u32x2_t w, float scale, float (&m)[kPer]) {
+    const float unit = scale * (1.f / 16129.f);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const float c = float(int8_t(w[k >> 2] >> (8 * (k & 3))));
-        m[k] = c * fabsf(c) * (1.f / 16129.f) * scale;  // 16129 * fl(1/16129) rounds to 1
+        m[k] = EXACT ? c * fabsf(c) * (1.f / 16129.f) * scale : c * fabsf(c) * unit;  // 16129 * fl(1/16129) rounds to 1
     }
 }
-__device__ __forceinline__ void unpack_root(u32x2_t w, float scale, float (&r)[kPer]) {
+template <bool EXACT> __device__ __forceinline__ void unpack_root(u32x2_t w, float scale, float (&r)[kPer]) {
+    const float unit = scale * (1.f / 65025.f);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const float d = float(uint8_t(w[k >> 2] >> (8 * (k & 3))));
-        r[k] = d * d * (1.f / 65025.f) * scale;
+        r[k] = EXACT ? d * d * (1.f / 65025.f) * scale : d * d * unit;
     }
 }
 
@@ -200,8 +220,8 @@ struct Adam8Args {
 // One chunk of a tensor by a block, 8 consecutive elements a thread, a group
 // by 16 lanes; every lane takes part in its group's reduction, with zeros
 // behind the tensor's end.  Codes behind the end are written as zeros, inside
-// the tensor's own code bytes.
-template <int D, bool SCALED>
+// the tensor's own code bytes.  WHOLE: the chunk has no such end.
+template <int D, bool SCALED, bool WHOLE>
 __device__ __forceinline__ void step_chunk(const Adam8Args& a, const TailDesc& t, int64_t begin) {
     float gs = 1.f;
     if constexpr (SCALED) gs = *a.gscale;
@@ -209,50 +229,58 @@ __device__ __forceinline__ void step_chunk(const Adam8Args& a, const TailDesc& t
     const uint8_t* g = a.grads + t.param_off;
     const Place pm = place(a.state, t.m1_off, t.numel), pr = place(a.state, t.m2_off, t.numel);
     const int64_t i = begin + int64_t(threadIdx.x) * kPer;
-    const int n = int(min(max(t.numel - i, int64_t(0)), int64_t(kPer)));
+    const int n = WHOLE ? kPer : int(min(max(t.numel - i, int64_t(0)), int64_t(kPer)));
     float gv[kPer] = {}, wv[kPer] = {}, m[kPer] = {}, r[kPer] = {};
     if (n > 0) {
         load_n<D>(g, i, n, gv);
         load_n<D>(w, i, n, wv);
         const u32x2_t cm = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pm.codes + i));
         const u32x2_t cr = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pr.codes + i));
-        unpack_first(cm, pm.scales[i / kGroup], m);
-        unpack_root(cr, pr.scales[i / kGroup], r);
+        unpack_first<false>(cm, pm.scales[i / kGroup], m);
+        unpack_root<false>(cr, pr.scales[i / kGroup], r);
+    }
+    // behind the end g, m and r are zeros (codes there are written as zeros; the state is zero-filled at first)
+    uint32_t least = ~0u;  // of the magnitudes that are not zero, as a bit pattern less 1
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        if constexpr (SCALED) gv[k] *= gs;
+        if (!WHOLE && k >= n) m[k] = r[k] = 0.f;
+        m[k] = __builtin_fmaf(a.b1, m[k], a.omb1 * gv[k]);
+        least = min(least, __float_as_uint(fmaxf(r[k], fabsf(gv[k]))) - 1);
+    }
+    if (__any(least < __float_as_uint(0x1p-40f) - 1)) {
+        // small values are squared at 2^64 times their size: no square is lost to the fp32 range
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const bool small = fmaxf(r[k], fabsf(gv[k])) < 0x1p-40f;
+            const float up = small ? 0x1p64f : 1.f, rk = r[k] * up, gk = gv[k] * up;
+            r[k] = __builtin_amdgcn_sqrtf(__builtin_fmaf(a.b2, rk * rk, a.omb2 * (gk * gk))) * (small ? 0x1p-64f : 1.f);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            r[k] = __builtin_amdgcn_sqrtf(__builtin_fmaf(a.b2, r[k] * r[k], a.omb2 * (gv[k] * gv[k])));
     }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        float gk = gv[k];
-        if constexpr (SCALED) gk *= gs;
-        // behind the end g, m and r are zeros (codes there are written as zeros; the state is zero-filled at first)
-        m[k] = k < n ? __builtin_fmaf(a.b1, m[k], a.omb1 * gk) : 0.f;
-        // small values are squared at 2^64 times their size: no square is lost to the fp32 range
-        const bool small = fmaxf(r[k], fabsf(gk)) < 0x1p-40f;
-        const float up = small ? 0x1p64f : 1.f, rk = r[k] * up;
-        gk *= up;
-        const float v = k < n ? __builtin_fmaf(a.b2, rk * rk, a.omb2 * (gk * gk)) : 0.f;
-        r[k] = __builtin_amdgcn_sqrtf(v) * (small ? 0x1p-64f : 1.f);
         // sqrt and reciprocal to 1 ulp each: 2e-7 of an update that is rounded with the parameter
         const float upd = m[k] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[k], a.root_bc2, a.eps));
         wv[k] = __builtin_fmaf(-a.lr_bc1, upd, __builtin_fmaf(-a.lrwd, wv[k], wv[k]));
     }
     const Scale sm = group_scale(m), sr = group_scale(r);
-    if (n <= 0) return;
-    store_n<D>(w, i, n, wv);
     // one hashed word for two elements, a byte for each of their codes
     const uint32_t key = mix(a.step + 0x9e3779b9u * uint32_t(t.entry + 1));
-    float um[kPer], ur[kPer];
+    uint32_t word[kPer / 2];
 #pragma unroll
-    for (int k = 0; k < kPer; k += 2) {
-        const uint64_t pair = uint64_t(i + k) >> 1;
-        const uint32_t h = mix(uint32_t(pair) + uint32_t(pair >> 32) * 0x9e3779b9u + key);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            um[k + e] = __builtin_fmaf(float(uint8_t(h >> (16 * e))), 1.f / 256.f, 1.f / 512.f);
-            ur[k + e] = __builtin_fmaf(float(uint8_t(h >> (16 * e + 8))), 1.f / 256.f, 1.f / 512.f);
-        }
+    for (int j = 0; j < kPer / 2; ++j) {
+        const uint64_t pair = uint64_t(i) / 2 + j;
+        word[j] = mix(uint32_t(pair) + uint32_t(pair >> 32) * 0x9e3779b9u + key);
     }
-    __builtin_nontemporal_store(pack_first(m, sm, um), reinterpret_cast<u32x2_t*>(pm.codes + i));
-    __builtin_nontemporal_store(pack_root(r, sr, ur), reinterpret_cast<u32x2_t*>(pr.codes + i));
+    const Packed p = pack<true>(m, sm, r, sr, word);
+    if (n <= 0) return;
+    store_n<D>(w, i, n, wv);
+    __builtin_nontemporal_store(p.first, reinterpret_cast<u32x2_t*>(pm.codes + i));
+    __builtin_nontemporal_store(p.root, reinterpret_cast<u32x2_t*>(pr.codes + i));
     if (threadIdx.x % kLanes == 0) {
         pm.scales[i / kGroup] = sm.value;
         pr.scales[i / kGroup] = sr.value;
@@ -265,10 +293,11 @@ __global__ __launch_bounds__(kThreads) void k_adamw8(Adam8Args a) {
     const int ti = upper_index(a.tail_begin, a.n_tail, chunk);
     const TailDesc t = a.tails[ti];
     const int64_t begin = int64_t(chunk - a.tail_begin[ti]) * kTailChunk;
+    const bool whole = begin + kTailChunk <= t.numel;
     if (t.dtype == kBF16)
-        step_chunk<kBF16, SCALED>(a, t, begin);
+        whole ? step_chunk<kBF16, SCALED, true>(a, t, begin) : step_chunk<kBF16, SCALED, false>(a, t, begin);
     else
-        step_chunk<kF32, SCALED>(a, t, begin);
+        whole ? step_chunk<kF32, SCALED, true>(a, t, begin) : step_chunk<kF32, SCALED, false>(a, t, begin);
 }
 
 // ---- moments as values ----
@@ -293,8 +322,8 @@ __global__ __launch_bounds__(kThreads) void k_moments_read(MomentArgs a) {
         const Place pm = place(a.state, a.m1_off, a.numel), pr = place(a.state, a.m2_off, a.numel);
         const u32x2_t cm = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pm.codes + i));
         const u32x2_t cr = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pr.codes + i));
-        unpack_first(cm, pm.scales[i / kGroup], m);
-        unpack_root(cr, pr.scales[i / kGroup], v);
+        unpack_first<true>(cm, pm.scales[i / kGroup], m);
+        unpack_root<true>(cr, pr.scales[i / kGroup], v);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] *= v[k];
     } else {
@@ -316,16 +345,14 @@ __global__ __launch_bounds__(kThreads) void k_moments_write(MomentArgs a) {
     }
     if constexpr (CODES) {
         const Place pm = place(a.state, a.m1_off, a.numel), pr = place(a.state, a.m2_off, a.numel);
-        float half[kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            v[k] = sqrtf(v[k]);  // correctly rounded: the root of a square is the value again
-            half[k] = 0.5f;  // to nearest
-        }
+        for (int k = 0; k < kPer; ++k) v[k] = sqrtf(v[k]);  // correctly rounded: the root of a square is the value again
         const Scale sm = group_scale(m), sr = group_scale(v);
+        const uint32_t half[kPer / 2] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+        const Packed p = pack<false>(m, sm, v, sr, half);
         if (n <= 0) return;
-        __builtin_nontemporal_store(pack_first(m, sm, half), reinterpret_cast<u32x2_t*>(pm.codes + i));
-        __builtin_nontemporal_store(pack_root(v, sr, half), reinterpret_cast<u32x2_t*>(pr.codes + i));
+        __builtin_nontemporal_store(p.first, reinterpret_cast<u32x2_t*>(pm.codes + i));
+        __builtin_nontemporal_store(p.root, reinterpret_cast<u32x2_t*>(pr.codes + i));
         if (threadIdx.x % kLanes == 0) {
             pm.scales[i / kGroup] = sm.value;
             pr.scales[i / kGroup] = sr.value;
