@@ -41,6 +41,7 @@ constexpr int kMaxTop = 64;             // a list of alternatives is one lane an
 constexpr int kPackThreads = 256;
 constexpr int kPadTokens = 256;         // rows of the packed batch: a multiple of both tile edges
 constexpr int64_t kFewTokens = 64;      // batches up to this are read straight from x and the table
+constexpr int64_t kCacheBytes = int64_t(256) << 20;  // the Infinity Cache
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -209,8 +210,7 @@ struct LogitArgs {
     Ids ids;
     float4* parts;       // [part][n]: M, S, W of a token over BT/2 rows of the table
     float* targets;      // [n]: y of the target, written where it is here
-    float* logits;       // NULL, or [n][ldl]: y
-    int64_t ldl;
+    float* logits;       // NULL, or [part][n][rows of a part]: y
 };
 
 // f(MFMA row tile, accumulator, row) for the rows of a wave's block that a
@@ -258,13 +258,13 @@ __device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_
             });
     }
     if (a.logits && in) {
-        float* to = a.logits + token * a.ldl + row0;
+        float* to = a.logits + (part * a.n + token) * (MM * 32);
 #pragma unroll
         for (int mi = 0; mi < MM; ++mi)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int r = mi * 32 + q * 8 + fhalf * 4;
-                if (!RAGGED || r < held)  // up to three values past the table's end, inside ldl
+                if (!RAGGED || r < held)  // up to three values past the table's end, inside the part
                     *reinterpret_cast<float4*>(to + r) =
                         make_float4(acc[mi][q * 4], acc[mi][q * 4 + 1], acc[mi][q * 4 + 2], acc[mi][q * 4 + 3]);
             }
@@ -317,16 +317,16 @@ struct FewArgs {
 
 // The 16 bytes of T (bf16 or fp32) that elements k .. of a row make, the row in
 // type D and at any address; zeros past the last column.  INSIDE: there are none.
-template <typename T, int D, bool INSIDE> __device__ __forceinline__ u32x4_t granule(const uint8_t* row, int k, int cols) {
+template <typename T, int D, bool INSIDE, bool PAST> __device__ __forceinline__ u32x4_t granule(const uint8_t* row, int k, int cols) {
     constexpr int N = 16 / int(sizeof(T));
     u32x4_t v = {0u, 0u, 0u, 0u};
     if (INSIDE || k + N <= cols) {
         if constexpr (D == kF32) {
             typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(4)));
-            v = *reinterpret_cast<const word_t*>(row + 4 * k);
+            v = PAST ? __builtin_nontemporal_load(reinterpret_cast<const word_t*>(row + 4 * k)) : *reinterpret_cast<const word_t*>(row + 4 * k);
         } else if constexpr (sizeof(T) == 2) {
             typedef unsigned int word_t __attribute__((ext_vector_type(4), aligned(2)));
-            v = *reinterpret_cast<const word_t*>(row + 2 * k);
+            v = PAST ? __builtin_nontemporal_load(reinterpret_cast<const word_t*>(row + 2 * k)) : *reinterpret_cast<const word_t*>(row + 2 * k);
         } else {
             typedef unsigned int word_t __attribute__((ext_vector_type(2), aligned(2)));
             const word_t r = *reinterpret_cast<const word_t*>(row + 2 * k);
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(256) void k_head_few(FewArgs f) {
     using T = std::conditional_t<WD == kBF16 && XD == kBF16, uint16_t, float>;
     constexpr int LINE = 128 / int(sizeof(T)), GE = 16 / int(sizeof(T));  // elements of a line and a granule
     constexpr int ROWS = (RB + NB) * 32;                                   // LDS rows of a wave's tile
-    constexpr int AHEAD = RB + NB == 2 ? 4 : 2;                            // lines loaded at once
+    constexpr int AHEAD = RB + NB == 2 ? 4 : 2;                            // lines on their way
     constexpr int TILE = 4 * ROWS * 128, SUMS = 4 * RB * NB * 16 * 64 * 4;
     const LogitArgs& a = f.l;
     __shared__ __attribute__((aligned(16))) uint8_t lds[TILE > SUMS ? TILE : SUMS];
@@ -383,48 +383,61 @@ __global__ __launch_bounds__(256) void k_head_few(FewArgs f) {
     for (int i = 0; i < NB * 4; ++i) x[i] = f.x + min(int64_t(i * 8 + (lane >> 3)), a.n - 1) * f.x_pitch;
     f32x16_t acc[RB][NB] = {};
     const int lines = (f.cols + LINE - 1) / LINE, mine = (lane & 7) * GE;
-    // L lines from `line` on, four apart
-    auto run = [&](int line, auto COUNT, auto INSIDE) {
-        constexpr int L = decltype(COUNT)::value;
-        u32x4_t ew[L][RB * 4], ex[L][NB * 4];
-#pragma unroll
-        for (int l = 0; l < L; ++l) {
-            const int k = (line + 4 * l) * LINE + mine;
-#pragma unroll
-            for (int i = 0; i < RB * 4; ++i) ew[l][i] = granule<T, WD, decltype(INSIDE)::value>(w[i], k, f.cols);
-#pragma unroll
-            for (int i = 0; i < NB * 4; ++i) ex[l][i] = granule<T, XD, decltype(INSIDE)::value>(x[i], k, f.cols);
-        }
-#pragma unroll
-        for (int l = 0; l < L; ++l) {
-#pragma unroll
-            for (int i = 0; i < (RB + NB) * 4; ++i) {
-                const int r = i * 8 + (lane >> 3);
-                *reinterpret_cast<u32x4_t*>(tile + r * 128 + swz_r<8>(r, lane & 7) * 16) = i < RB * 4 ? ew[l][i] : ex[l][i - RB * 4];
-            }
-            wave_exchange();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                u32x4_t fr[RB + NB];
-#pragma unroll
-                for (int j = 0; j < RB + NB; ++j) {
-                    const int r = j * 32 + frow;
-                    fr[j] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + swz_r<8>(r, 2 * kk + fhalf) * 16);
-                }
-#pragma unroll
-                for (int i = 0; i < RB; ++i)
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) Mfma<T>::step(acc[i][j], fr[i], fr[RB + j]);
-            }
-            wave_exchange();
-        }
+    struct Line {
+        u32x4_t w[RB * 4], x[NB * 4];
     };
-    using One = std::integral_constant<int, 1>;
+    auto load = [&](Line& to, int line, auto INSIDE) {
+        const int k = line * LINE + mine;
+#pragma unroll
+        for (int i = 0; i < RB * 4; ++i) to.w[i] = granule<T, WD, decltype(INSIDE)::value, true>(w[i], k, f.cols);
+#pragma unroll
+        for (int i = 0; i < NB * 4; ++i) to.x[i] = granule<T, XD, decltype(INSIDE)::value, false>(x[i], k, f.cols);
+    };
+    auto multiply = [&](const Line& from) {
+#pragma unroll
+        for (int i = 0; i < (RB + NB) * 4; ++i) {
+            const int r = i * 8 + (lane >> 3);
+            *reinterpret_cast<u32x4_t*>(tile + r * 128 + swz_r<8>(r, lane & 7) * 16) = i < RB * 4 ? from.w[i] : from.x[i - RB * 4];
+        }
+        wave_exchange();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            u32x4_t fr[RB + NB];
+#pragma unroll
+            for (int j = 0; j < RB + NB; ++j) {
+                const int r = j * 32 + frow;
+                fr[j] = *reinterpret_cast<const u32x4_t*>(tile + r * 128 + swz_r<8>(r, 2 * kk + fhalf) * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) Mfma<T>::step(acc[i][j], fr[i], fr[RB + j]);
+        }
+        wave_exchange();
+    };
+    // AHEAD lines on their way: one is multiplied, the one AHEAD lines of the wave further takes its registers (past
+    // the last whole line, that line again)
     const int whole = f.cols / LINE;  // lines without zeros
+    Line ring[AHEAD];
     int line = wave;
-    for (; line + 4 * (AHEAD - 1) < whole; line += 4 * AHEAD) run(line, std::integral_constant<int, AHEAD>{}, std::true_type{});
-    for (; line < whole; line += 4) run(line, One{}, std::true_type{});
-    if (line < lines) run(line, One{}, std::false_type{});
+    if (line < whole) {
+#pragma unroll
+        for (int l = 0; l < AHEAD; ++l) load(ring[l], min(line + 4 * l, whole - 1), std::true_type{});
+        while (line < whole) {
+#pragma unroll
+            for (int l = 0; l < AHEAD; ++l) {
+                if (line < whole) {
+                    multiply(ring[l]);
+                    load(ring[l], min(line + 4 * AHEAD, whole - 1), std::true_type{});
+                    line += 4;
+                }
+            }
+        }
+    }
+    if (line < lines) {
+        load(ring[0], line, std::false_type{});
+        multiply(ring[0]);
+    }
     __syncthreads();
     float* sums = reinterpret_cast<float*>(lds);  // [wave][i, j, accumulator][lane]
 #pragma unroll
@@ -446,6 +459,77 @@ __global__ __launch_bounds__(256) void k_head_few(FewArgs f) {
         const int first = row0 + q / NB * 32;
         if (first < a.rows)
             reduce_column<1, true>(a, col, q % NB * 32 + frow, first, a.rows - first, int64_t(blockIdx.x) * RB + q / NB, fhalf);
+    }
+}
+
+// The same for bf16 rows of whole 128-byte lines at 16-byte addresses: WV waves
+// with 32 rows of the table each, over the whole contraction, and NB * 32
+// tokens that they share.  Both operands come by direct global->LDS loads, a
+// line of every row a stage, into a ring of 3 stages: loads on their way take
+// no registers, waves share x, and none waits for the others' sums at the end.
+// One token over 50257 x 768: 14.8 us, 19.7 with the kernel above; 64 tokens
+// over 128256 x 4096: 217 and 232.  But 32 tokens there: 200 and 186, of a
+// table that does not fit the Infinity Cache; the kernel above has four lines
+// of a row on their way at once.
+template <int WV, int NB>
+__global__ __launch_bounds__(64 * WV) void k_head_stream(FewArgs f) {
+    constexpr int ROWS = WV * 32 + NB * 32, STAGE = ROWS * 128, SLOTS = 3;
+    constexpr int LP = ROWS / 8 / WV;  // loads a wave and stage: 8 rows each, the first 4 of the table
+    static_assert(ROWS / 8 % WV == 0, "whole loads");
+    const LogitArgs& a = f.l;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[SLOTS * STAGE];
+    const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
+    const int frow = lane & 31, fhalf = lane >> 5;
+    const int row0 = int(blockIdx.x) * WV * 32;
+    const uint8_t* from[LP];  // rows past the last are the last again
+#pragma unroll
+    for (int i = 0; i < LP; ++i) {
+        const int r = (i * WV + wave) * 8 + (lane >> 3);
+        from[i] = (i < 4 ? f.table + int64_t(min(row0 + r, a.rows - 1)) * f.pitch
+                         : f.x + min(int64_t(r - WV * 32), a.n - 1) * f.x_pitch) +
+                  swz_r<8>(r, lane & 7) * 16;
+    }
+    const int stages = f.cols / 64;
+    auto load = [&](int t) {
+        const int at = min(t, stages - 1) * 128;
+        uint8_t* to = lds + t % SLOTS * STAGE + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < LP; ++i) {
+            if (i < 4)  // the table past the caches (the last argument's bit 1)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from[i] + at),
+                                                 (__attribute__((address_space(3))) void*)(to + i * WV * 1024), 16, 0, 2);
+            else
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from[i] + at),
+                                                 (__attribute__((address_space(3))) void*)(to + i * WV * 1024), 16, 0, 0);
+        }
+    };
+    f32x16_t acc[NB] = {};
+#pragma unroll
+    for (int t = 0; t < SLOTS - 1; ++t) load(t);
+    for (int t = 0; t < stages; ++t) {
+        // this wave's loads of stage t have landed, then everyone's, and nobody reads stage t - 1 any more
+        waitcnt_seen<(SLOTS - 2) * LP, 0>();
+        __builtin_amdgcn_s_barrier();
+        load(t + SLOTS - 1);
+        const uint8_t* slot = lds + t % SLOTS * STAGE;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            auto fragment = [&](int r) { return *reinterpret_cast<const u32x4_t*>(slot + r * 128 + swz_r<8>(r, 2 * kk + fhalf) * 16); };
+            const u32x4_t w = fragment(wave * 32 + frow);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) Mfma<uint16_t>::step(acc[j], w, fragment(WV * 32 + j * 32 + frow));
+        }
+    }
+    wait_vmcnt<0>();  // the loads past the end, before LDS is released
+    const int first = row0 + wave * 32, held = a.rows - first;
+    if (held <= 0) return;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        f32x16_t col[1] = {acc[j]};
+        if (held >= 32)
+            reduce_column<1, false>(a, col, j * 32 + frow, first, held, int64_t(blockIdx.x) * WV + wave, fhalf);
+        else
+            reduce_column<1, true>(a, col, j * 32 + frow, first, held, int64_t(blockIdx.x) * WV + wave, fhalf);
     }
 }
 
@@ -509,7 +593,6 @@ struct RowArgs {
     const float4* parts;
     const float* targets;
     const float* logits;
-    int64_t ldl;
     int64_t n;
     int n_parts, part_rows, rows;
     Ids ids;
@@ -576,7 +659,7 @@ __device__ __forceinline__ void top_by_lists(const RowArgs& a, int64_t token, co
             const int p = __shfl(parts.id, min(k, 63), 64);
             const int64_t row = int64_t(p) * a.part_rows + i % a.part_rows;
             row4[u] = i < total && p != INT32_MAX && row < a.rows ? int(row) : -1;  // fewer parts, the table's end
-            y4[u] = row4[u] >= 0 ? a.logits[token * a.ldl + row] : 0.f;
+            y4[u] = row4[u] >= 0 ? a.logits[(int64_t(p) * a.n + token) * a.part_rows + i % a.part_rows] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) top.offer(y4[u], row4[u], row4[u] >= 0);
@@ -655,8 +738,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_head_few_rows(RowArgs a) {
     const int total = n_parts * a.part_rows;
     if (n_parts <= kRoomParts)
         for (int i = threadIdx.x; i < total; i += 64 * kRowWaves) {
-            const int64_t row = int64_t(parts[i / a.part_rows]) * a.part_rows + i % a.part_rows;
-            const float y = row < a.rows ? a.logits[token * a.ldl + row] : 0.f;
+            const int64_t p = parts[i / a.part_rows], row = p * a.part_rows + i % a.part_rows;
+            const float y = row < a.rows ? a.logits[(p * a.n + token) * a.part_rows + i % a.part_rows] : 0.f;
             if (row < a.rows && y >= least) {
                 const int at = atomicAdd(&n_rows, 1);
                 if (at < kRoomRows) {
@@ -1481,16 +1564,28 @@ template <int WD, int XD> void launch_few(const FewArgs& f, hipStream_t stream) 
             : k_head_few<WD, XD, 1, 2><<<grid, dim3(256), 0, stream>>>(f);
 }
 
+// Rows of a block of k_head_stream: 128 where that leaves three blocks a CU.
+void launch_stream(const FewArgs& f, hipStream_t stream) {
+    const bool large = f.l.rows >= 128 * 3 * kCusHead;
+    const dim3 grid(uint32_t(ceil_div(f.l.rows, large ? 128 : 64))), block(large ? 256 : 128);
+    if (f.l.n <= 32)
+        large ? k_head_stream<4, 1><<<grid, block, 0, stream>>>(f) : k_head_stream<2, 1><<<grid, block, 0, stream>>>(f);
+    else
+        large ? k_head_stream<4, 2><<<grid, block, 0, stream>>>(f) : k_head_stream<2, 2><<<grid, block, 0, stream>>>(f);
+}
+
 hipError_t launch_logprob(const mfsdp_entry& e, const HeadShape& s, const Batch& b, RowArgs r) {
     LogitArgs a = logit_args(e, s, b);
     a.parts = reinterpret_cast<float4*>(b.ws + s.parts);
     a.targets = reinterpret_cast<float*>(b.ws + s.targets);
     a.logits = r.top_k > 0 ? reinterpret_cast<float*>(b.ws + s.logits) : nullptr;
-    a.ldl = s.vp;
     if (s.few) {
         const int xs = b.x_type == kBF16 ? 2 : 4, es = e.dtype == kBF16 ? 2 : 4;
         const FewArgs f = {a, b.table, static_cast<const uint8_t*>(b.x), b.stride * xs, e.cols * es, int(e.cols)};
-        if (e.dtype == kBF16)
+        const bool lines = s.direct && xs == 2 && !misaligned(b.x, 16) && b.stride % 8 == 0;
+        if (lines && (b.n > 32 || e.rows * e.cols * es <= kCacheBytes))
+            launch_stream(f, b.stream);
+        else if (e.dtype == kBF16)
             b.x_type == kBF16 ? launch_few<kBF16, kBF16>(f, b.stream) : launch_few<kBF16, kF32>(f, b.stream);
         else
             b.x_type == kBF16 ? launch_few<kF32, kBF16>(f, b.stream) : launch_few<kF32, kF32>(f, b.stream);
@@ -1505,7 +1600,6 @@ hipError_t launch_logprob(const mfsdp_entry& e, const HeadShape& s, const Batch&
     r.parts = a.parts;
     r.targets = a.targets;
     r.logits = a.logits;
-    r.ldl = a.ldl;
     r.n_parts = int(s.n_parts);
     r.part_rows = s.part_rows;
     if (s.few)
