@@ -510,7 +510,10 @@ mfsdp_status mfsdp_embed_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_embe
  * its log probability is 0 and has no gradient, its entropy and alternatives
  * are the table's.  ids may be NULL: every row counts and none has a target.
  * Non-finite logits propagate by the formulas: a NaN or +Inf makes the row's
- * log probability and entropy NaN; a NaN is never among the alternatives.  An
+ * log probability and entropy NaN; a NaN is never among the alternatives.  A
+ * logit of -Inf has probability 0, as a target log probability -Inf, and comes
+ * last among the alternatives; a row of nothing else has log probability NaN
+ * and entropy 0.  dx is NaN in the columns where the table is infinite.  An
  * infinite value of an fp32 x or table may make a logit NaN where the formula
  * has an infinite one.
  *
@@ -573,7 +576,8 @@ typedef struct mfsdp_head_logprob_args {
  * Errors: INVALID_ARGUMENT (null pointer, entry out of range, n, first_id,
  * x_stride, scale or top_k out of range, misaligned buffer), UNSUPPORTED
  * (id_type, x_type, more than 2^20 columns, more than 2^24 - 1 tiles of 128 x
- * 128 logits), WORKSPACE_TOO_SMALL, HIP. */
+ * 128 logits or table elements or a third as many of 64 x 64 elements of x),
+ * WORKSPACE_TOO_SMALL, HIP. */
 mfsdp_status mfsdp_head_logprob(mfsdp_plan_t plan, int64_t entry, const mfsdp_head_logprob_args* args);
 
 typedef struct mfsdp_head_total_args {
