@@ -143,9 +143,8 @@ __device__ __forceinline__ Planes planes_of(float v) {
 // Rows of a matrix in the layout the tile loop takes, one plane of a bf16
 // matrix or three of an fp32 one: zeros behind each row's end, for rows past
 // the last and for padding tokens.
-template <int D>
-__global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a) {
-    const int64_t w = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
+template <int D> __device__ __forceinline__ void pack_word(const PackArgs& a, int64_t block) {
+    const int64_t w = block * kPackThreads + threadIdx.x;
     if (w >= a.words) return;
     const int64_t row = w / a.per_row;
     const int g = int(w % a.per_row), c = g * 8;
@@ -180,6 +179,15 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a) {
         for (int j = 0; j < 3; ++j) *reinterpret_cast<u32x4_t*>(dst + j * a.plane) = o[j];
     }
 }
+// One matrix, and another from block `second` on: the batch and the table in
+// one launch.
+template <int D, int D2>
+__global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a, PackArgs b, uint32_t second) {
+    if (blockIdx.x < second)
+        pack_word<D>(a, blockIdx.x);
+    else
+        pack_word<D2>(b, blockIdx.x - second);
+}
 
 // The packed batch turned over, a plane's 64 x 64 elements a block: rows are
 // its columns, contiguous along the tokens.
@@ -187,11 +195,13 @@ struct TurnArgs {
     const uint8_t* src;
     uint8_t* dst;
     int64_t src_block, dst_block, src_plane, dst_plane;
+    uint32_t across, stages, blocks;  // 64-token and 64-column blocks, and all of them
 };
-__global__ __launch_bounds__(256) void k_head_turn(TurnArgs a) {
+__device__ __forceinline__ void turn_block(const TurnArgs& a, uint32_t block) {
     __shared__ uint16_t t[64][66];
-    const uint8_t* src = a.src + blockIdx.z * a.src_plane + blockIdx.y * a.src_block + int64_t(blockIdx.x) * 8192;
-    uint8_t* dst = a.dst + blockIdx.z * a.dst_plane + blockIdx.x * a.dst_block + int64_t(blockIdx.y) * 8192;
+    const uint32_t bx = block % a.across, by = block / a.across % a.stages, bz = block / a.across / a.stages;
+    const uint8_t* src = a.src + bz * a.src_plane + by * a.src_block + int64_t(bx) * 8192;
+    uint8_t* dst = a.dst + bz * a.dst_plane + bx * a.dst_block + int64_t(by) * 8192;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int k = int(threadIdx.x) + i * 256, row = k >> 3, g = k & 7;
@@ -1167,19 +1177,36 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
         });
 }
 
-// The parts of dx added in their order.
-template <int D>
+// The parts of dx added up: SLICES groups of consecutive parts, each in its
+// order, by as many threads, then the groups' sums in theirs.  (8 tokens of 512
+// columns in 117 parts are 512 words of work: 30 us with one thread each, all
+// of it one load after another, 6.8 with 8.)
+template <int D, int SLICES>
 __global__ __launch_bounds__(256) void k_head_dx_sum(DxArgs a) {
-    const int64_t w = int64_t(blockIdx.x) * 256 + threadIdx.x, per = a.ld / 8;
+    constexpr int WORDS = 256 / SLICES;
+    __shared__ Values sums[SLICES][WORDS];
+    const int slice = int(threadIdx.x) / WORDS, in = int(threadIdx.x) % WORDS;
+    const int64_t w = int64_t(blockIdx.x) * WORDS + in, per = a.ld / 8;
     const int64_t token = w / per;
     const int col = int(w % per) * 8;
-    if (token >= a.n || col >= a.cols) return;
+    const bool here = token < a.n;
     Values v = {};
+    if (here) {
+        const int end = a.splits * (slice + 1) / SLICES;
 #pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) {
-        const float4* from = reinterpret_cast<const float4*>(a.sums + (s * a.n + token) * a.ld + col);
-        v = fma8(1.f, Values{from[0], from[1]}, v);
+        for (int s = a.splits * slice / SLICES; s < end; ++s) {
+            const float4* from = reinterpret_cast<const float4*>(a.sums + (s * a.n + token) * a.ld + col);
+            v = fma8(1.f, Values{from[0], from[1]}, v);
+        }
     }
+    if constexpr (SLICES > 1) {
+        sums[slice][in] = v;
+        __syncthreads();
+        if (slice > 0) return;
+#pragma unroll
+        for (int s = 1; s < SLICES; ++s) v = fma8(1.f, sums[s][in], v);
+    }
+    if (!here) return;
     if (!token_of(a.ids, token, a.rows).live) v = Values{};
     put8<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
 }
@@ -1211,10 +1238,10 @@ struct ListArgs {
     int* starts;
     uint32_t* list;
 };
-__global__ __launch_bounds__(256) void k_head_lists(ListArgs a) {
+__device__ __forceinline__ void list_block(const ListArgs& a, uint32_t block) {
     __shared__ int counts[4];
     const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
-    const int first = int(blockIdx.x) * kListRows;
+    const int first = int(block) * kListRows;
     int below = 0;
 #pragma unroll 4
     for (int i = threadIdx.x; i < a.n; i += 256) below += uint32_t(a.targets[i]) < uint32_t(first);
@@ -1222,7 +1249,7 @@ __global__ __launch_bounds__(256) void k_head_lists(ListArgs a) {
     if (lane == 0) counts[wave] = below;
     __syncthreads();
     int at = counts[0] + counts[1] + counts[2] + counts[3];
-    if (threadIdx.x == 0) a.starts[blockIdx.x] = at;
+    if (threadIdx.x == 0) a.starts[block] = at;
     if (first >= a.rows) return;  // the block past the last group: its start is the last one's end
     for (int i0 = 0; i0 < a.n; i0 += 256) {
         const int i = i0 + int(threadIdx.x);
@@ -1237,6 +1264,14 @@ __global__ __launch_bounds__(256) void k_head_lists(ListArgs a) {
         if (hit) a.list[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] = c << 24 | uint32_t(i);
         at += counts[0] + counts[1] + counts[2] + counts[3];
     }
+}
+
+// What dW needs besides dz, in one launch: x turned over, and the lists.
+__global__ __launch_bounds__(256) void k_head_turn(TurnArgs t, ListArgs l) {
+    if (blockIdx.x < t.blocks)
+        turn_block(t, blockIdx.x);
+    else
+        list_block(l, blockIdx.x - t.blocks);
 }
 
 // What rounding took from the targets' dz, times x, added to the staged rows
@@ -1474,8 +1509,9 @@ mfsdp_status check_common(mfsdp_plan_t plan, int64_t entry, int64_t n, int32_t x
     if (e.cols > kMaxCols) return fail(MFSDP_ERR_UNSUPPORTED, "a table of more than 2^20 columns");
     if (ceil_div(e.rows, 128) * ceil_div(n, 128) > kMaxTiles || ceil_div(e.rows, 128) * ceil_div(e.cols, 128) > kMaxTiles)
         return fail(MFSDP_ERR_UNSUPPORTED, "more than 2^24 - 1 tiles of 128 x 128 logits or table elements: cut the batch or the table");
-    if (ceil_div(e.cols, 64) * ceil_div(n, kPadTokens) * (kPadTokens / 64) * 3 > kMaxTiles)  // k_head_turn
-        return fail(MFSDP_ERR_UNSUPPORTED, "more than (2^24 - 1) / 3 tiles of 64 x 64 elements of x: cut the batch");
+    // k_head_turn's blocks
+    if (ceil_div(e.cols, 64) * ceil_div(n, kPadTokens) * (kPadTokens / 64) * 3 + ceil_div(e.rows, kListRows) + 1 > kMaxTiles)
+        return fail(MFSDP_ERR_UNSUPPORTED, "more than a third of 2^24 tiles of 64 x 64 elements of x: cut the batch");
     return MFSDP_OK;
 }
 
@@ -1505,15 +1541,28 @@ mfsdp_status check_space(const void* workspace, uint64_t have, uint64_t need) {
     return MFSDP_OK;
 }
 
-void launch_pack(const PackArgs& a, int src_type, hipStream_t stream) {
-    // a launch has fewer than 2^32 threads: whole rows each
-    constexpr int64_t kMost = ((int64_t(1) << 32) / kPackThreads - 1) * kPackThreads;
-    const int64_t per_row = a.per_row, chunk = kMost / per_row * per_row;
+// a launch has fewer than 2^32 threads: whole rows each
+constexpr int64_t kMostWords = ((int64_t(1) << 32) / kPackThreads - 2) * kPackThreads;
+
+void launch_pack(const PackArgs& a, int a_type, const PackArgs& b, int b_type, hipStream_t stream) {
+    const uint32_t second = uint32_t(ceil_div(a.words, kPackThreads));
+    const dim3 grid(second + uint32_t(ceil_div(b.words, kPackThreads))), block(kPackThreads);
+    if (a_type == kBF16)
+        b_type == kBF16 ? k_head_pack<kBF16, kBF16><<<grid, block, 0, stream>>>(a, b, second)
+                        : k_head_pack<kBF16, kF32><<<grid, block, 0, stream>>>(a, b, second);
+    else
+        b_type == kBF16 ? k_head_pack<kF32, kBF16><<<grid, block, 0, stream>>>(a, b, second)
+                        : k_head_pack<kF32, kF32><<<grid, block, 0, stream>>>(a, b, second);
+}
+
+// A matrix of any size, by launches of whole rows.
+void launch_pack(const PackArgs& a, int type, hipStream_t stream) {
+    const int64_t per_row = a.per_row, chunk = kMostWords / per_row * per_row;
     for (int64_t w = 0; w < a.words; w += chunk) {
         PackArgs b = a;
         const int64_t row = w / per_row;
         b.words = std::min(chunk, a.words - w);
-        b.src = a.src + row * a.stride * (src_type == kBF16 ? 2 : 4);
+        b.src = a.src + row * a.stride * (type == kBF16 ? 2 : 4);
         b.dst = a.dst + row * 128;
         b.rows = std::max<int64_t>(0, a.rows - row);
         if (a.ids.ids) b.ids.ids = static_cast<const uint8_t*>(a.ids.ids) + row * (a.ids.type == MFSDP_I64 ? 8 : 4);
@@ -1521,11 +1570,7 @@ void launch_pack(const PackArgs& a, int src_type, hipStream_t stream) {
             b.targets = a.targets + row;
             b.rest = a.rest + row;
         }
-        const dim3 grid(uint32_t(ceil_div(b.words, kPackThreads)));
-        if (src_type == kBF16)
-            k_head_pack<kBF16><<<grid, dim3(kPackThreads), 0, stream>>>(b);
-        else
-            k_head_pack<kF32><<<grid, dim3(kPackThreads), 0, stream>>>(b);
+        launch_pack(b, type, PackArgs{}, type, stream);
     }
 }
 
@@ -1571,10 +1616,10 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
         p.targets = reinterpret_cast<int*>(b.ws + s.targets);
         p.rest = reinterpret_cast<float*>(b.ws + s.rest);
     }
-    launch_pack(p, b.x_type, b.stream);
+    const PackArgs x = p;
     a.x = Operand{p.dst, 128, p.block, s.np, s.stages, s.x_planes, p.plane};
     a.table = Operand{b.table, e.cols * 2, 128, e.rows, s.stages, 1, 0};
-    if (s.direct) return;
+    if (s.direct) return launch_pack(x, b.x_type, b.stream);
     p.src = b.table;
     p.dst = b.ws + s.table;
     p.stride = e.cols;
@@ -1584,20 +1629,27 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
     p.words = e.rows * p.per_row;
     p.ids = Ids{};
     p.targets = nullptr;
-    launch_pack(p, e.dtype, b.stream);
+    if (x.words + p.words <= kMostWords) {
+        launch_pack(x, b.x_type, p, e.dtype, b.stream);
+    } else {
+        launch_pack(x, b.x_type, b.stream);
+        launch_pack(p, e.dtype, b.stream);
+    }
     a.table = Operand{p.dst, 128, p.block, e.rows, s.stages, s.table_planes, p.plane};
 }
 
 template <int WD, int XD> void launch_few(const FewArgs& f, hipStream_t stream) {
-    // 64 rows a block where that leaves two blocks a CU: x is read half as often
-    const bool two = f.l.rows >= 64 * 2 * kCusHead;
+    // Rows of a block: 64 where that leaves two blocks a CU, since x is then read half as often, and for more than 32
+    // tokens 32, since three blocks fit a CU (60 tokens over 50000 x 1000: 60 us, 66 with 64 rows; over 50000 x 1001
+    // fp32 129 and 145; 40 over 128256 x 1001 179 and 174).
+    const bool two = f.l.n <= 32 && f.l.rows >= 64 * 2 * kCusHead;
     const dim3 grid(uint32_t(ceil_div(f.l.rows, two ? 64 : 32)));
-    if (f.l.n <= 32)
-        two ? k_head_few<WD, XD, 2, 1><<<grid, dim3(256), 0, stream>>>(f)
-            : k_head_few<WD, XD, 1, 1><<<grid, dim3(256), 0, stream>>>(f);
+    if (f.l.n > 32)
+        k_head_few<WD, XD, 1, 2><<<grid, dim3(256), 0, stream>>>(f);
+    else if (two)
+        k_head_few<WD, XD, 2, 1><<<grid, dim3(256), 0, stream>>>(f);
     else
-        two ? k_head_few<WD, XD, 2, 2><<<grid, dim3(256), 0, stream>>>(f)
-            : k_head_few<WD, XD, 1, 2><<<grid, dim3(256), 0, stream>>>(f);
+        k_head_few<WD, XD, 1, 1><<<grid, dim3(256), 0, stream>>>(f);
 }
 
 // Rows of a block of k_head_stream: 128 where that leaves three blocks a CU.
@@ -1663,7 +1715,11 @@ template <int D> void launch_dx(const DxArgs& a, int tile, hipStream_t stream) {
         k_head_dx<D, 256><<<grid, dim3(256), 0, stream>>>(a);
     else
         k_head_dx<D, 128><<<grid, dim3(256), 0, stream>>>(a);
-    if (a.splits > 1) k_head_dx_sum<D><<<dim3(uint32_t(ceil_div(a.n * (a.ld / 8), 256))), dim3(256), 0, stream>>>(a);
+    const int64_t words = a.n * (a.ld / 8);
+    if (a.splits >= 16)  // fewer are all on their way at once
+        k_head_dx_sum<D, 8><<<dim3(uint32_t(ceil_div(words, 32))), dim3(256), 0, stream>>>(a);
+    else if (a.splits > 1)
+        k_head_dx_sum<D, 1><<<dim3(uint32_t(ceil_div(words, 256))), dim3(256), 0, stream>>>(a);
 }
 
 template <int D> void launch_dw(const DwArgs& a, int tile, hipStream_t stream) {
@@ -1721,8 +1777,12 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     if (g.grad) {
         DwArgs a = {};
         const int64_t kp = int64_t(s.stages) * 64;
-        const TurnArgs t = {d.l.x.base, b.ws + s.turned, d.l.x.block, kp * 128, d.l.x.plane, d.l.x.plane};
-        k_head_turn<<<dim3(uint32_t(s.np / 64), uint32_t(s.stages), uint32_t(s.x_planes)), dim3(256), 0, b.stream>>>(t);
+        const uint32_t across = uint32_t(s.np / 64), groups = rest ? uint32_t(ceil_div(e.rows, kListRows) + 1) : 0;
+        const TurnArgs t = {d.l.x.base, b.ws + s.turned, d.l.x.block, kp * 128, d.l.x.plane, d.l.x.plane,
+                            across, uint32_t(s.stages), across * uint32_t(s.stages) * uint32_t(s.x_planes)};
+        const ListArgs l = {targets, int(b.n), int(e.rows), reinterpret_cast<int*>(b.ws + s.starts),
+                            reinterpret_cast<uint32_t*>(b.ws + s.list)};
+        k_head_turn<<<dim3(t.blocks + groups), dim3(256), 0, b.stream>>>(t, l);
         a.turned = Operand{t.dst, 128, t.dst_block, kp, int(s.np / 64), s.x_planes, t.dst_plane};
         a.x = d.l.x;
         a.dz = dz;
@@ -1735,11 +1795,6 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.starts = reinterpret_cast<int*>(b.ws + s.starts);
         a.list = reinterpret_cast<uint32_t*>(b.ws + s.list);
         a.rest = rest;
-        if (rest) {
-            const ListArgs l = {targets, int(b.n), int(e.rows), reinterpret_cast<int*>(b.ws + s.starts),
-                                reinterpret_cast<uint32_t*>(b.ws + s.list)};
-            k_head_lists<<<dim3(uint32_t(ceil_div(e.rows, kListRows) + 1)), dim3(256), 0, b.stream>>>(l);
-        }
         a.grad = g.grad;
         a.vector = e.cols * (e.dtype == kBF16 ? 2 : 4) % 16 == 0;  // the entry is 16-byte aligned
         a.add = g.add;
