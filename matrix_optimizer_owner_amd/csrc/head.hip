@@ -1247,7 +1247,7 @@ struct DwArgs {
     int rows, cols;
     int tp, tq;          // tiles along the columns and the vocabulary
     int stages;          // of the contraction over the batch
-    const int* starts;   // of k_head_lists
+    const int* starts;   // of the lists below
     const uint32_t* list;
     const float* rest;   // NULL, or the rests of the targets' dz (x then has one plane)
     uint8_t* grad;
@@ -1410,7 +1410,7 @@ mfsdp_status hip_fail(hipError_t e, const char* what) {
 bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 constexpr int64_t kMaxTokens = int64_t(1) << 22, kMaxFirst = int64_t(1) << 62, kMaxStride = int64_t(1) << 40;
-constexpr int64_t kMaxCols = int64_t(1) << 20;         // byte offsets inside a stage stay below 2^31
+constexpr int64_t kMaxCols = int64_t(1) << 20;         // byte offsets inside a stage stay below 2^31 (rows: a plan's 2^22)
 constexpr int64_t kMaxTiles = (int64_t(1) << 32) / 256 - 1;  // a launch has fewer than 2^32 threads
 constexpr int kCusHead = 256;
 
