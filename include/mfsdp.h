@@ -501,8 +501,9 @@ mfsdp_status mfsdp_embed_grad(mfsdp_plan_t plan, int64_t entry, const mfsdp_embe
  * The table may be any 2D entry of up to 2^20 columns, bf16 or fp32, tied to
  * the embedding or not.  Logits are sums in fp32 of products of the values
  * given, bf16 or fp32 (exact, but for at most 2^-22 of a product of two fp32
- * values, and bits under 2^-133 of an fp32 value below 2^-109); the sums over them are fp32 in an order that sizes alone fix
- * (bitwise the same from run to run, no atomics).
+ * values, and bits under 2^-133 of an fp32 value below 2^-109); the sums over
+ * them are fp32 in an order that sizes alone fix (bitwise the same from run to
+ * run, no atomics).
  *
  * A negative id marks padding: log probability and entropy 0, no
  * alternatives, no gradient, and whatever x holds there (NaN too) is not read
