@@ -34,6 +34,12 @@
 #include "plan_internal.h"
 #include "tile_loop.h"
 
+// Products are rounded before they are added, but where __builtin_fmaf says
+// otherwise: y - max has to be at most 0, and 0 for the largest y, however
+// large y is.  Fused, a scaled sum less its own rounded value is what rounding
+// took, up to 2^102, and 2 to that power is infinite.
+#pragma clang fp contract(off)
+
 namespace mfsdp {
 namespace {
 
