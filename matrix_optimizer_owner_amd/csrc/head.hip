@@ -51,8 +51,9 @@ constexpr int64_t kFewTokens = 64;      // batches up to this are read straight 
 constexpr int64_t kCacheBytes = int64_t(256) << 20;  // the Infinity Cache
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-// A logit of -inf has probability 0 and no part in a sum: the exponent of its
-// probability is kept finite, where that is 0 already.  NaN stays NaN.
+// A logit of -inf, or one far below the largest, has probability 0 and no part
+// in a sum: the exponent of its probability is kept where that is 0 already and
+// its product with any sum is finite.  NaN stays NaN.
 __device__ __forceinline__ float not_below(float y) { return __builtin_elementwise_maximum(y, -1024.f); }
 
 // ---- token ids ----
@@ -577,7 +578,7 @@ struct Sums {
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
     if (b.s == 0.f) return a;  // no part: NaN sums are not equal to 0
     if (a.s == 0.f) return b;
-    const float m = fmaxf(a.m, b.m), da = a.m - m, db = b.m - m;
+    const float m = fmaxf(a.m, b.m), da = not_below(a.m - m), db = not_below(b.m - m);  // da * s stays finite
     const float fa = exp2_fast(da), fb = exp2_fast(db);
     return Sums{m, __builtin_fmaf(a.s, fa, b.s * fb),
                 __builtin_fmaf(fa, __builtin_fmaf(da, a.s, a.w), fb * __builtin_fmaf(db, b.s, b.w))};
@@ -972,7 +973,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
             m = r.max;
             ls = log2f(r.sum);
             // dz = hit - p (b + c lp), lp = log2 p
-            b = d.scale * __builtin_fmaf(dh, nat(ls - r.wsum / r.sum), up);
+            b = d.scale * (d.dentropy ? __builtin_fmaf(dh, nat(ls - r.wsum / r.sum), up) : up);
             c = d.scale * dh * kLn2;
             if (tok.target >= 0 && r.found && live) {
                 t = tok.target - row0;
