@@ -280,14 +280,17 @@ template <int MM, bool RAGGED, typename A>
 __device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_t token, int row0, int held, int64_t part,
                                               int fhalf) {
     const bool in = token < a.n;
-    float most = -FLT_MAX, sum[2] = {0.f, 0.f}, wsum[2] = {0.f, 0.f};
+    // The largest, NaN where none is a number: such a part is not among the ones
+    // that may hold alternatives, one with a -inf is.
+    float most = NAN, sum[2] = {0.f, 0.f}, wsum[2] = {0.f, 0.f};
     each_row<MM>(fhalf, [&](int mi, int e, int r) {
         acc[mi][e] *= a.c2;
         if (!RAGGED || r < held) most = fmaxf(most, acc[mi][e]);
     });
     most = fmaxf(most, __shfl_xor(most, 32, 64));
+    const float base = fmaxf(most, -FLT_MAX);
     each_row<MM>(fhalf, [&](int mi, int e, int r) {
-        const float d = not_below(acc[mi][e] - most), p = exp2_fast(d);
+        const float d = not_below(acc[mi][e] - base), p = exp2_fast(d);
         if (!RAGGED || r < held) {
             sum[e & 1] += p;
             wsum[e & 1] = __builtin_fmaf(p, d, wsum[e & 1]);
@@ -296,7 +299,7 @@ __device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_
     float s = sum[0] + sum[1], w = wsum[0] + wsum[1];
     s += __shfl_xor(s, 32, 64);
     w += __shfl_xor(w, 32, 64);
-    if (in && fhalf == 0) a.parts[part * a.n + token] = make_float4(s == 0.f ? -INFINITY : most, s, w, 0.f);
+    if (in && fhalf == 0) a.parts[part * a.n + token] = make_float4(most, s, w, 0.f);
     if (a.ids.ids) {
         const int t = in ? token_of(a.ids, token, a.rows).target - row0 : -1;
         if (__ballot(t >= 0 && t < MM * 32))
