@@ -975,8 +975,9 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
             const float up = r.found ? d.dlogp[token] : 0.f, dh = d.dentropy ? d.dentropy[token] : 0.f;
             m = r.max;
             ls = log2f(r.sum);
-            // dz = hit - p (b + c lp), lp = log2 p
+            // dz = hit - p (b + c lp), lp = log2 p; NaN where the sum is none
             b = d.scale * (d.dentropy ? __builtin_fmaf(dh, nat(ls - r.wsum / r.sum), up) : up);
+            if (!(r.sum > 0.f)) b = NAN;
             c = d.scale * dh * kLn2;
             if (tok.target >= 0 && r.found && live) {
                 t = tok.target - row0;
@@ -984,7 +985,8 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
             }
         }
         each_row<S::MM>(fhalf, [&](int mi, int e, int) {
-            const float lp = not_below((acc[mi][ni][e] * a.c2 - m) - ls);
+            // at most 0: y is formed again, in another order than by k_head_few, and may pass the largest by its rounding
+            const float lp = __builtin_amdgcn_fmed3f((acc[mi][ni][e] * a.c2 - m) - ls, -1024.f, 0.f);
             const float v = -exp2_fast(lp) * __builtin_fmaf(c, lp, b);
             acc[mi][ni][e] = live ? v : 0.f;
         });

@@ -43,3 +43,26 @@ def test_large_equal_logits(n, table, x, weight):
     half += 2.0 ** -8 if table == "bf16" else 0.0      # dw's own type
     assert ((dw[:, 0].double() - want).abs() <= want.abs() * (1.01 * half + LN2 * U * 2 * math.log2(rows) + 8 * U)).all()
     assert torch.isfinite(dx).all() and not dx[1:].any()
+
+
+@pytest.mark.parametrize("size", [1e7, 1e12, 1e30])
+@pytest.mark.parametrize("table,x", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_probabilities_of_logits_formed_again(n, table, x, size):
+    """The gradient's logits are summed in another order than the forward call's of few tokens: what that moves them by is
+    many powers of 2 here, and a probability is at most 1 all the same."""
+    rows, cols = 2000, 200
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    h = Head(rows, cols, table, values=torch.randn(rows, cols, generator=gen, device="cuda") * size)
+    data = torch.randn(n, cols, generator=gen, device="cuda").to(TYPES[x][0])
+    ids = torch.randint(0, rows, (n,), generator=gen, device="cuda")
+    out = h.logprob(data, ids)
+    assert torch.isfinite(out["logp"]).all() and (out["logp"] <= 0).all() and (out["entropy"] >= 0).all()
+    dlogp = torch.randn(n, generator=gen, device="cuda")
+    dx, dw = h.grad(data, out["records"], dlogp, None, ids)
+    a = dlogp.double().abs()[:, None]
+    # |dz| is at most |a| for a row's target (1 - p) and for the others (p) together twice that; bf16 steps and sums on top
+    assert (dw.double().abs() <= 1.02 * (a * data.double().abs()).sum(0)).all()
+    top = h.w.double().abs().amax(0)
+    spread = 1.02 * (a * top * 2)
+    assert (dx.double().abs() <= spread).all()
