@@ -1534,8 +1534,9 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     };
     s.x_plane = uint64_t(s.np) * uint64_t(kp) * 2;
     s.table_plane = uint64_t(e.rows) * uint64_t(kp) * 2;
-    s.x = region(uint64_t(s.x_planes) * s.x_plane);
-    s.table = region(s.direct ? 0 : uint64_t(s.table_planes) * s.table_plane);
+    // few tokens read x and the table where they lie
+    s.x = region(s.few ? 0 : uint64_t(s.x_planes) * s.x_plane);
+    s.table = region(s.few || s.direct ? 0 : uint64_t(s.table_planes) * s.table_plane);
     s.targets = region(uint64_t(s.np) * 4);
     if (grad) {
         s.rest = region(uint64_t(s.np) * 4);
