@@ -383,8 +383,8 @@ mfsdp_status mfsdp_owner_step_scaled(mfsdp_plan_t plan, const mfsdp_step_args* a
  *   the odd one's; the dither is (byte + 0.5) / 256.
  * Non-finite moments: a group that holds one is NaN from then on (its
  * parameters of that step follow the formulas).  Both moments are kept for
- * gradients down to 1e-37; a squared gradient above the fp32 range counts as
- * non-finite.
+ * gradients down to 1e-37, to fp32 roundings or, where a value is subnormal,
+ * half of 2^-149; a squared gradient above the fp32 range counts as non-finite.
  *
  * mfsdp_moments_read and mfsdp_moments_write turn an entry's state into
  * values and back, for a run that goes over to 8 bits or back, or a

@@ -20,12 +20,14 @@
 // about 0.1%, a tenth of half a code step: rounded to nearest it would never
 // move at all; with the dither its mean does.  A moment that stays the same
 // share of its scale keeps its code (the dither keeps 1/512 away from 0 and
-// 1, over 60 times the fp32 error of the share), so idle rows decay exactly.
+// 1, over 60 times the fp32 error of the share), so in idle rows only scales
+// move, by the betas and fp32 roundings.
 //
 // A group with a moment that is not finite gets the scale NaN and is NaN from
 // then on.  Moments are formed in fp32 as the 32-bit step forms them, but r is
-// held and not v, and small values are squared at 2^64 times their size, so
-// that gradients down to the fp32 range's end have a second moment.
+// held and not v, and small values are squared at 2^100 times their size, so
+// that gradients down to the fp32 range's end have a second moment: within a
+// few roundings, or half of 2^-149 each where values are subnormal.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -173,21 +175,23 @@ __device__ __forceinline__ Packed pack(const float (&m)[kPer], const Scale& sm, 
     if (__any(sm.pre != 1.f || sr.pre != 1.f)) return pack_codes<DITHER, true>(m, sm, r, sr, word);
     return pack_codes<DITHER, false>(m, sm, r, sr, word);
 }
-// EXACT: the group's largest value is its scale, bit for bit; else within half a step of fp32
-template <bool EXACT> __device__ __forceinline__ void unpack_first(u32x2_t w, float scale, float (&m)[kPer]) {
-    const float unit = scale * (1.f / 16129.f);
+// A code's share first, then the scale: a group's largest value is its scale,
+// bit for bit, since 16129 * fl(1/16129) and 65025 * fl(1/65025) round to 1, and
+// no factor of a value is below the fp32 range's normal numbers unless the value
+// is.  (scale / 16129 first would save a product a value, and is subnormal from
+// 1.9e-34 down.)
+__device__ __forceinline__ void unpack_first(u32x2_t w, float scale, float (&m)[kPer]) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const float c = float(int8_t(w[k >> 2] >> (8 * (k & 3))));
-        m[k] = EXACT ? c * fabsf(c) * (1.f / 16129.f) * scale : c * fabsf(c) * unit;  // 16129 * fl(1/16129) rounds to 1
+        m[k] = c * fabsf(c) * (1.f / 16129.f) * scale;
     }
 }
-template <bool EXACT> __device__ __forceinline__ void unpack_root(u32x2_t w, float scale, float (&r)[kPer]) {
-    const float unit = scale * (1.f / 65025.f);
+__device__ __forceinline__ void unpack_root(u32x2_t w, float scale, float (&r)[kPer]) {
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const float d = float(uint8_t(w[k >> 2] >> (8 * (k & 3))));
-        r[k] = EXACT ? d * d * (1.f / 65025.f) * scale : d * d * unit;
+        r[k] = d * d * (1.f / 65025.f) * scale;
     }
 }
 
@@ -240,8 +244,8 @@ __device__ __forceinline__ void step_chunk(const Adam8Args& a, const TailDesc& t
         load_n<D>(w, i, n, wv);
         const u32x2_t cm = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pm.codes + i));
         const u32x2_t cr = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pr.codes + i));
-        unpack_first<false>(cm, pm.scales[i / kGroup], m);
-        unpack_root<false>(cr, pr.scales[i / kGroup], r);
+        unpack_first(cm, pm.scales[i / kGroup], m);
+        unpack_root(cr, pr.scales[i / kGroup], r);
     }
     // behind the end g, m and r are zeros (codes there are written as zeros; the state is zero-filled at first)
     uint32_t least = ~0u;  // of the magnitudes that are not zero, as a bit pattern less 1
@@ -253,12 +257,12 @@ __device__ __forceinline__ void step_chunk(const Adam8Args& a, const TailDesc& t
         least = min(least, __float_as_uint(fmaxf(r[k], fabsf(gv[k]))) - 1);
     }
     if (__any(least < __float_as_uint(0x1p-40f) - 1)) {
-        // small values are squared at 2^64 times their size: no square is lost to the fp32 range
+        // small values are squared at 2^100 times their size: the least there is, 2^-149, has a normal square
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const bool small = fmaxf(r[k], fabsf(gv[k])) < 0x1p-40f;
-            const float up = small ? 0x1p64f : 1.f, rk = r[k] * up, gk = gv[k] * up;
-            r[k] = __builtin_amdgcn_sqrtf(__builtin_fmaf(a.b2, rk * rk, a.omb2 * (gk * gk))) * (small ? 0x1p-64f : 1.f);
+            const float up = small ? 0x1p100f : 1.f, rk = r[k] * up, gk = gv[k] * up;
+            r[k] = __builtin_amdgcn_sqrtf(__builtin_fmaf(a.b2, rk * rk, a.omb2 * (gk * gk))) * (small ? 0x1p-100f : 1.f);
         }
     } else {
 #pragma unroll
@@ -328,8 +332,8 @@ __global__ __launch_bounds__(kThreads) void k_moments_read(MomentArgs a) {
         const Place pm = place(a.state, a.m1_off, a.numel), pr = place(a.state, a.m2_off, a.numel);
         const u32x2_t cm = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pm.codes + i));
         const u32x2_t cr = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pr.codes + i));
-        unpack_first<true>(cm, pm.scales[i / kGroup], m);
-        unpack_root<true>(cr, pr.scales[i / kGroup], v);
+        unpack_first(cm, pm.scales[i / kGroup], m);
+        unpack_root(cr, pr.scales[i / kGroup], v);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) v[k] *= v[k];
     } else {
