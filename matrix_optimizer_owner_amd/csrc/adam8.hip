@@ -118,7 +118,7 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
 // as bit patterns, which orders them and puts Inf and NaN above the rest.
 struct Scale {
     float value;      // stored: the largest magnitude, NaN where one is not finite
-    float pre, inv;   // |x| * pre * inv is |x| / value; pre keeps 1 / value a normal number
+    float pre, inv;   // |x| * pre * inv is |x| / value; pre keeps 1 / value a normal number, and is 0 with a NaN
 };
 __device__ __forceinline__ Scale group_scale(const float (&x)[kPer]) {
     uint32_t most = 0;
@@ -127,7 +127,7 @@ __device__ __forceinline__ Scale group_scale(const float (&x)[kPer]) {
     most = group_max(most);
     Scale s;
     s.value = most < 0x7f800000u ? __uint_as_float(most) : __uint_as_float(0x7fc00000u);
-    s.pre = s.value > 0x1p100f ? 0x1p-30f : s.value < 0x1p-90f && s.value > 0.f ? 0x1p60f : 1.f;
+    s.pre = s.value > 0x1p100f ? 0x1p-30f : s.value < 0x1p-90f && s.value > 0.f ? 0x1p60f : s.value >= 0.f ? 1.f : 0.f;
     const float v = s.value * s.pre;
     s.inv = v > 0.f ? __builtin_amdgcn_rcpf(v) : 0.f;
     return s;
@@ -137,10 +137,11 @@ __device__ __forceinline__ Scale group_scale(const float (&x)[kPer]) {
 // value) + 1/2) + byte, whose 256th part rounded down is the code with the
 // dither (byte + 1/2) / 256; else without the 1/2, so that byte 128 gives the
 // nearest code.  The root is at most 1 + 2^-22: no code exceeds count.
-// PRE: the scale's pre is not 1 somewhere in the wave.
+// PRE: the scale's pre is not 1 somewhere in the wave.  A group that is NaN
+// has shares of 0: what is no number has no code.
 template <bool DITHER, bool PRE>
 __device__ __forceinline__ uint32_t code_of(float x, const Scale& s, float count, uint32_t byte) {
-    const float share = PRE ? fabsf(x) * s.pre * s.inv : fabsf(x) * s.inv;
+    const float share = !PRE ? fabsf(x) * s.inv : s.pre > 0.f ? fabsf(x) * s.pre * s.inv : 0.f;
     return uint32_t(__builtin_fmaf(__builtin_amdgcn_sqrtf(share), 256.f * count, DITHER ? 0.5f : 0.f)) + byte;
 }
 

@@ -89,3 +89,20 @@ def test_gradients_of_the_ranges_end(std, beta2):
                 bad = (c < lo) | (c > hi)
                 assert not bad.any(), (i, region, int(bad.sum()), c[bad][:3], lo[bad][:3], hi[bad][:3])
         o.new_grads(std)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e38])
+def test_codes_of_a_group_that_is_nan(bad):
+    """No element of it has a code but 0 in the first moment, and 0 or 1 in the root; other groups are as without it."""
+    a, b = Owner([(4, 256, B.F32, A8)]), Owner([(4, 256, B.F32, A8)])
+    a.view(a.grads, 0)[300] = bad
+    for o in (a, b):
+        o.step(1)
+    got, want = a.state.cpu().numpy(), b.state.cpu().numpy()
+    for region in (0, 1):
+        (c, s), (c0, s0) = (ref.split(o.regions(st, 0)[region], 1024) for o, st in ((a, got), (b, want)))
+        hit = np.zeros(1024, dtype=bool)
+        hit[256:384] = np.isnan(s[2])
+        assert np.isnan(s[2]) or (region == 0 and bad == 3e38)
+        assert (c[hit] <= region).all() and np.array_equal(np.delete(s, 2), np.delete(s0, 2))
+        assert np.array_equal(np.delete(c, np.arange(256, 384)), np.delete(c0, np.arange(256, 384)))
