@@ -21,11 +21,13 @@
 //   dz_j = scale (dlogp ([j = t] - p_j) - dH p_j (ln p_j + H)),
 //   dx = dz W,  dW = dz^T x,
 // dz from the logits formed again, stored once, then two more products.  With
-// fp32 among the operands dz is three planes, else one, rounded to bf16: errors
-// of half a step that are independent from element to element and average out
-// in the sums over the vocabulary and the batch, but for a row's target, which
-// alone can outweigh the rest; what rounding takes from it is kept in fp32 and
-// added where dx and dW are written.
+// fp32 among the operands dz is three planes, else one, rounded to bf16.  Errors
+// of half a step, independent from element to element, average out in sums of
+// many alike, but not where a few entries carry a row, as its target does and
+// a likely other token.  What rounding takes from the entries of a 32nd or more
+// of a row's sum |dz_j| (kShare), of which there are at most 32, is kept in fp32
+// and added where dx and dW are written; what is left of the rounding is at
+// most 2^-8 |dz_j| each, in the 2-norm 2^-8 sqrt(1/32) of the row's sum.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -49,6 +51,8 @@ constexpr int kPackThreads = 256;
 constexpr int kPadTokens = 256;         // rows of the packed batch: a multiple of both tile edges
 constexpr int64_t kFewTokens = 64;      // batches up to this are read straight from x and the table
 constexpr int64_t kCacheBytes = int64_t(256) << 20;  // the Infinity Cache
+constexpr float kShare = 1.f / 32;      // of a row's sum of |dz|: entries from it on keep what rounding takes
+constexpr int kMaxRests = 48;           // such entries of a row, and some more than there can be but for rounding
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // A logit of -inf, or one far below the largest, has probability 0 and no part
@@ -126,8 +130,8 @@ struct PackArgs {
     int cols;
     Ids ids;            // rows with a negative id become zeros
     int table_rows;
-    int* targets;       // NULL, or a row's target in the table, -1 without one ...
-    float* rest;        // ... and a zero
+    int* zeros;         // these words become zeros
+    int64_t n_zeros;
 };
 
 // An fp32 value as three bf16 ones that add up to it, each the nearest to what
@@ -157,10 +161,7 @@ template <int D> __device__ __forceinline__ void pack_word(const PackArgs& a, in
     const int64_t row = w / a.per_row;
     const int g = int(w % a.per_row), c = g * 8;
     const Token t = row < a.rows ? token_of(a.ids, row, a.table_rows) : Token{-1, false};
-    if (a.targets && c == 0) {
-        a.targets[row] = t.target;
-        a.rest[row] = 0.f;
-    }
+    for (int64_t i = w; i < a.n_zeros; i += a.words) a.zeros[i] = 0;
     const bool in = t.live && c < a.cols;
     const uint8_t* src = a.src + row * a.stride * (D == kBF16 ? 2 : 4);
     uint8_t* dst = a.dst + int64_t(g >> 3) * a.block + row * 128 + (g & 7) * 16;
@@ -930,6 +931,30 @@ __global__ __launch_bounds__(256) void k_head_empty(RowArgs a) {
 
 // ---- backward ----
 
+// What rounding to bf16 took from the large entries of dz, a token's in no
+// order: the k-th at [k][token].  A token that counts more than kMaxRests (the
+// records were not of these operands) has none.
+constexpr int kListRows = 128;
+struct Rests {
+    int* counts;      // [token]
+    int* groups;      // [128 rows of the table]: entries there, those of tokens that have none among them
+    int* rows;        // [kMaxRests][token]: of the table
+    float* values;
+    int64_t tokens;   // from k to k + 1
+    __device__ __forceinline__ int count(int64_t token) const {
+        const int c = counts[token];
+        return c <= kMaxRests ? c : 0;
+    }
+    // (the order of arrival is settled where they are read)
+    __device__ __forceinline__ void add(int64_t token, int row, float value) const {
+        const int k = atomicAdd(&counts[token], 1);
+        if (k >= kMaxRests) return;
+        atomicAdd(&groups[row / kListRows], 1);
+        rows[k * tokens + token] = row;
+        values[k * tokens + token] = value;
+    }
+};
+
 struct DzArgs {
     LogitArgs l;
     const mfsdp_head_record* records;
@@ -939,7 +964,7 @@ struct DzArgs {
     int64_t block;     // bytes from 64 rows to the next 64
     int planes;
     int64_t plane;
-    float* rest;       // [n]: what rounding took from the target's dz (one plane)
+    Rests rests;       // one plane
 };
 
 // dz of a tile: formed in the accumulators, staged in LDS as [token][row of
@@ -965,7 +990,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
 #pragma unroll
     for (int ni = 0; ni < S::MN; ++ni) {
         const int64_t token = int64_t(tj) * BT + wn * S::WTN + ni * 32 + frow;
-        float m = 0.f, ls = 0.f, b = 0.f, c = 0.f, hit = 0.f;
+        float m = 0.f, ls = 0.f, b = 0.f, c = 0.f, hit = 0.f, least = INFINITY;
         int t = -1;
         bool live = false;
         if (token < a.n) {
@@ -979,6 +1004,12 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
             b = d.scale * (d.dentropy ? __builtin_fmaf(dh, nat(ls - r.wsum / r.sum), up) : up);
             if (!(r.sum > 0.f)) b = NAN;
             c = d.scale * dh * kLn2;
+            if (d.planes == 1 && live) {
+                // sum |dz_j| is at most |scale| (|dlogp| 2 (1 - p_t) + |dH| 2 H); 1 - p_t and H as far as roundings leave them
+                const float pt = r.found ? exp2_fast(fminf((r.target - m) - ls, 0.f)) : 1.f;
+                const float h = d.dentropy ? fmaxf(nat(ls - r.wsum / r.sum), 0x1p-15f) : 0.f;
+                least = 2.f * kShare * fabsf(d.scale) * (fabsf(up) * fmaxf(1.f - pt, 0x1p-15f) + fabsf(dh) * h);
+            }
             if (tok.target >= 0 && r.found && live) {
                 t = tok.target - row0;
                 hit = d.scale * up;
@@ -996,12 +1027,25 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
             });
         if (__ballot(t >= 0 && t < S::WTM))
             each_row<S::MM>(fhalf, [&](int mi, int e, int r) {
-                if (r == t) {
-                    const float v = acc[mi][ni][e] + hit;
-                    acc[mi][ni][e] = v;
-                    if (d.planes == 1) d.rest[token] = fabsf(v) < INFINITY ? v - bf16_to_f32(f32_to_bf16(v)) : 0.f;
-                }
+                if (r == t) acc[mi][ni][e] += hit;
             });
+        float most = 0.f;
+        each_row<S::MM>(fhalf, [&](int mi, int e, int) { most = fmaxf(most, fabsf(acc[mi][ni][e])); });
+        if (!__ballot(most >= least)) continue;
+        // the large ones, a bit each; then one a lane at a time
+        uint64_t large = 0;
+        each_row<S::MM>(fhalf, [&](int mi, int e, int) {
+            large |= fabsf(acc[mi][ni][e]) >= least ? uint64_t(1) << (mi * 16 + e) : 0;
+        });
+        while (__ballot(large != 0)) {
+            const int q = large ? __ffsll(static_cast<unsigned long long>(large)) - 1 : -1;
+            large &= large - 1;
+            float v = 0.f;
+            each_row<S::MM>(fhalf, [&](int mi, int e, int) { v = q == mi * 16 + e ? acc[mi][ni][e] : v; });
+            const float rest = v - bf16_to_f32(f32_to_bf16(v));  // 0, NaN and infinite ones are none
+            if (q >= 0 && fabsf(rest) > 0.f && fabsf(rest) < INFINITY)
+                d.rests.add(token, row0 + (q >> 4) * 32 + (q >> 2 & 3) * 8 + fhalf * 4 + (q & 3), rest);
+        }
     }
     for (int plane = 0; plane < d.planes; ++plane) {
         __syncthreads();  // the operands' stages, or the plane before, have been read
@@ -1169,8 +1213,7 @@ struct DxArgs {
     int tp, tq;           // tiles along the columns and the batch
     int stages, splits;   // of the contraction over the vocabulary, and the parts it is cut into
     Ids ids;
-    const int* targets;
-    const float* rest;    // NULL, or the rests of the targets' dz (the table then has one plane)
+    const float* rests;   // NULL, or [n][ld]: what the large entries' rests add
     uint8_t* dx;
     int64_t stride;
     int vector;
@@ -1202,33 +1245,26 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
     const int k0 = int(int64_t(a.stages) * split / a.splits), k1 = int(int64_t(a.stages) * (split + 1) / a.splits);
     f32x16_t acc[S::MM][S::MN];
     tile_loop<true, false, BT>(acc, a.table, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, k0, k1, lds);
-    struct Extra {
-        float rest;
-        Eight<kBF16> w;
-    };
     walk_columns<BT>(
         acc, lds, [](int, const Staging<BT>&) {},
         [&](int c, int r) {
             const int64_t token = int64_t(tj) * BT + c;
             const int col = ti * BT + r;
-            Extra x = {};
-            if (a.rest && split == 0 && token < a.n && col < a.cols) {
-                x.rest = a.rest[token];
-                const int t = a.targets[token];  // columns past the last are inside their block
-                if (t >= 0) x.w.load(a.table.at(t, col), 0, 8, true);
-            }
+            Eight<kF32> x = {};
+            if (a.rests && a.splits == 1 && token < a.n && col < a.cols)
+                x.load(reinterpret_cast<const uint8_t*>(a.rests + token * a.ld), col, 8, true);  // ld: of 8
             return x;
         },
-        [&](int c, int r, const Extra& x, Values v) {
+        [&](int c, int r, const Eight<kF32>& x, Values v) {
             const int64_t token = int64_t(tj) * BT + c;
             const int col = ti * BT + r;
             if (token >= a.n || col >= a.cols) return;
-            if (x.rest != 0.f) v = fma8(x.rest, x.w.get(), v);
             if (a.splits > 1) {
                 float4* to = reinterpret_cast<float4*>(a.sums + (split * a.n + token) * a.ld + col);  // ld: of 8
                 to[0] = v.a;
                 to[1] = v.b;
             } else {
+                if (a.rests) v = fma8(1.f, x.get(), v);
                 if (!token_of(a.ids, token, a.rows).live) v = Values{};
                 put8<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
             }
@@ -1249,6 +1285,10 @@ __global__ __launch_bounds__(256) void k_head_dx_sum(DxArgs a) {
     const int col = int(w % per) * 8;
     const bool here = token < a.n;
     Values v = {};
+    if (here && a.rests && slice == 0) {
+        const float4* from = reinterpret_cast<const float4*>(a.rests + token * a.ld + col);
+        v = Values{from[0], from[1]};
+    }
     if (here) {
         const int end = a.splits * (slice + 1) / SLICES;
 #pragma unroll 8
@@ -1269,6 +1309,44 @@ __global__ __launch_bounds__(256) void k_head_dx_sum(DxArgs a) {
     put8<D>(a.dx + token * a.stride * (D == kBF16 ? 2 : 4), col, a.cols - col, a.vector, v);
 }
 
+// What the rests of a token's large entries add to dx, a wave a token: times
+// their rows of the table, in the rows' order, so that sums do not depend on
+// which was found first.  HBM: the rows' bytes, and n x cols fp32 written.
+struct GatherArgs {
+    Rests rests;
+    Operand table;     // one plane
+    int64_t n;
+    int64_t ld;        // of 8, and at most whole column blocks
+    float* out;        // [n][ld]
+    uint32_t blocks;
+};
+__device__ __forceinline__ void gather_block(const GatherArgs& a, uint32_t block) {
+    const int lane = threadIdx.x & 63;
+    const int64_t token = int64_t(block) * 4 + uni(int(threadIdx.x) >> 6);
+    if (token >= a.n) return;
+    const int count = uni(a.rests.count(token));
+    static_assert(kMaxRests <= 64, "a lane an entry");
+    int row = lane < count ? a.rests.rows[lane * a.rests.tokens + token] : 0;
+    float value = lane < count ? a.rests.values[lane * a.rests.tokens + token] : 0.f;
+    int place = 0;  // among the rows, which differ
+    for (int k = 0; k < count; ++k) place += __builtin_amdgcn_readlane(row, k) < row;
+    if (lane >= count) place = lane;
+    row = __builtin_amdgcn_ds_permute(place * 4, row);
+    value = __int_as_float(__builtin_amdgcn_ds_permute(place * 4, __float_as_int(value)));
+    for (int64_t col = lane * 8; col < a.ld; col += 512) {
+        Values v = {};
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+            Eight<kBF16> w;
+            w.load(a.table.at(__builtin_amdgcn_readlane(row, k), int(col)), 0, 8, true);
+            v = fma8(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), k)), w.get(), v);
+        }
+        float4* to = reinterpret_cast<float4*>(a.out + token * a.ld + col);
+        to[0] = v.a;
+        to[1] = v.b;
+    }
+}
+
 struct DwArgs {
     Operand turned, dz;  // x with its columns as rows
     Operand x;
@@ -1276,65 +1354,100 @@ struct DwArgs {
     int rows, cols;
     int tp, tq;          // tiles along the columns and the vocabulary
     int stages;          // of the contraction over the batch
-    const int* starts;   // of the lists below
-    const uint32_t* list;
-    const float* rest;   // NULL, or the rests of the targets' dz (x then has one plane)
+    const int2* bounds;  // NULL, or of the lists below (x then has one plane)
+    const uint2* list;
     uint8_t* grad;
     int vector;
     int add;
 };
 
-// The tokens whose target lies in each group of 128 rows of the table, in
-// order: list[starts[g]] .. list[starts[g + 1] - 1], each the row in its group
-// << 24 | the token (at most 2^22 of them).  A block a group looks through all
-// targets: once for those of the groups before, whose number is the list's
-// start, and once for its own.
-constexpr int kListRows = 128;
+// The large entries of dz in each group of 128 rows of the table, in an order
+// that sizes and the entries alone fix: list[bounds[g].x] .. list[bounds[g].y -
+// 1], each the row in its group << 24 | the token (at most 2^22 of them), and
+// the rest.  A block a group looks through all tokens, 256 at a time, each
+// token's entries from the lowest row up; the first two of the next 256 are on
+// their way meanwhile.
 struct ListArgs {
-    const int* targets;
+    Rests rests;
     int n, rows;
-    int* starts;
-    uint32_t* list;
+    int2* bounds;
+    uint2* list;
 };
 __device__ __forceinline__ void list_block(const ListArgs& a, uint32_t block) {
     __shared__ int counts[4];
     const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
     const int first = int(block) * kListRows;
+    struct Ahead {
+        int count, rows[2];
+    };
+    auto load = [&](int i) {
+        Ahead h = {0, {0, 0}};
+        if (i < a.n) h = Ahead{a.rests.counts[i], {a.rests.rows[i], a.rests.rows[a.rests.tokens + i]}};  // held or not
+        return h;
+    };
+    Ahead next_ones = load(threadIdx.x);
     int below = 0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < a.n; i += 256) below += uint32_t(a.targets[i]) < uint32_t(first);
+    for (int g = threadIdx.x; g < int(block); g += 256) below += a.rests.groups[g];
     for (int off = 1; off < 64; off <<= 1) below += __shfl_xor(below, off, 64);
     if (lane == 0) counts[wave] = below;
     __syncthreads();
-    int at = counts[0] + counts[1] + counts[2] + counts[3];
-    if (threadIdx.x == 0) a.starts[block] = at;
-    if (first >= a.rows) return;  // the block past the last group: its start is the last one's end
+    const int start = counts[0] + counts[1] + counts[2] + counts[3];
+    int at = start;
     for (int i0 = 0; i0 < a.n; i0 += 256) {
         const int i = i0 + int(threadIdx.x);
-        const uint32_t c = i < a.n ? uint32_t(a.targets[i] - first) : ~0u;  // no target: -1 - first
-        const bool hit = c < uint32_t(kListRows);
-        const uint64_t mask = __ballot(hit);
-        __syncthreads();
-        if (lane == 0) counts[wave] = __popcll(mask);
-        __syncthreads();
-        int before = at;
-        for (int w = 0; w < wave; ++w) before += counts[w];
-        if (hit) a.list[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] = c << 24 | uint32_t(i);
-        at += counts[0] + counts[1] + counts[2] + counts[3];
+        const Ahead h = next_ones;
+        next_ones = load(i + 256);
+        const int c = h.count <= kMaxRests ? h.count : 0;
+        int last = -1;  // the row in the group that this token's entries up to it are listed
+        for (bool more = true; more;) {
+            int next = kListRows, from = 0, left = 0;
+            auto look = [&](int k, int row) {
+                const int r = row - first;
+                if (r <= last || r >= kListRows) return;
+                ++left;
+                if (r < next) {
+                    next = r;
+                    from = k;
+                }
+            };
+            if (c > 0) look(0, h.rows[0]);
+            if (c > 1) look(1, h.rows[1]);
+            for (int k = 2; k < c; ++k) look(k, a.rests.rows[k * a.rests.tokens + i]);
+            const uint64_t mask = __ballot(left > 0), again = __ballot(left > 1);
+            __syncthreads();
+            if (lane == 0) counts[wave] = __popcll(mask) | (again ? 1 << 16 : 0);
+            __syncthreads();
+            int before = at, all = 0;
+            for (int w = 0; w < 4; ++w) {
+                if (w < wave) before += counts[w] & 0xffff;
+                all += counts[w];
+            }
+            if (left > 0)
+                a.list[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
+                    make_uint2(uint32_t(next) << 24 | uint32_t(i), __float_as_uint(a.rests.values[from * a.rests.tokens + i]));
+            at += all & 0xffff;
+            more = all >> 16;
+            last = next;
+        }
     }
+    if (threadIdx.x == 0) a.bounds[block] = make_int2(start, at);
 }
 
-// What dW needs besides dz, in one launch: x turned over, and the lists.
-__global__ __launch_bounds__(256) void k_head_turn(TurnArgs t, ListArgs l) {
-    if (blockIdx.x < t.blocks)
-        turn_block(t, blockIdx.x);
+// What dx and dW need besides dz, in one launch: the rests' part of dx, x
+// turned over, and the lists.
+__global__ __launch_bounds__(256) void k_head_turn(TurnArgs t, ListArgs l, GatherArgs g) {
+    uint32_t block = blockIdx.x;
+    if (block < g.blocks) return gather_block(g, block);
+    block -= g.blocks;
+    if (block < t.blocks)
+        turn_block(t, block);
     else
-        list_block(l, blockIdx.x - t.blocks);
+        list_block(l, block - t.blocks);
 }
 
-// What rounding took from the targets' dz, times x, added to the staged rows
-// of the table's gradient: the wave that a row falls to (row mod 4) adds its
-// entries in the list's order, so sums do not depend on timing.
+// What rounding took from the large entries of dz, times x, added to the staged
+// rows of the table's gradient: the wave that a row falls to (row mod 4) adds
+// its entries in the list's order, so sums do not depend on timing.
 template <int BT>
 __device__ __forceinline__ void add_rests(const DwArgs& a, const Staging<BT>& st, int first, int end, int first_col) {
     static_assert(Staging<BT>::COLS == kListRows, "a pass is a group");
@@ -1342,8 +1455,8 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, const Staging<BT>& st
     const int col = first_col + lane * 4;
     const bool holds = lane * 4 < BT && col < a.cols;
     for (int e0 = first; e0 < end; e0 += 64) {
-        const uint32_t mine = e0 + lane < end ? a.list[e0 + lane] : 0u;
-        uint64_t own = __ballot(e0 + lane < end && int(mine >> 24 & 3) == wave);
+        const uint2 mine = e0 + lane < end ? a.list[e0 + lane] : make_uint2(0u, 0u);
+        uint64_t own = __ballot(e0 + lane < end && int(mine.x >> 24 & 3) == wave);
         while (own) {  // eight entries' loads on their way: text has rows with hundreds of tokens
             constexpr int N = 8;
             uint2 x[N];
@@ -1355,12 +1468,13 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, const Staging<BT>& st
                 x[u] = make_uint2(0u, 0u);
                 rest[u] = 0.f;
                 if (own) {
-                    const uint32_t entry = __builtin_amdgcn_readlane(mine, __ffsll(static_cast<unsigned long long>(own)) - 1);
+                    const int from = __ffsll(static_cast<unsigned long long>(own)) - 1;
+                    const uint32_t entry = __builtin_amdgcn_readlane(mine.x, from);
                     own &= own - 1;
                     const int64_t token = entry & 0xffffff;
                     c[u] = int(entry >> 24);
                     if (holds) x[u] = *reinterpret_cast<const uint2*>(a.x.at(token, col));
-                    rest[u] = a.rest[token];
+                    rest[u] = __uint_as_float(__builtin_amdgcn_readlane(mine.y, from));
                 }
             }
 #pragma unroll
@@ -1385,11 +1499,13 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[Pipe<BT, 4>::BYTES];
     int ti, tj;
     tile_of(int(blockIdx.x), a.tp * a.tq, a.tp, a.tq, ti, tj);
-    int starts[Staging<BT>::PASSES + 1] = {};
-    if (a.rest)
+    int2 bounds[Staging<BT>::PASSES] = {};
+    if (a.bounds)
 #pragma unroll
-        for (int h = 0; h <= Staging<BT>::PASSES; ++h)
-            starts[h] = uni(a.starts[min(tj * Staging<BT>::PASSES + h, (a.rows + kListRows - 1) / kListRows)]);
+        for (int h = 0; h < Staging<BT>::PASSES; ++h) {
+            const int g = tj * Staging<BT>::PASSES + h;
+            if (g * kListRows < a.rows) bounds[h] = make_int2(uni(a.bounds[g].x), uni(a.bounds[g].y));
+        }
     f32x16_t acc[S::MM][S::MN];
     tile_loop<false, true, BT>(acc, a.turned, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
     const int left = a.cols - ti * BT, under = a.rows - tj * BT;  // columns and rows from the tile's first on
@@ -1398,7 +1514,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     walk_columns<BT>(
         acc, lds,
         [&](int h, const Staging<BT>& st) {
-            if (a.rest) add_rests<BT>(a, st, starts[h], starts[h + 1], ti * BT);
+            if (a.bounds) add_rests<BT>(a, st, bounds[h].x, bounds[h].y, ti * BT);
         },
         [&](int c, int r) {
             Eight<D> old = {};
@@ -1506,7 +1622,7 @@ struct HeadShape {
     int64_t n_parts;
     int tile_dw;
     DxCut dx;
-    uint64_t x, turned, table, parts, targets, logits, dz, rest, starts, list, sums, total;
+    uint64_t x, turned, table, parts, targets, logits, dz, counts, rows, values, bounds, list, sums, rests, total;
     uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane (turned over: as x)
 };
 
@@ -1537,11 +1653,15 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
     // few tokens read x and the table where they lie
     s.x = region(s.few ? 0 : uint64_t(s.x_planes) * s.x_plane);
     s.table = region(s.few || s.direct ? 0 : uint64_t(s.table_planes) * s.table_plane);
-    s.targets = region(uint64_t(s.np) * 4);
     if (grad) {
-        s.rest = region(uint64_t(s.np) * 4);
-        s.starts = region(uint64_t(ceil_div(e.rows, kListRows) + 1) * 4);
-        s.list = region(uint64_t(s.np) * 4);
+        if (s.dz_planes == 1) {
+            s.counts = region((uint64_t(s.np) + uint64_t(ceil_div(e.rows, kListRows))) * 4);  // of tokens, then of groups
+            s.rows = region(uint64_t(s.np) * kMaxRests * 4);
+            s.values = region(uint64_t(s.np) * kMaxRests * 4);
+            s.bounds = region(uint64_t(ceil_div(e.rows, kListRows)) * 8);
+            s.list = region(uint64_t(s.np) * kMaxRests * 8);
+            s.rests = region(uint64_t(n) * align_up(uint64_t(e.cols), 8) * 4);
+        }
         s.turned = region(uint64_t(s.x_planes) * s.x_plane);
         s.dz_plane = uint64_t(s.np) * uint64_t(s.vp) * 2;
         s.dz = region(uint64_t(s.dz_planes) * s.dz_plane);
@@ -1550,6 +1670,7 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
         s.tile_dw = pick_tile(e.rows, e.cols, int(ceil_div(n, 64)) * (of_dw == 9 ? 6 : of_dw));
         s.sums = region(uint64_t(dx_sum_rows(e, n)) * align_up(uint64_t(e.cols), 8) * 4);
     } else {
+        s.targets = region(uint64_t(s.np) * 4);
         // the most that either edge, or a smaller batch in another form, needs
         s.parts = region(16 * std::max(uint64_t(2 * ceil_div(e.rows, 128)) * uint64_t(n),
                                        uint64_t(ceil_div(e.rows, 32)) * uint64_t(std::min(n, kFewTokens))));
@@ -1627,10 +1748,7 @@ void launch_pack(const PackArgs& a, int type, hipStream_t stream) {
         b.dst = a.dst + row * 128;
         b.rows = std::max<int64_t>(0, a.rows - row);
         if (a.ids.ids) b.ids.ids = static_cast<const uint8_t*>(a.ids.ids) + row * (a.ids.type == MFSDP_I64 ? 8 : 4);
-        if (a.targets) {
-            b.targets = a.targets + row;
-            b.rest = a.rest + row;
-        }
+        if (w > 0) b.n_zeros = 0;
         launch_pack(b, type, PackArgs{}, type, stream);
     }
 }
@@ -1659,8 +1777,8 @@ LogitArgs logit_args(const mfsdp_entry& e, const HeadShape& s, const Batch& b) {
 }
 
 // The batch, and a table that cannot be read in place, in the tile loop's
-// layout.  rest: also the targets' rows, and zeros there.
-void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, bool rest, LogitArgs& a) {
+// layout, and n_zeros words of zeros.
+void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, int* zeros, int64_t n_zeros, LogitArgs& a) {
     PackArgs p = {};
     p.src = static_cast<const uint8_t*>(b.x);
     p.dst = b.ws + s.x;
@@ -1673,10 +1791,8 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
     p.cols = int(e.cols);
     p.ids = b.ids;
     p.table_rows = int(e.rows);
-    if (rest) {
-        p.targets = reinterpret_cast<int*>(b.ws + s.targets);
-        p.rest = reinterpret_cast<float*>(b.ws + s.rest);
-    }
+    p.zeros = zeros;
+    p.n_zeros = n_zeros;
     const PackArgs x = p;
     a.x = Operand{p.dst, 128, p.block, s.np, s.stages, s.x_planes, p.plane};
     a.table = Operand{b.table, e.cols * 2, 128, e.rows, s.stages, 1, 0};
@@ -1689,7 +1805,7 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, boo
     p.plane = int64_t(s.table_plane);
     p.words = e.rows * p.per_row;
     p.ids = Ids{};
-    p.targets = nullptr;
+    p.n_zeros = 0;
     if (x.words + p.words <= kMostWords) {
         launch_pack(x, b.x_type, p, e.dtype, b.stream);
     } else {
@@ -1739,7 +1855,7 @@ hipError_t launch_logprob(const mfsdp_entry& e, const HeadShape& s, const Batch&
         else
             b.x_type == kBF16 ? launch_few<kF32, kBF16>(f, b.stream) : launch_few<kF32, kF32>(f, b.stream);
     } else {
-        pack_operands(e, s, b, false, a);
+        pack_operands(e, s, b, nullptr, 0, a);
         const dim3 grid(uint32_t(a.tp) * uint32_t(a.tq));
         if (s.tile == 256)
             k_head_logits<256><<<grid, dim3(256), 0, b.stream>>>(a);
@@ -1792,9 +1908,17 @@ template <int D> void launch_dw(const DwArgs& a, int tile, hipStream_t stream) {
 }
 
 hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b, const GradOut& g) {
+    const bool kept = s.dz_planes == 1;  // what rounding takes from large entries
+    const int64_t ld = int64_t(align_up(uint64_t(e.cols), 8));
+    const int64_t groups = kept ? ceil_div(e.rows, kListRows) : 0;
+    Rests rests = {};
+    if (kept) {
+        int* counts = reinterpret_cast<int*>(b.ws + s.counts);
+        rests = Rests{counts, counts + s.np, reinterpret_cast<int*>(b.ws + s.rows), reinterpret_cast<float*>(b.ws + s.values), s.np};
+    }
     DzArgs d = {};
     d.l = logit_args(e, s, b);
-    pack_operands(e, s, b, true, d.l);
+    pack_operands(e, s, b, rests.counts, kept ? s.np + groups : 0, d.l);
     d.records = g.records;
     d.dlogp = g.dlogp;
     d.dentropy = g.dentropy;
@@ -1803,7 +1927,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     d.block = s.np * 128;
     d.planes = s.dz_planes;
     d.plane = int64_t(s.dz_plane);
-    d.rest = reinterpret_cast<float*>(b.ws + s.rest);
+    d.rests = rests;
     const dim3 grid(uint32_t(d.l.tp) * uint32_t(d.l.tq));
     if (s.tile == 256)
         k_head_dz<256><<<grid, dim3(256), 0, b.stream>>>(d);
@@ -1811,8 +1935,27 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         k_head_dz<128><<<grid, dim3(256), 0, b.stream>>>(d);
     // tokens and vocabulary rows that dz was written for
     const Operand dz = {d.dz, 128, d.block, int64_t(d.l.tq) * s.tile, d.l.tp * (s.tile / 64), s.dz_planes, d.plane};
-    const int* targets = reinterpret_cast<const int*>(b.ws + s.targets);
-    const float* rest = s.dz_planes == 1 ? d.rest : nullptr;
+    TurnArgs t = {};
+    ListArgs l = {};
+    GatherArgs of_dx = {};
+    int64_t blocks = 0;  // of x turned over, and the lists
+    if (g.grad) {
+        const int64_t kp = int64_t(s.stages) * 64;
+        const uint32_t across = uint32_t(s.np / 64);
+        t = TurnArgs{d.l.x.base, b.ws + s.turned, d.l.x.block, kp * 128, d.l.x.plane, d.l.x.plane,
+                     across, uint32_t(s.stages), across * uint32_t(s.stages) * uint32_t(s.x_planes)};
+        l = ListArgs{rests, int(b.n), int(e.rows), reinterpret_cast<int2*>(b.ws + s.bounds),
+                     reinterpret_cast<uint2*>(b.ws + s.list)};
+        blocks = int64_t(t.blocks) + groups;
+    }
+    if (g.dx && kept)
+        of_dx = GatherArgs{rests, d.l.table, b.n, ld, reinterpret_cast<float*>(b.ws + s.rests), uint32_t(ceil_div(b.n, 4))};
+    if (blocks + of_dx.blocks > kMaxTiles) {
+        k_head_turn<<<dim3(of_dx.blocks), dim3(256), 0, b.stream>>>(TurnArgs{}, ListArgs{}, of_dx);
+        of_dx.blocks = 0;
+    }
+    blocks += of_dx.blocks;
+    if (blocks > 0) k_head_turn<<<dim3(uint32_t(blocks)), dim3(256), 0, b.stream>>>(t, l, of_dx);
     if (g.dx) {
         DxArgs a = {};
         const int tile = s.dx.tile, xs = b.x_type == kBF16 ? 2 : 4;
@@ -1826,25 +1969,17 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.stages = int(ceil_div(e.rows, 64));
         a.splits = s.dx.splits;
         a.ids = b.ids;
-        a.targets = targets;
-        a.rest = rest;
+        a.rests = kept ? reinterpret_cast<const float*>(b.ws + s.rests) : nullptr;
         a.dx = g.dx;
         a.stride = g.dx_stride;
         a.vector = !misaligned(g.dx, 16) && g.dx_stride * xs % 16 == 0;
         a.sums = reinterpret_cast<float*>(b.ws + s.sums);
-        a.ld = int64_t(align_up(uint64_t(e.cols), 8));
+        a.ld = ld;
         b.x_type == kBF16 ? launch_dx<kBF16>(a, tile, b.stream) : launch_dx<kF32>(a, tile, b.stream);
     }
     if (g.grad) {
         DwArgs a = {};
-        const int64_t kp = int64_t(s.stages) * 64;
-        const uint32_t across = uint32_t(s.np / 64), groups = rest ? uint32_t(ceil_div(e.rows, kListRows) + 1) : 0;
-        const TurnArgs t = {d.l.x.base, b.ws + s.turned, d.l.x.block, kp * 128, d.l.x.plane, d.l.x.plane,
-                            across, uint32_t(s.stages), across * uint32_t(s.stages) * uint32_t(s.x_planes)};
-        const ListArgs l = {targets, int(b.n), int(e.rows), reinterpret_cast<int*>(b.ws + s.starts),
-                            reinterpret_cast<uint32_t*>(b.ws + s.list)};
-        k_head_turn<<<dim3(t.blocks + groups), dim3(256), 0, b.stream>>>(t, l);
-        a.turned = Operand{t.dst, 128, t.dst_block, kp, int(s.np / 64), s.x_planes, t.dst_plane};
+        a.turned = Operand{t.dst, 128, t.dst_block, int64_t(s.stages) * 64, int(s.np / 64), s.x_planes, t.dst_plane};
         a.x = d.l.x;
         a.dz = dz;
         a.n = b.n;
@@ -1853,9 +1988,8 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.tp = int(ceil_div(e.cols, s.tile_dw));
         a.tq = int(ceil_div(e.rows, s.tile_dw));
         a.stages = int(ceil_div(b.n, 64));
-        a.starts = reinterpret_cast<int*>(b.ws + s.starts);
-        a.list = reinterpret_cast<uint32_t*>(b.ws + s.list);
-        a.rest = rest;
+        a.bounds = kept ? l.bounds : nullptr;
+        a.list = l.list;
         a.grad = g.grad;
         a.vector = e.cols * (e.dtype == kBF16 ? 2 : 4) % 16 == 0;  // the entry is 16-byte aligned
         a.add = g.add;

@@ -1,0 +1,155 @@
+"""Gradients of the output head where a few tokens carry a row's probability, the
+target among them or not: what rounding dz to bf16 leaves, against 64 bits.
+
+An entry of dz from 1/32 of its row's sum of magnitudes on is as good as fp32,
+the others are rounded: errors of at most 2^-8 of themselves, independent, of
+mean 0.  The elementwise bound adds them up.  A sharper one is for the component
+of a row's error along the row itself, <got - want, want> / <want, want>, to
+which independent roundings add little, and the rounding of one entry that
+carries the row all of itself: six standard deviations of those roundings, each
+1 / sqrt(3) of its largest error, as one of uniform errors has.
+
+A row that is one factor times bf16 values has roundings to its own type that
+are not independent (of a factor just below 1, nearly all go up).  For dx, whose
+rows are of that kind only where the factor is as good as fp32, the difference
+is taken from the rounded row; the table's gradient is added to random values.
+"""
+
+import math
+
+import pytest
+
+from matrix_optimizer_owner_amd import binding as B
+from tests.head_ref import Reference
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests.test_head_gpu import Head, stream  # noqa: E402
+
+H = 2.0 ** -8
+
+
+def peaked(rows, cols, n, peaks, seed=3):
+    """A table, and x whose logits are large at `peaks` rows of the table a token; (values, x, those rows)."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    values = (torch.randn(rows, cols, generator=gen, device="cuda") / math.sqrt(cols)).bfloat16()
+    at = torch.randint(0, rows, (n, peaks), generator=gen, device="cuda")
+    height = 9 + 4 * torch.rand(n, 1, 1, generator=gen, device="cuda") + torch.rand(n, peaks, 1, generator=gen, device="cuda")
+    x = (values.float()[at] * height).sum(1).bfloat16()
+    return values, x, at
+
+
+def along(got, whole, want, w, e, bound):
+    """The component of got - whole along `want` in each row, against six deviations of the roundings e of `w`'s coefficients
+    and of `whole` to bf16, and the rest of the bound."""
+    size = (want * want).sum(1)
+    own = (H * whole * want / math.sqrt(3)).square().sum(1)
+    dz = ((e / math.sqrt(3)) * (want @ w.t())).square().sum(1)
+    off = ((got.double() - whole) * want).sum(1).abs()
+    tol = 6 * (own + dz).sqrt() + (bound * want.abs()).sum(1)
+    far = (off > tol) & (size > 0)
+    assert not far.any(), (int(far.sum()), (off / size)[far][:4], (tol / size)[far][:4])
+
+
+class Want:
+    """Gradients over the table rows lo .. hi - 1 of a reference, what the roundings of dz may be, and the rest's bounds."""
+
+    def __init__(self, ref, x, dlogp, dent, lo=0, hi=None):
+        part = slice(lo, hi)
+        found = ref.target >= 0
+        _, self.ex, _, ew = ref.grads(dlogp, dent, torch.float32, found=found)
+        self.ew = ew[part]
+        a = torch.where(found, dlogp.double(), 0.0)[:, None]
+        b = dent.double()[:, None] if dent is not None else torch.zeros_like(a)
+        hot = torch.zeros_like(ref.p)
+        hot[found, ref.target[found]] = 1.0
+        dz = ref.scale * (a * (hot - ref.p) - b * ref.p * (ref.lp * math.log(2) + ref.entropy))
+        pt = torch.where(found[:, None], (ref.p * hot).sum(1, keepdim=True), 1.0)
+        share = 2 / 32 * abs(ref.scale) * (a.abs() * (1 - pt).clamp_min(2.0 ** -15) + b.abs() * ref.entropy.clamp_min(2.0 ** -15))
+        dz = dz[:, part]
+        self.w, self.x = ref.w[part], x.double()
+        self.e = torch.where(dz.abs() >= share * 1.01, 0.0, H * 1.01 * dz.abs())
+        self.dx, self.dw = dz @ self.w, dz.t() @ self.x
+        gen = torch.Generator(device="cuda").manual_seed(77)
+        size = self.dw.square().mean(1, keepdim=True).sqrt()
+        self.before = (torch.randn(self.dw.shape, generator=gen, device="cuda") * size).bfloat16()
+
+    def check(self, dx, dw):
+        """dw was added to `before`."""
+        whole = self.before.double() + self.dw
+        for got, want, e, m, small in ((dx, self.dx, self.e, self.w, self.ex), (dw, whole, self.e.t(), self.x, self.ew)):
+            bound = small + e @ m.abs() + 2.0 ** -24 * want.abs()
+            bad = (got.double() - want).abs() > bound + H * (want.abs() + bound)
+            assert not bad.any(), int(bad.sum())
+        along(dx, self.dx.bfloat16().double(), self.dx, self.w, self.e, self.ex)
+        along(dw, whole, self.dw, self.x, self.e.t(), self.ew + 2.0 ** -24 * whole.abs())
+
+
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("target", ["peak", "other", "none", "mixed"])
+@pytest.mark.parametrize("peaks", [1, 2, 5, 20])
+@pytest.mark.parametrize("rows,cols,n", [(3001, 256, 300), (700, 200, 40), (7690, 1030, 1490)])
+def test_peaked_rows(rows, cols, n, peaks, target, entropy):
+    values, x, at = peaked(rows, cols, n, peaks)
+    h = Head(rows, cols, values=values)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    ids = at[:, 0].clone() if target == "peak" else torch.randint(0, rows, (n,), generator=gen, device="cuda")
+    if target == "mixed":
+        ids = torch.where(torch.rand(n, generator=gen, device="cuda") < 0.5, at[:, 0], ids)
+        ids[::7] = rows + 5
+    if target == "none":
+        ids = None
+    out = h.logprob(x, ids, scale=1.1)
+    t = torch.full((n,), -1, device="cuda") if ids is None else torch.where(ids < rows, ids, -1)
+    ref = Reference(x, h.w, t, torch.ones(n, dtype=torch.bool, device="cuda"), 1.1)
+    ref.check_forward(out["logp"], out["entropy"])
+    dlogp = torch.randn(n, generator=gen, device="cuda")
+    dent = torch.randn(n, generator=gen, device="cuda") if entropy else None
+    want = Want(ref, x, dlogp, dent)
+    dx, dw = h.grad(x, out["records"], dlogp, dent, ids, 1.1, add=want.before)
+    want.check(dx, dw)
+    again = h.grad(x, out["records"], dlogp, dent, ids, 1.1, add=want.before)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+@pytest.mark.parametrize("peaks", [1, 3])
+def test_target_in_another_entry(peaks):
+    rows, cols, n = 2002, 256, 260
+    values, x, at = peaked(rows, cols, n, peaks)
+    h = Head(rows, cols, values=values, shards=2)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    # peaks in either half, the target in the other one
+    ids = (at[:, 0] + rows // 2) % rows
+    parts = [h.logprob(x, ids, entry=e)["records"] for e in range(2)]
+    both = torch.cat([p.reshape(-1) for p in parts])
+    records = torch.empty(n, 6, device="cuda")
+    B.head_total(both.data_ptr(), 2, n, records.data_ptr(), stream=stream())
+    ref = Reference(x, h.w, ids, torch.ones(n, dtype=torch.bool, device="cuda"), 1.0)
+    dlogp = torch.randn(n, generator=gen, device="cuda")
+    for e in range(2):
+        want = Want(ref, x, dlogp, None, h.firsts[e], h.firsts[e] + h.sizes[e])
+        want.check(*h.grad(x, records, dlogp, None, ids, entry=e, add=want.before))
+
+
+def test_records_of_other_operands():
+    """More entries count as large than a row of the right records can have: such a row is rounded as any other, and results
+    repeat."""
+    rows, cols, n = 1500, 128, 200
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    h = Head(rows, cols)
+    x = torch.randn(n, cols, generator=gen, device="cuda").bfloat16()
+    ids = torch.randint(0, rows, (n,), generator=gen, device="cuda")
+    records = h.logprob(x, ids)["records"]
+    records[:, 1] = 1.0  # a sum of 1: every p is far above what it was, and the target's too
+    records[:, 3] = records[:, 0]
+    dlogp = torch.ones(n, device="cuda")
+    dx, dw = h.grad(x, records, dlogp, None, ids)
+    again = h.grad(x, records, dlogp, None, ids)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    y = x.double() @ h.w.double().t() / math.log(2)
+    dz = -torch.exp2(y - records[:, :1].double())
+    dz[torch.arange(n, device="cuda"), ids] += 1.0
+    want, bound = dz @ h.w.double(), (1.01 * H * dz.abs()) @ h.w.double().abs()
+    assert ((dx.double() - want).abs() <= bound + 1.01 * H * (want.abs() + bound) + 1e-4).all()
