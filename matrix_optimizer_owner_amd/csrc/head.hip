@@ -37,9 +37,7 @@
 #include "tile_loop.h"
 
 // Products are rounded before they are added, but where __builtin_fmaf says
-// otherwise: y - max has to be at most 0, and 0 for the largest y, however
-// large y is.  Fused, a scaled sum less its own rounded value is what rounding
-// took, up to 2^102, and 2 to that power is infinite.
+// otherwise (see reduce_column).
 #pragma clang fp contract(off)
 
 namespace mfsdp {
@@ -281,17 +279,21 @@ template <int MM, bool RAGGED, typename A>
 __device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_t token, int row0, int held, int64_t part,
                                               int fhalf) {
     const bool in = token < a.n;
-    // The largest, NaN where none is a number: such a part is not among the ones
-    // that may hold alternatives, one with a -inf is.
     float most = NAN, sum[2] = {0.f, 0.f}, wsum[2] = {0.f, 0.f};
+    const float sign = copysignf(1.f, a.c2);
     each_row<MM>(fhalf, [&](int mi, int e, int r) {
-        acc[mi][e] *= a.c2;
-        if (!RAGGED || r < held) most = fmaxf(most, acc[mi][e]);
+        if (!RAGGED || r < held) most = fmaxf(most, acc[mi][e] * sign);
     });
     most = fmaxf(most, __shfl_xor(most, 32, 64));
-    const float base = fmaxf(most, -FLT_MAX);
+    // y less its largest, fused: what rounding takes from the largest y is in the sums then, and entropies have a third of
+    // the error that rounded y leave (1.7e-7).  But of large y that is many powers of 2, more than an exponential holds,
+    // and is taken off again.  A part of no number but NaN has a NaN for the largest, and so is not among the ones that may
+    // hold alternatives; one with a -inf is.
+    const float exact = most * sign;
+    most = exact * a.c2;
+    const float base = fmaxf(most, -FLT_MAX), over = fabsf(most) > 0x1p10f && fabsf(most) < INFINITY ? __builtin_fmaf(exact, a.c2, -most) : 0.f;
     each_row<MM>(fhalf, [&](int mi, int e, int r) {
-        const float d = not_below(acc[mi][e] - base), p = exp2_fast(d);
+        const float d = not_below(__builtin_fmaf(acc[mi][e], a.c2, -base) - over), p = exp2_fast(d);
         if (!RAGGED || r < held) {
             sum[e & 1] += p;
             wsum[e & 1] = __builtin_fmaf(p, d, wsum[e & 1]);
@@ -305,7 +307,7 @@ __device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_
         const int t = in ? token_of(a.ids, token, a.rows).target - row0 : -1;
         if (__ballot(t >= 0 && t < MM * 32))
             each_row<MM>(fhalf, [&](int mi, int e, int r) {
-                if (r == t) a.targets[token] = acc[mi][e];
+                if (r == t) a.targets[token] = acc[mi][e] * a.c2;
             });
     }
     if (a.logits && in) {
@@ -316,8 +318,8 @@ __device__ __forceinline__ void reduce_column(const LogitArgs& a, A& acc, int64_
             for (int q = 0; q < 4; ++q) {
                 const int r = mi * 32 + q * 8 + fhalf * 4;
                 if (!RAGGED || r < held)  // up to three values past the table's end, inside the part
-                    *reinterpret_cast<float4*>(to + r) =
-                        make_float4(acc[mi][q * 4], acc[mi][q * 4 + 1], acc[mi][q * 4 + 2], acc[mi][q * 4 + 3]);
+                    *reinterpret_cast<float4*>(to + r) = make_float4(acc[mi][q * 4] * a.c2, acc[mi][q * 4 + 1] * a.c2,
+                                                                     acc[mi][q * 4 + 2] * a.c2, acc[mi][q * 4 + 3] * a.c2);
             }
     }
 }
@@ -1016,7 +1018,8 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
             }
         }
         each_row<S::MM>(fhalf, [&](int mi, int e, int) {
-            // at most 0: y is formed again, in another order than by k_head_few, and may pass the largest by its rounding
+            // y rounded: the largest less m is 0 however large it is; and at most 0, since y is formed again, in another
+            // order than by k_head_few, and may pass the largest by its rounding
             const float lp = __builtin_amdgcn_fmed3f((acc[mi][ni][e] * a.c2 - m) - ls, -1024.f, 0.f);
             const float v = -exp2_fast(lp) * __builtin_fmaf(c, lp, b);
             acc[mi][ni][e] = live ? v : 0.f;
