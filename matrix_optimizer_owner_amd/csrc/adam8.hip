@@ -227,7 +227,7 @@ struct Adam8Args {
 // behind the tensor's end.  Codes behind the end are written as zeros, inside
 // the tensor's own code bytes.  WHOLE: the chunk has no such end.
 // HBM: 10 bytes of a bf16 element and 14 of an fp32 one, 16 a group; 525 M bf16
-// elements in 861 - 985 us (5.4 - 6.2 TB/s, by machine; in 32 bits 22 bytes,
+// elements in 830 - 990 us (5.4 - 6.4 TB/s, by machine; in 32 bits 22 bytes,
 // 1919 us), and next to it the codes' arithmetic, 8 elements a thread so that
 // roots, reciprocals and hashes of neighbours overlap.
 template <int D, bool SCALED, bool WHOLE>

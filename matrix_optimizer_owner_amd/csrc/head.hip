@@ -333,8 +333,8 @@ template <int MM, int MN> struct Column {
 
 // A tile of logits, BT rows of the table by BT tokens, reduced over each
 // wave's BT/2 rows.  Bound by the MFMAs at the clock they leave: 4096 tokens
-// over 128256 x 4096 in 3.30 ms, 1.30 PFLOP/s (a library product of the shape,
-// whose 1 GB of logits is not reduced, 3.00); 1024 over 50257 x 768 in 97 us,
+// over 128256 x 4096 in 3.30 - 3.48 ms, by machine, 1.24 - 1.30 PFLOP/s (a library
+// product of the shape, whose 1 GB of logits is not reduced, 3.00); 1024 over 50257 x 768 in 97 us,
 // 12 stages, of which starting and reducing a tile takes a part; of 80 or 245
 // tiles, one a CU, 0.5 us a stage, LDS reads and MFMAs in turn.
 template <int BT>
@@ -972,8 +972,8 @@ struct DzArgs {
 // dz of a tile: formed in the accumulators, staged in LDS as [token][row of
 // the table] in bf16, a plane at a time, and written in whole 16-byte words.
 // Zeros for tokens and rows past the last, and for padding.  Bound as
-// k_head_logits: 3.49 ms for 4096 tokens over 128256 x 4096 (1.23 PFLOP/s, and
-// 1 GB of dz written), 115 us for 1024 over 50257 x 768.
+// k_head_logits: 3.54 - 3.62 ms for 4096 tokens over 128256 x 4096 (1.19 - 1.22
+// PFLOP/s, and 1 GB of dz written), 115 - 134 us for 1024 over 50257 x 768.
 template <int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
     using S = Shape<BT, 4>;
@@ -1226,8 +1226,8 @@ struct DxArgs {
 
 // dx = dz W: P is W, read K-major (its rows are the contraction).  Its result
 // is small and its contraction long, so that it is cut into parts (dx_cut).
-// Bound by the MFMAs: 3.26 ms for 4096 tokens over 128256 x 4096 (1.32
-// PFLOP/s), 85 + 8 us for 1024 over 50257 x 768 (0.93; 9 parts).
+// Bound by the MFMAs: 3.23 - 3.33 ms for 4096 tokens over 128256 x 4096 (1.29 - 1.33
+// PFLOP/s), 84 - 97 + 8 us for 1024 over 50257 x 768 (0.93; 9 parts).
 template <int D, int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dx(DxArgs a) {
     using S = Shape<BT, 4>;
@@ -1437,7 +1437,8 @@ __device__ __forceinline__ void list_block(const ListArgs& a, uint32_t block) {
 }
 
 // What dx and dW need besides dz, in one launch: the rests' part of dx, x
-// turned over, and the lists.
+// turned over, and the lists.  Latency, of a list's tokens 256 at a time: 47 us
+// for 4096 tokens over 128256 x 4096, 10 for 1024 over 50257 x 768.
 __global__ __launch_bounds__(256) void k_head_turn(TurnArgs t, ListArgs l, GatherArgs g) {
     uint32_t block = blockIdx.x;
     if (block < g.blocks) return gather_block(g, block);
@@ -1494,8 +1495,8 @@ __device__ __forceinline__ void add_rests(const DwArgs& a, const Staging<BT>& st
 
 // dW = dz^T x: P is x turned over, Q is dz, read K-major (its rows are the
 // contraction).  Bound by the MFMAs and what the walk adds, the table's size
-// read or written: 3.68 ms for 4096 tokens over 128256 x 4096 (1.17 PFLOP/s),
-// 103 us for 1024 over 50257 x 768, added to 77 MB of gradients.
+// read or written: 3.66 - 3.78 ms for 4096 tokens over 128256 x 4096 (1.14 - 1.18
+// PFLOP/s), 101 - 118 us for 1024 over 50257 x 768, added to 77 MB of gradients.
 template <int D, int BT>
 __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
     using S = Shape<BT, 4>;
@@ -1819,9 +1820,9 @@ void pack_operands(const mfsdp_entry& e, const HeadShape& s, const Batch& b, int
 }
 
 template <int WD, int XD> void launch_few(const FewArgs& f, hipStream_t stream) {
-    // Rows of a block: 64 where that leaves two blocks a CU, since x is then read half as often, and for more than 32
-    // tokens 32, since three blocks fit a CU (60 tokens over 50000 x 1000: 60 us, 66 with 64 rows; over 50000 x 1001
-    // fp32 129 and 145; 40 over 128256 x 1001 179 and 174).
+    // Rows of a block: 64 where that leaves two blocks a CU, since x is then read half as often; for more than 32 tokens
+    // 32, as measured (60 tokens over 50000 x 1000: 60 us, 66 with 64 rows; over 50000 x 1001 fp32 129 and 145; 40 over
+    // 128256 x 1001 179 and 174).  Registers leave two blocks a CU either way.
     const bool two = f.l.n <= 32 && f.l.rows >= 64 * 2 * kCusHead;
     const dim3 grid(uint32_t(ceil_div(f.l.rows, two ? 64 : 32)));
     if (f.l.n > 32)
