@@ -635,8 +635,9 @@ typedef struct mfsdp_head_grad_args {
  *   dx = dz W,  G (+)= dz^T x.
  * Logits are formed again.  Where x and the table are bf16, dz is rounded to
  * bf16, but for a row's entries of 1/32 or more of |scale| (|dlogp| 2 (1 - p_t)
- * + |dentropy| 2 entropy), its sum of |dz| or more, which count as in fp32 (with
- * records of other operands than the call's they may not); else it is fp32.  The
+ * + |dentropy| 2 entropy), its sum of |dz| or more, which keep 2^-16 of
+ * themselves or better (with records of other operands than the call's they may
+ * not); else it is fp32.  The
  * sums are fp32, rounded once to x_type and to the entry's type (after what was
  * there is added).  No rows and accumulate = 0 writes zeros.
  * Errors: as mfsdp_head_logprob, and INVALID_ARGUMENT (records or dlogp NULL

@@ -26,8 +26,9 @@
 // many alike, but not where a few entries carry a row, as its target does and
 // a likely other token.  What rounding takes from the entries of a 32nd or more
 // of a row's sum |dz_j| (kShare), of which there are at most 32, is kept in fp32
-// and added where dx and dW are written; what is left of the rounding is at
-// most 2^-8 |dz_j| each, in the 2-norm 2^-8 sqrt(1/32) of the row's sum.
+// and added where dx and dW are written (in bf16 for rows of the table that many
+// tokens share); what is left of the rounding is at most 2^-8 |dz_j| each, in
+// the 2-norm 2^-8 sqrt(1/32) of the row's sum.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -939,7 +940,7 @@ __global__ __launch_bounds__(256) void k_head_empty(RowArgs a) {
 constexpr int kListRows = 128;
 struct Rests {
     int* counts;      // [token]
-    int* groups;      // [128 rows of the table]: entries there, those of tokens that have none among them
+    int* groups;      // [128 rows of the table]: entries found there, those of tokens that have none among them
     int* rows;        // [kMaxRests][token]: of the table
     float* values;
     int64_t tokens;   // from k to k + 1
@@ -947,11 +948,10 @@ struct Rests {
         const int c = counts[token];
         return c <= kMaxRests ? c : 0;
     }
-    // (the order of arrival is settled where they are read)
-    __device__ __forceinline__ void add(int64_t token, int row, float value) const {
-        const int k = atomicAdd(&counts[token], 1);
+    // places of `some` more of a token's entries, from the one returned on (their order is settled where they are read)
+    __device__ __forceinline__ int places(int64_t token, int some) const { return atomicAdd(&counts[token], some); }
+    __device__ __forceinline__ void put(int k, int64_t token, int row, float value) const {
         if (k >= kMaxRests) return;
-        atomicAdd(&groups[row / kListRows], 1);
         rows[k * tokens + token] = row;
         values[k * tokens + token] = value;
     }
@@ -989,6 +989,8 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
     const int lane = threadIdx.x & 63, wave = uni(int(threadIdx.x) >> 6);
     const int wm = wave >> 1, wn = wave & 1, frow = lane & 31, fhalf = lane >> 5;
     const int row0 = ti * BT + wm * S::WTM, held = a.rows - row0;
+    int found = 0;  // large entries of the wave, all in one group of rows
+    static_assert(kListRows % S::WTM == 0, "a wave's rows lie in one group");
 #pragma unroll
     for (int ni = 0; ni < S::MN; ++ni) {
         const int64_t token = int64_t(tj) * BT + wn * S::WTN + ni * 32 + frow;
@@ -1011,6 +1013,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
                 const float pt = r.found ? exp2_fast(fminf((r.target - m) - ls, 0.f)) : 1.f;
                 const float h = d.dentropy ? fmaxf(nat(ls - r.wsum / r.sum), 0x1p-15f) : 0.f;
                 least = 2.f * kShare * fabsf(d.scale) * (fabsf(up) * fmaxf(1.f - pt, 0x1p-15f) + fabsf(dh) * h);
+                if (least == 0.f) least = INFINITY;  // no gradient, no entries
             }
             if (tok.target >= 0 && r.found && live) {
                 t = tok.target - row0;
@@ -1035,21 +1038,24 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
         float most = 0.f;
         each_row<S::MM>(fhalf, [&](int mi, int e, int) { most = fmaxf(most, fabsf(acc[mi][ni][e])); });
         if (!__ballot(most >= least)) continue;
-        // the large ones, a bit each; then one a lane at a time
+        // the large ones, a bit each; then one a lane at a time, while their places are on their way
         uint64_t large = 0;
         each_row<S::MM>(fhalf, [&](int mi, int e, int) {
             large |= fabsf(acc[mi][ni][e]) >= least ? uint64_t(1) << (mi * 16 + e) : 0;
         });
-        while (__ballot(large != 0)) {
+        int place = large ? d.rests.places(token, __popcll(large)) : 0;
+        while (const uint64_t some = __ballot(large != 0)) {
             const int q = large ? __ffsll(static_cast<unsigned long long>(large)) - 1 : -1;
             large &= large - 1;
             float v = 0.f;
             each_row<S::MM>(fhalf, [&](int mi, int e, int) { v = q == mi * 16 + e ? acc[mi][ni][e] : v; });
-            const float rest = v - bf16_to_f32(f32_to_bf16(v));  // 0, NaN and infinite ones are none
-            if (q >= 0 && fabsf(rest) > 0.f && fabsf(rest) < INFINITY)
-                d.rests.add(token, row0 + (q >> 4) * 32 + (q >> 2 & 3) * 8 + fhalf * 4 + (q & 3), rest);
+            const float rest = v - bf16_to_f32(f32_to_bf16(v));
+            if (q >= 0)
+                d.rests.put(place++, token, row0 + (q >> 4) * 32 + (q >> 2 & 3) * 8 + fhalf * 4 + (q & 3), fabsf(rest) < INFINITY ? rest : 0.f);
+            found += __popcll(some);
         }
     }
+    if (found > 0 && lane == 0) atomicAdd(&d.rests.groups[row0 / kListRows], found);
     for (int plane = 0; plane < d.planes; ++plane) {
         __syncthreads();  // the operands' stages, or the plane before, have been read
 #pragma unroll
@@ -1338,11 +1344,14 @@ __device__ __forceinline__ void gather_block(const GatherArgs& a, uint32_t block
     value = __int_as_float(__builtin_amdgcn_ds_permute(place * 4, __float_as_int(value)));
     for (int64_t col = lane * 8; col < a.ld; col += 512) {
         Values v = {};
-#pragma unroll 4
-        for (int k = 0; k < count; ++k) {
-            Eight<kBF16> w;
-            w.load(a.table.at(__builtin_amdgcn_readlane(row, k), int(col)), 0, 8, true);
-            v = fma8(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), k)), w.get(), v);
+        for (int k = 0; k < count; k += 4) {  // four rows on their way
+            Eight<kBF16> w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                w[u].load(a.table.at(__builtin_amdgcn_readlane(row, min(k + u, count - 1)), int(col)), 0, 8, true);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (k + u < count) v = fma8(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(value), k + u)), w[u].get(), v);
         }
         float4* to = reinterpret_cast<float4*>(a.out + token * a.ld + col);
         to[0] = v.a;
@@ -1359,27 +1368,67 @@ struct DwArgs {
     int stages;          // of the contraction over the batch
     const int2* bounds;  // NULL, or of the lists below (x then has one plane)
     const uint2* list;
+    const uint8_t* dense;
     uint8_t* grad;
     int vector;
     int add;
 };
 
-// The large entries of dz in each group of 128 rows of the table, in an order
-// that sizes and the entries alone fix: list[bounds[g].x] .. list[bounds[g].y -
-// 1], each the row in its group << 24 | the token (at most 2^22 of them), and
-// the rest.  A block a group looks through all tokens, 256 at a time, each
-// token's entries from the lowest row up; the first two of the next 256 are on
-// their way meanwhile.
+// For dW, the large entries of dz by a tile's rows of the table, 1 or 2 groups
+// of 128 (span): as lists, or, where more entries than a quarter of the tokens
+// lie in them, as a second plane of dz there, rests in bf16, which the tile then
+// multiplies in a run of its own.  An entry of a list takes its tile 1/32 us, a
+// run 1/128 us a token and up to three times that, so lists alone would cost
+// hot rows (a likely token of every row; a table of 256 rows: the gradients of
+// 4096 tokens of 768 columns 838 us, 114 so) far more than all other work, and
+// planes alone all tiles as much again.  At most 32 entries a row make at most 128 such tiles.
 struct ListArgs {
     Rests rests;
     int n, rows;
-    int2* bounds;
+    int span;            // groups of a tile of dW
+    int capacity;        // of the list
+    int2* bounds;        // [group]: first entry in the list and past the last; or -1 and the plane's number
     uint2* list;
+    uint8_t* dense;      // [plane][64 rows][token][64] bf16
+    uint32_t units, planes, chunks;  // tiles of dW along the rows, planes there is room for, pieces of a plane
 };
+constexpr int kMostPlanes = 128, kPiece = 256;  // tokens of a piece
+static_assert(kPadTokens % kPiece == 0, "whole pieces");
+__device__ __forceinline__ int unit_entries(const ListArgs& a, int unit) {
+    const int groups = (a.rows + kListRows - 1) / kListRows, g = unit * a.span;
+    return a.rests.groups[g] + (a.span > 1 && g + 1 < groups ? a.rests.groups[g + 1] : 0);
+}
+__device__ __forceinline__ bool is_dense(const ListArgs& a, int entries) { return entries > a.n / 4; }
+
+// One group's list, in an order that sizes and the entries alone fix: each the
+// row in the group << 24 | the token (at most 2^22 of them), and the rest.  The
+// block looks through all tokens, kLook times 256 at a time, each token's
+// entries from the lowest row up; the first two of the next ones are on their
+// way meanwhile.  Latency: a turn is a load, a barrier and the counts.
+constexpr int kLook = 4;
 __device__ __forceinline__ void list_block(const ListArgs& a, uint32_t block) {
-    __shared__ int counts[4];
+    __shared__ int4 turns[2][kLook];
+    int(&counts)[2][kLook][4] = reinterpret_cast<int(&)[2][kLook][4]>(turns);  // [.][.][wave]
     const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
-    const int first = int(block) * kListRows;
+    const int first = int(block) * kListRows, unit = int(block) / a.span;
+    // a sum over the block, `most` at most (twice that is a whole number of 32 bits)
+    auto block_sum = [&](int x, int most) {
+        for (int off = 1; off < 64; off <<= 1) x = min(x + __shfl_xor(x, off, 64), most);
+        if (lane == 0) counts[0][0][wave] = x;
+        __syncthreads();
+        const int4 c = turns[0][0];
+        return min(min(c.x + c.y, most) + min(c.z + c.w, most), most);
+    };
+    if (is_dense(a, unit_entries(a, unit))) {
+        int before = 0;  // such tiles before
+        for (int u = threadIdx.x; u < unit; u += 256) before += is_dense(a, unit_entries(a, u));
+        const int plane = block_sum(before, kMostPlanes);
+        if (plane < int(a.planes)) {
+            if (threadIdx.x == 0) a.bounds[block] = make_int2(-1, plane);
+            return;
+        }
+        __syncthreads();
+    }
     struct Ahead {
         int count, rows[2];
     };
@@ -1388,65 +1437,117 @@ __device__ __forceinline__ void list_block(const ListArgs& a, uint32_t block) {
         if (i < a.n) h = Ahead{a.rests.counts[i], {a.rests.rows[i], a.rests.rows[a.rests.tokens + i]}};  // held or not
         return h;
     };
-    Ahead next_ones = load(threadIdx.x);
-    int below = 0;
-    for (int g = threadIdx.x; g < int(block); g += 256) below += a.rests.groups[g];
-    for (int off = 1; off < 64; off <<= 1) below += __shfl_xor(below, off, 64);
-    if (lane == 0) counts[wave] = below;
-    __syncthreads();
-    const int start = counts[0] + counts[1] + counts[2] + counts[3];
-    int at = start;
-    for (int i0 = 0; i0 < a.n; i0 += 256) {
-        const int i = i0 + int(threadIdx.x);
-        const Ahead h = next_ones;
-        next_ones = load(i + 256);
-        const int c = h.count <= kMaxRests ? h.count : 0;
-        int last = -1;  // the row in the group that this token's entries up to it are listed
+    Ahead next_ones[kLook];
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) next_ones[u] = load(u * 256 + int(threadIdx.x));
+    int below = 0;  // entries of the groups before
+    for (int g = threadIdx.x; g < int(block); g += 256) below = min(below + a.rests.groups[g], a.capacity);
+    const int start = block_sum(below, a.capacity);
+    int at = start, turn = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kLook * 256) {
+        Ahead h[kLook];
+        int last[kLook];  // the row in the group that this token's entries up to it are listed
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+            h[u] = next_ones[u];
+            next_ones[u] = load(i0 + (kLook + u) * 256 + int(threadIdx.x));
+            last[u] = -1;
+        }
         for (bool more = true; more;) {
-            int next = kListRows, from = 0, left = 0;
-            auto look = [&](int k, int row) {
-                const int r = row - first;
-                if (r <= last || r >= kListRows) return;
-                ++left;
-                if (r < next) {
-                    next = r;
-                    from = k;
-                }
-            };
-            if (c > 0) look(0, h.rows[0]);
-            if (c > 1) look(1, h.rows[1]);
-            for (int k = 2; k < c; ++k) look(k, a.rests.rows[k * a.rests.tokens + i]);
-            const uint64_t mask = __ballot(left > 0), again = __ballot(left > 1);
-            __syncthreads();
-            if (lane == 0) counts[wave] = __popcll(mask) | (again ? 1 << 16 : 0);
-            __syncthreads();
-            int before = at, all = 0;
-            for (int w = 0; w < 4; ++w) {
-                if (w < wave) before += counts[w] & 0xffff;
-                all += counts[w];
+            int next[kLook], from[kLook], left[kLook];
+            uint64_t mask[kLook], again = 0;
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                const int c = h[u].count <= kMaxRests ? h[u].count : 0;
+                next[u] = kListRows;
+                from[u] = left[u] = 0;
+                auto look = [&](int k, int row) {
+                    const int r = row - first;
+                    if (r <= last[u] || r >= kListRows) return;
+                    ++left[u];
+                    if (r < next[u]) {
+                        next[u] = r;
+                        from[u] = k;
+                    }
+                };
+                if (c > 0) look(0, h[u].rows[0]);
+                if (c > 1) look(1, h[u].rows[1]);
+                for (int k = 2; k < c; ++k) look(k, a.rests.rows[k * a.rests.tokens + i0 + u * 256 + int(threadIdx.x)]);
+                mask[u] = __ballot(left[u] > 0);
+                again |= __ballot(left[u] > 1);
             }
-            if (left > 0)
-                a.list[before + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
-                    make_uint2(uint32_t(next) << 24 | uint32_t(i), __float_as_uint(a.rests.values[from * a.rests.tokens + i]));
-            at += all & 0xffff;
-            more = all >> 16;
-            last = next;
+            turn ^= 1;  // one barrier a turn: counts of the last are still read
+            if (lane == 0)
+#pragma unroll
+                for (int u = 0; u < kLook; ++u) counts[turn][u][wave] = __popcll(mask[u]) | (u == 0 && again ? 1 << 16 : 0);
+            __syncthreads();
+            more = false;
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                const int4 c = turns[turn][u];
+                const int before = ((wave > 0 ? c.x : 0) + (wave > 1 ? c.y : 0) + (wave > 2 ? c.z : 0)) & 0xffff;
+                const int all = c.x + c.y + c.z + c.w, to = at + before + __popcll(mask[u] & ((uint64_t(1) << lane) - 1));
+                const int64_t i = i0 + u * 256 + int(threadIdx.x);
+                if (left[u] > 0 && to < a.capacity)
+                    a.list[to] = make_uint2(uint32_t(next[u]) << 24 | uint32_t(i), __float_as_uint(a.rests.values[from[u] * a.rests.tokens + i]));
+                at += all & 0xffff;
+                more |= all >> 16 != 0;
+                last[u] = next[u];
+            }
         }
     }
-    if (threadIdx.x == 0) a.bounds[block] = make_int2(start, at);
+    if (threadIdx.x == 0) a.bounds[block] = make_int2(start, min(at, a.capacity));
 }
 
-// What dx and dW need besides dz, in one launch: the rests' part of dx, x
-// turned over, and the lists.  Latency, of a list's tokens 256 at a time: 47 us
-// for 4096 tokens over 128256 x 4096, 10 for 1024 over 50257 x 768.
+// A piece of one plane, whose tile is the one with as many before it.
+__device__ __forceinline__ void dense_block(const ListArgs& a, uint32_t block) {
+    __shared__ int counts[4], found;
+    const int lane = threadIdx.x & 63, wave = int(threadIdx.x) >> 6;
+    const uint32_t plane = block / a.chunks, chunk = block % a.chunks;
+    if (threadIdx.x == 0) found = -1;
+    int seen = 0;
+    for (uint32_t u0 = 0; u0 < a.units; u0 += 256) {
+        const uint32_t u = u0 + threadIdx.x;
+        const bool it = u < a.units && is_dense(a, unit_entries(a, int(u)));
+        const uint64_t mask = __ballot(it);
+        __syncthreads();
+        if (lane == 0) counts[wave] = __popcll(mask);
+        __syncthreads();
+        int place = seen;
+        for (int w = 0; w < wave; ++w) place += counts[w];
+        if (it && place + __popcll(mask & ((uint64_t(1) << lane) - 1)) == int(plane)) found = int(u);
+        seen += counts[0] + counts[1] + counts[2] + counts[3];
+    }
+    __syncthreads();
+    if (found < 0) return;
+    // a token a thread: zeros, then its entries in them
+    const int held = a.span * kListRows, row0 = found * held;
+    const int64_t token = int64_t(chunk) * kPiece + threadIdx.x, line = a.rests.tokens * 128;
+    uint8_t* to = a.dense + int64_t(plane) * (held / 64) * line + token * 128;
+    const int c = token < a.n ? a.rests.count(token) : 0;
+    typedef u32x4_t __attribute__((may_alias)) any_word_t;
+    for (int w = 0; w < held / 8; ++w) *reinterpret_cast<any_word_t*>(to + w / 8 * line + w % 8 * 16) = any_word_t{0u, 0u, 0u, 0u};
+    for (int k = 0; k < c; ++k) {
+        const int r = a.rests.rows[k * a.rests.tokens + token] - row0;
+        if (r < 0 || r >= held) continue;
+        typedef uint16_t __attribute__((may_alias)) any_half_t;
+        *reinterpret_cast<any_half_t*>(to + r / 64 * line + r % 64 * 2) = f32_to_bf16(a.rests.values[k * a.rests.tokens + token]);
+    }
+}
+
+// What dx and dW need besides dz, in one launch: the rests' part of dx, x turned
+// over, planes and lists.  Latency, of a list's turns: 48 us for 4096 tokens over
+// 128256 x 4096, 10 for 1024 over 50257 x 768.
 __global__ __launch_bounds__(256) void k_head_turn(TurnArgs t, ListArgs l, GatherArgs g) {
     uint32_t block = blockIdx.x;
     if (block < g.blocks) return gather_block(g, block);
     block -= g.blocks;
-    if (block < t.blocks)
-        turn_block(t, block);
+    if (block < t.blocks) return turn_block(t, block);
+    block -= t.blocks;
+    if (block < l.planes * l.chunks)
+        dense_block(l, block);
     else
-        list_block(l, block - t.blocks);
+        list_block(l, block - l.planes * l.chunks);
 }
 
 // What rounding took from the large entries of dz, times x, added to the staged
@@ -1510,15 +1611,21 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dw(DwArgs a) {
             const int g = tj * Staging<BT>::PASSES + h;
             if (g * kListRows < a.rows) bounds[h] = make_int2(uni(a.bounds[g].x), uni(a.bounds[g].y));
         }
+    Operand dz = a.dz;
+    const bool dense = bounds[0].x < 0;  // the tile's large entries are a plane
+    if (dense) {
+        dz.planes = 2;
+        dz.plane = a.dense + int64_t(bounds[0].y) * (BT / 64) * dz.block - (dz.base + int64_t(tj) * (BT / 64) * dz.block);
+    }
     f32x16_t acc[S::MM][S::MN];
-    tile_loop<false, true, BT>(acc, a.turned, a.dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
+    tile_loop<false, true, BT>(acc, a.turned, dz, int64_t(ti) * BT, int64_t(tj) * BT, 0, a.stages, lds);
     const int left = a.cols - ti * BT, under = a.rows - tj * BT;  // columns and rows from the tile's first on
     const uint32_t pitch = uint32_t(a.cols) * (D == kBF16 ? 2 : 4);  // at most 2^22
     uint8_t* to = a.grad + int64_t(tj) * BT * pitch + int64_t(ti) * BT * (D == kBF16 ? 2 : 4);
     walk_columns<BT>(
         acc, lds,
         [&](int h, const Staging<BT>& st) {
-            if (a.bounds) add_rests<BT>(a, st, bounds[h].x, bounds[h].y, ti * BT);
+            if (a.bounds && !dense) add_rests<BT>(a, st, bounds[h].x, bounds[h].y, ti * BT);
         },
         [&](int c, int r) {
             Eight<D> old = {};
@@ -1626,7 +1733,8 @@ struct HeadShape {
     int64_t n_parts;
     int tile_dw;
     DxCut dx;
-    uint64_t x, turned, table, parts, targets, logits, dz, counts, rows, values, bounds, list, sums, rests, total;
+    uint64_t x, turned, table, parts, targets, logits, dz, counts, rows, values, bounds, list, dense, sums, rests, total;
+    int planes;               // of large entries that there is room for
     uint64_t x_plane, table_plane, dz_plane;   // bytes of a plane (turned over: as x)
 };
 
@@ -1664,6 +1772,8 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
             s.values = region(uint64_t(s.np) * kMaxRests * 4);
             s.bounds = region(uint64_t(ceil_div(e.rows, kListRows)) * 8);
             s.list = region(uint64_t(s.np) * kMaxRests * 8);
+            // room for either tile edge of dW
+            s.dense = region(uint64_t(std::min<int64_t>(kMostPlanes * 256, s.vp)) * uint64_t(s.np) * 2);
             s.rests = region(uint64_t(n) * align_up(uint64_t(e.cols), 8) * 4);
         }
         s.turned = region(uint64_t(s.x_planes) * s.x_plane);
@@ -1672,6 +1782,7 @@ HeadShape head_shape(const mfsdp_entry& e, int64_t n, int x_type, int top_k, boo
         const int of_dx = s.dz_planes * s.table_planes, of_dw = s.dz_planes * s.x_planes;
         s.dx = dx_cut(e, n, of_dx == 9 ? 6 : of_dx);
         s.tile_dw = pick_tile(e.rows, e.cols, int(ceil_div(n, 64)) * (of_dw == 9 ? 6 : of_dw));
+        s.planes = s.dz_planes == 1 ? int(std::min<int64_t>(kMostPlanes, ceil_div(e.rows, s.tile_dw))) : 0;
         s.sums = region(uint64_t(dx_sum_rows(e, n)) * align_up(uint64_t(e.cols), 8) * 4);
     } else {
         s.targets = region(uint64_t(s.np) * 4);
@@ -1942,23 +2053,21 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
     TurnArgs t = {};
     ListArgs l = {};
     GatherArgs of_dx = {};
-    int64_t blocks = 0;  // of x turned over, and the lists
+    int64_t blocks = 0;  // of x turned over, lists, pieces of planes
     if (g.grad) {
         const int64_t kp = int64_t(s.stages) * 64;
         const uint32_t across = uint32_t(s.np / 64);
         t = TurnArgs{d.l.x.base, b.ws + s.turned, d.l.x.block, kp * 128, d.l.x.plane, d.l.x.plane,
                      across, uint32_t(s.stages), across * uint32_t(s.stages) * uint32_t(s.x_planes)};
-        l = ListArgs{rests, int(b.n), int(e.rows), reinterpret_cast<int2*>(b.ws + s.bounds),
-                     reinterpret_cast<uint2*>(b.ws + s.list)};
-        blocks = int64_t(t.blocks) + groups;
+        if (kept)
+            l = ListArgs{rests, int(b.n), int(e.rows), s.tile_dw / kListRows, int(s.np) * kMaxRests,
+                         reinterpret_cast<int2*>(b.ws + s.bounds), reinterpret_cast<uint2*>(b.ws + s.list), b.ws + s.dense,
+                         uint32_t(ceil_div(e.rows, s.tile_dw)), uint32_t(s.planes), uint32_t(s.np / kPiece)};
+        blocks = int64_t(t.blocks) + groups + int64_t(l.planes) * l.chunks;
     }
     if (g.dx && kept)
         of_dx = GatherArgs{rests, d.l.table, b.n, ld, reinterpret_cast<float*>(b.ws + s.rests), uint32_t(ceil_div(b.n, 4))};
-    if (blocks + of_dx.blocks > kMaxTiles) {
-        k_head_turn<<<dim3(of_dx.blocks), dim3(256), 0, b.stream>>>(TurnArgs{}, ListArgs{}, of_dx);
-        of_dx.blocks = 0;
-    }
-    blocks += of_dx.blocks;
+    blocks += of_dx.blocks;  // with one plane of x a third of 2^24 at most, 2^15, 2^21 and 2^20
     if (blocks > 0) k_head_turn<<<dim3(uint32_t(blocks)), dim3(256), 0, b.stream>>>(t, l, of_dx);
     if (g.dx) {
         DxArgs a = {};
@@ -1994,6 +2103,7 @@ hipError_t launch_grad(const mfsdp_entry& e, const HeadShape& s, const Batch& b,
         a.stages = int(ceil_div(b.n, 64));
         a.bounds = kept ? l.bounds : nullptr;
         a.list = l.list;
+        a.dense = l.dense;
         a.grad = g.grad;
         a.vector = e.cols * (e.dtype == kBF16 ? 2 : 4) % 16 == 0;  // the entry is 16-byte aligned
         a.add = g.add;

@@ -39,7 +39,7 @@ struct Operand {
     int64_t block;    // bytes from one 128-byte column block of a row to the next
     int64_t rows;     // rows that may be read
     int blocks;       // column blocks that may be read
-    int planes;       // 1 or 3
+    int planes;       // 1 or 3; Q beside a P of one plane: also 2
     int64_t plane;    // bytes from one plane to the next
     // element (row, col), inside plane 0
     __device__ __forceinline__ const uint8_t* at(int64_t row, int col) const {
@@ -58,6 +58,9 @@ struct Runs {
         } else if (q == 1) {
             list = 0x012;
             count = 3;
+        } else if (q == 2) {  // of one plane by two
+            list = 0x04;
+            count = 2;
         } else if (p == 1) {
             list = 0x048;
             count = 3;
