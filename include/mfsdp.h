@@ -539,11 +539,12 @@ typedef struct mfsdp_head_record {
 } mfsdp_head_record;
 
 /* Device workspace of mfsdp_head_logprob on up to n rows with up to top_k
- * alternatives, and with grad = 1 of mfsdp_head_grad on as many too: n * rows
- * bf16 elements more, n rounded up to 256, three times as many with fp32 among
- * the operands.  For more than 64 rows, and with grad = 1, it holds a copy of a
- * table that is fp32 or whose cols are no multiple of 64.  It never falls as n
- * grows, so one for the largest batch serves every smaller one.
+ * alternatives, and with grad = 1 of mfsdp_head_grad on as many too: about n *
+ * (rows + min(rows, 32768)) bf16 elements and 8 bytes for each of x more, n
+ * rounded up to 256; with fp32 among the operands n * rows times 6 bytes.  For
+ * more than 64 rows, and with grad = 1, it holds a copy of a table that is fp32
+ * or whose cols are no multiple of 64.  It never falls as n grows, so one for the
+ * largest batch serves every smaller one.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (as mfsdp_head_logprob). */
 mfsdp_status mfsdp_plan_head_workspace_bytes(mfsdp_plan_t plan, int64_t entry, int64_t n, int32_t x_type,
                                              int32_t top_k, int32_t grad, uint64_t* bytes);
