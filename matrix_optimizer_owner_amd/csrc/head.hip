@@ -994,7 +994,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
 #pragma unroll
     for (int ni = 0; ni < S::MN; ++ni) {
         const int64_t token = int64_t(tj) * BT + wn * S::WTN + ni * 32 + frow;
-        float m = 0.f, ls = 0.f, b = 0.f, c = 0.f, hit = 0.f, least = INFINITY;
+        float m = 0.f, ls = 0.f, b = 0.f, c = 0.f, hit = 0.f, least = NAN;  // least: of large entries, NaN where none is kept
         int t = -1;
         bool live = false;
         if (token < a.n) {
@@ -1013,7 +1013,7 @@ __global__ __launch_bounds__(256, BT == 256 ? 1 : 2) void k_head_dz(DzArgs d) {
                 const float pt = r.found ? exp2_fast(fminf((r.target - m) - ls, 0.f)) : 1.f;
                 const float h = d.dentropy ? fmaxf(nat(ls - r.wsum / r.sum), 0x1p-15f) : 0.f;
                 least = 2.f * kShare * fabsf(d.scale) * (fabsf(up) * fmaxf(1.f - pt, 0x1p-15f) + fabsf(dh) * h);
-                if (least == 0.f) least = INFINITY;  // no gradient, no entries
+                if (least == 0.f) least = NAN;  // no gradient
             }
             if (tok.target >= 0 && r.found && live) {
                 t = tok.target - row0;

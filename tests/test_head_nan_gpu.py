@@ -30,3 +30,24 @@ def test_alternatives_beside_parts_of_nan(k, finite, n, kind):
     h.view(h.params, h.offs[0], rows).copy_(h.w)
     out = h.logprob(x, None, top_k=k)
     assert (out["top_ids"] == -1).all() and torch.isnan(out["entropy"]).all()
+
+
+@pytest.mark.parametrize("table,x", [("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("n", [20, 300])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, 3e38, math.nan])
+def test_gradients_that_are_not_finite(n, table, x, bad):
+    """An infinite, huge or NaN gradient of one row's log probability spoils that row of dx alone."""
+    rows, cols = 700, 96
+    h = Head(rows, cols, table)
+    data, ids = batch(n, cols, x, rows=rows)
+    out = h.logprob(data, ids)
+    dlogp = torch.ones(n, device="cuda")
+    dlogp[3] = 0.0
+    want, _ = h.grad(data, out["records"], dlogp, None, ids)
+    dlogp[3] = bad
+    for dent in (None, torch.full((n,), 0.0, device="cuda")):
+        dx, dw = h.grad(data, out["records"], dlogp, dent, ids)
+        others = torch.arange(n, device="cuda") != 3
+        assert torch.equal(dx[others], want[others])
+        assert not torch.isfinite(dx[3]).all() or bad == 3e38
+        assert not torch.isfinite(dw).all() or bad == 3e38
