@@ -179,3 +179,47 @@ def test_likely_tokens_of_every_row(rows, cols, n, peaks):
     assert not dx[::5].any()
     again = h.grad(x, out["records"], dlogp, None, ids, add=want.before)
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+def test_captured_gradients_of_shared_rows():
+    """Planes and lists in a captured call: counts start at zero in every replay, whatever the workspace holds."""
+    rows, cols, n = 900, 128, 600
+    h = Head(rows, cols, values=(torch.randn(rows, cols, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+                                 / math.sqrt(cols)).bfloat16())
+    ws = h.space(n, B.BF16, grad=True)
+    x = torch.empty(n, cols, dtype=torch.bfloat16, device="cuda")
+    ids, dlogp = torch.empty(n, dtype=torch.int64, device="cuda"), torch.randn(n, device="cuda")
+    rec, dx = torch.empty(n, 6, device="cuda"), torch.empty_like(x)
+    grads = torch.zeros(h.nbytes, dtype=torch.uint8, device="cuda")
+
+    def fill(seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        at = torch.randint(0, rows, (n, 2), generator=gen, device="cuda")
+        at[:, 1] = 130 + seed % 3  # in every row
+        x.copy_((h.w.float()[at] * (8 + torch.rand(n, 2, 1, generator=gen, device="cuda"))).sum(1))
+        ids.copy_(torch.randint(0, rows, (n,), generator=gen, device="cuda"))
+
+    def call():
+        s = stream()
+        h.plan.head_logprob(0, h.params.data_ptr(), x.data_ptr(), n, rec.data_ptr(), ws.data_ptr(), ws.numel(),
+                            ids=ids.data_ptr(), stream=s)
+        h.plan.head_grad(0, h.params.data_ptr(), grads.data_ptr(), x.data_ptr(), n, rec.data_ptr(), dlogp.data_ptr(),
+                         ws.data_ptr(), ws.numel(), dx=dx.data_ptr(), ids=ids.data_ptr(), stream=s)
+
+    fill(1)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for seed in range(2, 6):
+        fill(seed)
+        call()
+        torch.cuda.synchronize()
+        want = dx.clone(), grads.clone()
+        dx.zero_()
+        grads.zero_()
+        ws.fill_(0xFF if seed % 2 else 0x11)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want[0]) and torch.equal(grads, want[1])
